@@ -16,6 +16,10 @@ import ctypes
 import math
 import os
 
+from . import kvcache
+from .kvcache import (KVCache8, cache_append, cache_attn, cache_attn_workspace_bytes, cache_evict,
+                      cache_read, cache_weights, rope, rope_freqs, rope_tables)
+
 MASK_NONE, MASK_CAUSAL, MASK_BLOCK_CAUSAL = 0, 1, 2
 TILE_M, TILE_N = 128, 128   # attention kernel's query rows per CTA / keys per KV tile
 
@@ -107,6 +111,7 @@ def lib():
         L.sage_w8a8_gemm.argtypes = [P, P, P, P, LL, LL, LL, P, P, P]
         L.sage_sync_status.restype = I
         L.sage_sync_status.argtypes = [P]
+        kvcache.declare(L)
         _lib = L
     return _lib
 

@@ -22,6 +22,7 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC,-fvisibility=hidden",
     "-Xptxas", "-v",
     "--expt-relaxed-constexpr",
+    "--threads", "0",  # source files in parallel
 ]
 
 

@@ -11,7 +11,9 @@
 #include <cstdint>
 #include <mutex>
 
+#include "api.cuh"
 #include "attn.cuh"
+#include "cache.cuh"
 #include "ceilings.cuh"
 #include "quant.cuh"
 #include "sage.h"
@@ -70,6 +72,7 @@ DeviceState* device_state() {
     if (e == cudaSuccess) e = attn_prepare(128);
     if (e == cudaSuccess) e = attn_prepare(64);
     if (e == cudaSuccess) e = w8a8_prepare();
+    if (e == cudaSuccess) e = cache_prepare();
     if (e != cudaSuccess) return nullptr;
     d.status = static_cast<int*>(p);
     d.ready = true;
@@ -205,6 +208,16 @@ __global__ void k_exp2(const float* x, float* y, size_t n) {
 }
 
 }  // namespace
+
+int* api_status_word() {
+  DeviceState* d = device_state();
+  return d ? d->status : nullptr;
+}
+long long api_wait_budget() { return kWaitBudget; }
+bool api_tile_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t tiles, uint32_t D) {
+  return encode_u8_3d(m, base, D, rows, tiles, D, static_cast<uint32_t>(rows),
+                      D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
 }  // namespace sage
 
 using namespace sage;

@@ -1,0 +1,512 @@
+"""Rotary positions and the paged 8-bit key/value cache: ctypes wrappers of
+``sage_rope*`` and ``sage_cache_*`` (include/sage.h documents the operators).
+
+A streaming or serving loop keeps one ``KVCache8`` and, per step:
+
+    k = rope(k, positions, inv_freq)                     # before it is cached
+    cache_append(cache, k, v, pages, lengths)            # lengths: before
+    lengths += n
+    o, lse = cache_attn(rope(q, ...), cache, pages, lengths, "causal", return_lse=True)
+    cache_weights(q, cache, lse, pages, lengths, "causal")     # optional:
+    kept, lengths = cache_evict(cache, pages, lengths, keep)   # prune
+
+Every call takes the tensors' device (not the current one) and, without
+``stream``, that device's current stream; what it allocates belongs to that
+stream.
+"""
+import ctypes
+import math
+
+PAGE = 64          # tokens per page
+MIN_V_EXP = -40
+_MASKS = "mask must be None, 'causal', ('block_causal', n) or " \
+         "('window', frame_len, window_frames, sink_tokens)"
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_i8", "k_scale", "v_f8", "v_exp", "weight")] + \
+               [(n, ctypes.c_int) for n in ("n_pages", "heads", "D")]
+
+
+class _Seqs(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("B", ctypes.c_int),
+                ("max_pages", ctypes.c_int)]
+
+
+class _Query(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_strides", ctypes.c_longlong * 3),
+                ("q_lens", ctypes.c_void_p), ("type", ctypes.c_int), ("H", ctypes.c_int),
+                ("Nq", ctypes.c_int), ("max_len", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+_Strides = ctypes.c_longlong * 3
+
+
+def declare(L):
+    """Result and argument types of the library's functions (called by lib())."""
+    P, I, SZ, LL, F = (ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong,
+                       ctypes.c_float)
+    L.sage_rope.restype = I
+    L.sage_rope.argtypes = [P, P, I, I, I, I, I, I, P, P, P, I, LL, P, F, I, I, P]
+    L.sage_rope_tables.restype = I
+    L.sage_rope_tables.argtypes = [I, I, P, I, P, F, P, P, P]
+    L.sage_cache_append.restype = I
+    L.sage_cache_append.argtypes = [P, P, P, P, I, I, P, P, P, P, P]
+    L.sage_cache_read.restype = I
+    L.sage_cache_read.argtypes = [P, P, I, P, P, P, P, P, P]
+    L.sage_cache_attn_workspace_bytes.restype = SZ
+    L.sage_cache_attn_workspace_bytes.argtypes = [I] * 10
+    L.sage_cache_attn.restype = I
+    L.sage_cache_attn.argtypes = [P, P, P, I, I, I, I, P, P, P, P, SZ, P]
+    L.sage_cache_weights.restype = I
+    L.sage_cache_weights.argtypes = [P, P, P, I, I, I, I, P, I, P]
+    L.sage_cache_evict_workspace_bytes.restype = SZ
+    L.sage_cache_evict_workspace_bytes.argtypes = [I] * 4
+    L.sage_cache_evict.restype = I
+    L.sage_cache_evict.argtypes = [P, P, I, I, I, P, I, P, P, P, SZ, P]
+
+
+def _lib():
+    from . import lib
+    return lib()
+
+
+def _check(code, what):
+    if code != 0:
+        from . import SageError
+        raise SageError(code, what)
+
+
+def _type(t):
+    import torch
+    return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(t.dtype, -1)
+
+
+class _On:
+    """The device of `t` made current, and a stream of it: `stream`, or the
+    device's current one.  Tensors allocated inside belong to that stream."""
+
+    def __init__(self, t, stream):
+        import torch
+        if not t.is_cuda:
+            raise ValueError("tensors must be CUDA tensors")
+        self.other = None
+        if t.device.index != torch.cuda.current_device():
+            self.other = torch.cuda.device(t.device)
+        self.given = None if stream is None else torch.cuda.stream(stream)
+        if stream is not None and stream.device != t.device:
+            raise ValueError("the stream belongs to %s, the tensors to %s" % (stream.device,
+                                                                              t.device))
+
+    def __enter__(self):
+        import torch
+        if self.other is not None:
+            self.other.__enter__()
+        if self.given is not None:
+            self.given.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.given is not None:
+            self.given.__exit__(*exc)
+        if self.other is not None:
+            self.other.__exit__(*exc)
+
+
+def _strides(t):
+    s = t.stride()
+    if s[3] != 1 and t.shape[3] > 1:
+        raise ValueError("the last dimension must have unit stride")
+    return _Strides(*[0 if t.shape[i] == 1 else s[i] for i in range(3)])
+
+
+def _out_strides(t):
+    if any(t.shape[i] > 1 and t.stride(i) == 0 for i in range(3)):
+        raise ValueError("out must not be an expanded tensor")
+    return _strides(t)
+
+
+def _int32(t, shape, what, dev):
+    import torch
+    if t.dtype != torch.int32 or t.device != dev or tuple(t.shape) != shape or \
+            not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 tensor %s on %s" % (what, shape, dev))
+    return t.data_ptr()
+
+
+# ---------------------------------------------------------------- rotary positions
+
+def rope_freqs(dim, theta=10000.0, scaling=None, device="cuda"):
+    """Angle per position of the dim / 2 channel pairs (fp64 tensor on
+    `device`) and the amplitude that goes with them.
+
+    scaling: None: f_p = theta^(-2 p / dim).  ("linear", s): f_p / s.
+    ("ntk", s): theta becomes theta s^(dim / (dim - 2)).  ("yarn", s, L[,
+    fast, slow]): by parts -- pairs that turn `fast` (32) times or more within
+    the original context L keep f_p, those below `slow` (1) turns get f_p / s,
+    linear in the turns between; amplitude 0.1 ln s + 1."""
+    import torch
+    if dim < 2 or dim % 2:
+        raise ValueError("dim must be even and at least 2")
+    if not theta > 0:
+        raise ValueError("theta must be positive")
+    p = torch.arange(dim // 2, dtype=torch.float64)
+    amp = 1.0
+    if scaling is None:
+        f = theta ** (-2.0 * p / dim)
+    else:
+        kind, s = scaling[0], float(scaling[1]) if len(scaling) > 1 else 0.0
+        if not s > 0 or not math.isfinite(s):
+            raise ValueError("the scaling factor must be positive")
+        if kind == "linear" and len(scaling) == 2:
+            f = theta ** (-2.0 * p / dim) / s
+        elif kind == "ntk" and len(scaling) == 2:
+            f = (theta * s ** (dim / (dim - 2)) if dim > 2 else theta) ** (-2.0 * p / dim)
+        elif kind == "yarn" and len(scaling) in (3, 5):
+            fast, slow = (32.0, 1.0) if len(scaling) == 3 else scaling[3:]
+            if not fast > slow or not scaling[2] > 0:
+                raise ValueError("yarn needs a positive context and fast > slow")
+            f = theta ** (-2.0 * p / dim)
+            keep = ((scaling[2] * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+            f = f * keep + f / s * (1 - keep)
+            amp = max(1.0, 0.1 * math.log(s) + 1.0)
+        else:
+            raise ValueError("scaling must be None, ('linear', s), ('ntk', s) or "
+                             "('yarn', s, context[, fast, slow])")
+    return f.to(device), amp
+
+
+def _positions(positions, N, B, dev):
+    import torch
+    if positions.dtype not in (torch.int32, torch.int64) or positions.device != dev or \
+            not positions.is_contiguous():
+        raise ValueError("positions must be a contiguous int32 or int64 tensor on %s" % dev)
+    if tuple(positions.shape) not in ((N,), (B, N)):
+        raise ValueError("positions must be [N] or [B, N]")
+    return positions.data_ptr(), int(positions.dtype == torch.int64), \
+        (N if positions.dim() == 2 else 0)
+
+
+def _freqs(inv_freq, dev):
+    import torch
+    if inv_freq.dtype != torch.float64 or inv_freq.device != dev or inv_freq.dim() != 1 or \
+            not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous float64 vector on %s" % dev)
+    return inv_freq.data_ptr(), 2 * inv_freq.numel()
+
+
+def rope(x, positions, inv_freq, layout="interleaved", amplitude=1.0, inverse=False, out=None,
+         stream=None):
+    """sage_rope on x [B, H, N, D] (bf16, fp16 or fp32 CUDA, unit channel
+    stride, any others).  positions: int32/int64 [N] or [B, N]; inv_freq: fp64
+    [R / 2] (rope_freqs), R <= D channels are turned.  layout: "interleaved"
+    pairs (2p, 2p + 1), "half" pairs (p, p + R/2).  inverse: turn back -- the
+    gradient of the forward call with respect to x, from that of its result.
+    out: None, a tensor like x, or x itself."""
+    import torch
+    if x.dim() != 4 or _type(x) < 0:
+        raise ValueError("x must be a bf16, fp16 or fp32 tensor [B, H, N, D]")
+    if layout not in ("interleaved", "half"):
+        raise ValueError("layout must be 'interleaved' or 'half'")
+    B, H, N, D = x.shape
+    on = _On(x, stream)
+    pos, p64, pstride = _positions(positions, N, B, x.device)
+    freq, R = _freqs(inv_freq, x.device)
+    if R > D:
+        raise ValueError("inv_freq has more pairs than the heads")
+    if out is not None and (out.shape != x.shape or out.dtype != x.dtype or
+                            out.device != x.device):
+        raise ValueError("out must have x's shape, type and device")
+    with on as st:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if x.numel() == 0:
+            return out
+        _check(_lib().sage_rope(x.data_ptr(), out.data_ptr(), _type(x), B, H, N, D, R, _strides(x),
+                                _out_strides(out), pos, p64, pstride, freq, float(amplitude),
+                                int(layout == "half"), int(bool(inverse)), st), "sage_rope")
+    return out
+
+
+def rope_tables(positions, inv_freq, amplitude=1.0, stream=None):
+    """sage_rope_tables: (cos, sin), f32 [N, R / 2], the tables quant_qk and
+    quant_qk_window take (R = D, interleaved pairs)."""
+    import torch
+    on = _On(positions, stream)
+    N = positions.shape[0]
+    pos, p64, _ = _positions(positions, N, 1, positions.device)
+    if positions.dim() != 1:
+        raise ValueError("positions must be [N]")
+    freq, R = _freqs(inv_freq, positions.device)
+    with on as st:
+        c = torch.empty((N, R // 2), dtype=torch.float32, device=positions.device)
+        s = torch.empty_like(c)
+        if c.numel():
+            _check(_lib().sage_rope_tables(N, R, pos, p64, freq, float(amplitude), c.data_ptr(),
+                                           s.data_ptr(), st), "sage_rope_tables")
+    return c, s
+
+
+# ---------------------------------------------------------------- cache
+
+class KVCache8:
+    """Pages of an 8-bit key/value cache: k_i8 int8 [P, heads, 64, D], k_scale
+    f32 [P, heads], v_f8 uint8 (e4m3 codes) like k_i8, v_exp int8 [P, heads]
+    and, with track_weight, weight f32 [P, heads, 64]."""
+
+    def __init__(self, num_pages, kv_heads, head_dim, device="cuda", track_weight=False):
+        import torch
+        shape = (int(num_pages), int(kv_heads), PAGE, int(head_dim))
+        self._bind(torch.zeros(shape, dtype=torch.int8, device=device),
+                   torch.zeros(shape[:2], dtype=torch.float32, device=device),
+                   torch.zeros(shape, dtype=torch.uint8, device=device),
+                   torch.full(shape[:2], MIN_V_EXP, dtype=torch.int8, device=device),
+                   torch.zeros(shape[:3], dtype=torch.float32, device=device)
+                   if track_weight else None)
+
+    @classmethod
+    def from_buffers(cls, k_i8, k_scale, v_f8, v_exp, weight=None):
+        """A cache over existing CUDA tensors of the layouts above."""
+        self = cls.__new__(cls)
+        self._bind(k_i8, k_scale, v_f8, v_exp, weight)
+        return self
+
+    def _bind(self, k_i8, k_scale, v_f8, v_exp, weight):
+        import torch
+        if k_i8.dim() != 4 or k_i8.shape[2] != PAGE or k_i8.shape[3] not in (64, 128):
+            raise ValueError("codes must be [pages, heads, %d, 64 or 128]" % PAGE)
+        P, h, _, D = k_i8.shape
+        for t, shape, dt, what in ((k_i8, (P, h, PAGE, D), torch.int8, "k_i8"),
+                                   (k_scale, (P, h), torch.float32, "k_scale"),
+                                   (v_f8, (P, h, PAGE, D), torch.uint8, "v_f8"),
+                                   (v_exp, (P, h), torch.int8, "v_exp"),
+                                   (weight, (P, h, PAGE), torch.float32, "weight")):
+            if t is None and what == "weight":
+                continue
+            if tuple(t.shape) != shape or t.dtype != dt or not t.is_contiguous() or \
+                    not t.is_cuda or t.device != k_i8.device:
+                raise ValueError("%s must be a contiguous %s CUDA tensor %s on one device"
+                                 % (what, dt, shape))
+        self.k_i8, self.k_scale, self.v_f8, self.v_exp, self.weight = (k_i8, k_scale, v_f8, v_exp,
+                                                                        weight)
+        self.num_pages, self.kv_heads, self.head_dim = P, h, D
+        self.device = k_i8.device
+
+    def struct(self, weight=None):
+        w = self.weight if weight is None else weight
+        return _Cache(self.k_i8.data_ptr(), self.k_scale.data_ptr(), self.v_f8.data_ptr(),
+                      self.v_exp.data_ptr(), None if w is None else w.data_ptr(), self.num_pages,
+                      self.kv_heads, self.head_dim)
+
+
+def _seqs(cache, pages, lengths):
+    import torch
+    if pages.dim() != 2:
+        raise ValueError("pages must be [B, max_pages]")
+    B, width = pages.shape
+    return _Seqs(_int32(pages, (B, width), "pages", cache.device),
+                 _int32(lengths, (B,), "lengths", cache.device), B, width)
+
+
+def cache_append(cache, k, v, pages, lengths, n_new=None, k_shift=None, stream=None):
+    """sage_cache_append: k, v [B, heads, n, D] (bf16 or fp16, unit channel
+    stride) behind the `lengths` tokens that the sequences hold; the caller
+    advances lengths.  n_new: int32 [B], tokens of each sequence (None: n).
+    k_shift: f32 [heads, D] subtracted from the keys, or None."""
+    import torch
+    on = _On(cache.k_i8, stream)
+    sq = _seqs(cache, pages, lengths)
+    if k.dim() != 4 or k.shape[0] != sq.B or k.shape[1] != cache.kv_heads or \
+            k.shape[3] != cache.head_dim or v.shape != k.shape:
+        raise ValueError("k and v must be [B, %d, n, %d]" % (cache.kv_heads, cache.head_dim))
+    if k.dtype not in (torch.bfloat16, torch.float16) or v.dtype != k.dtype or \
+            k.device != cache.device or v.device != cache.device:
+        raise ValueError("k and v must be bf16 or fp16 tensors on %s" % cache.device)
+    _shift_ok(cache, k_shift)
+    nn = None if n_new is None else _int32(n_new, (sq.B,), "n_new", cache.device)
+    if k.shape[2] == 0 or sq.B == 0:
+        return
+    with on as st:
+        _check(_lib().sage_cache_append(
+            ctypes.byref(cache.struct()), ctypes.byref(sq), k.data_ptr(), v.data_ptr(), _type(k),
+            k.shape[2], _strides(k), _strides(v), nn,
+            None if k_shift is None else k_shift.data_ptr(), st), "sage_cache_append")
+
+
+def _shift_ok(cache, k_shift):
+    import torch
+    if k_shift is not None and (tuple(k_shift.shape) != (cache.kv_heads, cache.head_dim) or
+                                k_shift.dtype != torch.float32 or not k_shift.is_contiguous() or
+                                k_shift.device != cache.device):
+        raise ValueError("k_shift must be a contiguous float32 tensor [%d, %d] on %s" % (
+            cache.kv_heads, cache.head_dim, cache.device))
+
+
+def cache_read(cache, pages, lengths, n, starts=None, k_shift=None, weights=False, stream=None):
+    """sage_cache_read: (k, v), f32 [B, heads, n, D], of n tokens of each
+    sequence from token starts[b] (int32 [B]; None: 0) on, zero where there is
+    none; with `weights` also their summed weights, f32 [B, heads, n]."""
+    import torch
+    on = _On(cache.k_i8, stream)
+    sq = _seqs(cache, pages, lengths)
+    _shift_ok(cache, k_shift)
+    sp = None if starts is None else _int32(starts, (sq.B,), "starts", cache.device)
+    if weights and cache.weight is None:
+        raise ValueError("the cache keeps no weights")
+    with on as st:
+        k = torch.empty((sq.B, cache.kv_heads, n, cache.head_dim), dtype=torch.float32,
+                        device=cache.device)
+        v = torch.empty_like(k)
+        w = torch.empty(k.shape[:3], dtype=torch.float32, device=cache.device) if weights else None
+        if k.numel():
+            _check(_lib().sage_cache_read(
+                ctypes.byref(cache.struct()), ctypes.byref(sq), n, sp,
+                None if k_shift is None else k_shift.data_ptr(), k.data_ptr(), v.data_ptr(),
+                None if w is None else w.data_ptr(), st), "sage_cache_read")
+    return (k, v, w) if weights else (k, v)
+
+
+def _mask(mask):
+    if mask is None or mask == "none":
+        return 0, 0, 0, 0
+    if mask == "causal":
+        return 1, 0, 0, 0
+    if isinstance(mask, tuple) and mask and mask[0] == "block_causal" and len(mask) == 2:
+        return 2, int(mask[1]), 0, 0
+    if isinstance(mask, tuple) and mask and mask[0] == "window" and len(mask) == 4:
+        return 3, int(mask[1]), int(mask[2]), int(mask[3])
+    raise ValueError(_MASKS)
+
+
+def _query(q, cache, sq, q_lens, max_len, scale):
+    import torch
+    if q.dim() != 4 or q.shape[0] != sq.B or q.shape[3] != cache.head_dim or \
+            q.shape[1] % cache.kv_heads:
+        raise ValueError("q must be [B, H, Nq, %d], H a multiple of %d" % (cache.head_dim,
+                                                                         cache.kv_heads))
+    if q.dtype not in (torch.bfloat16, torch.float16) or q.device != cache.device:
+        raise ValueError("q must be a bf16 or fp16 tensor on %s" % cache.device)
+    cap = sq.max_pages * PAGE
+    return _Query(q.data_ptr(), _strides(q),
+                  None if q_lens is None else _int32(q_lens, (sq.B,), "q_lens", cache.device),
+                  _type(q), q.shape[1], q.shape[2], cap if max_len is None else min(int(max_len), cap),
+                  cache.head_dim ** -0.5 if scale is None else float(scale))
+
+
+def cache_attn_workspace_bytes(cache, B, H, Nq, max_len, mask=None):
+    """sage_cache_attn_workspace_bytes on the cache's device."""
+    with _On(cache.k_i8, None):
+        n = _lib().sage_cache_attn_workspace_bytes(B, cache.kv_heads, H, Nq, cache.head_dim,
+                                                   int(max_len), *_mask(mask))
+    if n == 0:
+        raise ValueError("invalid shape or mask")
+    return int(n)
+
+
+def cache_attn(q, cache, pages, lengths, mask=None, q_lens=None, max_len=None, scale=None,
+               out=None, lse=None, return_lse=False, workspace=None, stream=None):
+    """sage_cache_attn: attention of q [B, H, Nq, D] (bf16 or fp16, unit
+    channel stride) over the cached tokens; returns out, or (out, lse).
+
+    mask: None, "causal", ("block_causal", n) or ("window", frame_len,
+    window_frames, sink_tokens).  q_lens: int32 [B], query rows of each
+    sequence (None: Nq); other rows of out are left as they are.  max_len: a
+    bound on the lengths known to the host (None: what the page table holds);
+    it only chooses how the work is cut.  scale: None is 1 / sqrt(D)."""
+    import torch
+    on = _On(cache.k_i8, stream)
+    sq = _seqs(cache, pages, lengths)
+    qs = _query(q, cache, sq, q_lens, max_len, scale)
+    m = _mask(mask)
+    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or
+                            out.device != q.device):
+        raise ValueError("out must have q's shape, type and device")
+    if lse is not None and (lse.shape != q.shape[:3] or lse.dtype != torch.float32 or
+                            lse.device != q.device or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 tensor [B, H, Nq]")
+    with on as st:
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if lse is None and return_lse:
+            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        if q.numel():
+            if workspace is None:
+                n = _lib().sage_cache_attn_workspace_bytes(
+                    sq.B, cache.kv_heads, qs.H, qs.Nq, cache.head_dim, qs.max_len, *m)
+                workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+            elif workspace.device != q.device or not workspace.is_contiguous():
+                raise ValueError("workspace must be a contiguous tensor on %s" % q.device)
+            _check(_lib().sage_cache_attn(
+                ctypes.byref(cache.struct()), ctypes.byref(sq), ctypes.byref(qs), *m,
+                out.data_ptr(), _out_strides(out), None if lse is None else lse.data_ptr(),
+                workspace.data_ptr(), workspace.numel() * workspace.element_size(), st),
+                "sage_cache_attn")
+    return (out, lse) if return_lse else out
+
+
+def cache_weights(q, cache, lse, pages, lengths, mask=None, q_lens=None, max_len=None, scale=None,
+                  weight=None, accumulate=True, stream=None):
+    """sage_cache_weights: the attention weight that each cached token got from
+    the rows of q, from cache_attn's lse of the same arguments, added to (or,
+    accumulate=False, written over) cache.weight -- or `weight`, a float32
+    tensor [pages, heads, 64].  Returns that tensor."""
+    import torch
+    on = _On(cache.k_i8, stream)
+    sq = _seqs(cache, pages, lengths)
+    qs = _query(q, cache, sq, q_lens, max_len, scale)
+    if lse.shape != q.shape[:3] or lse.dtype != torch.float32 or lse.device != q.device or \
+            not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 tensor [B, H, Nq]")
+    w = cache.weight if weight is None else weight
+    if w is None:
+        raise ValueError("the cache keeps no weights")
+    if tuple(w.shape) != tuple(cache.k_i8.shape[:3]) or w.dtype != torch.float32 or \
+            w.device != cache.device or not w.is_contiguous():
+        raise ValueError("weight must be a contiguous float32 tensor [pages, heads, %d]" % PAGE)
+    if sq.B == 0 or q.shape[1] == 0 or q.shape[2] == 0:
+        return w
+    with on as st:
+        _check(_lib().sage_cache_weights(
+            ctypes.byref(cache.struct(w)), ctypes.byref(sq), ctypes.byref(qs), *_mask(mask),
+            lse.data_ptr(), int(bool(accumulate)), st), "sage_cache_weights")
+    return w
+
+
+def cache_evict(cache, pages, lengths, keep, sink=0, recent=0, pages_out=None, workspace=None,
+                stream=None):
+    """sage_cache_evict: cut every sequence and head to at most `keep` tokens,
+    by cache.weight.  Returns (kept, lengths): int32 [B, heads, keep], the
+    survivors' old places in order, then -1; int32 [B].  pages_out: int32 [B,
+    >= ceil(keep / 64)], pages the survivors go to (none of them in `pages`);
+    None: the sequences' own first pages."""
+    import torch
+    on = _On(cache.k_i8, stream)
+    sq = _seqs(cache, pages, lengths)
+    keep, sink, recent = int(keep), int(sink), int(recent)
+    if cache.weight is None:
+        raise ValueError("the cache keeps no weights")
+    if keep < 1 or sink < 0 or recent < 0 or sink + recent > keep:
+        raise ValueError("keep must be at least 1 and at least sink + recent")
+    po, width = None, 0
+    if pages_out is not None:
+        if pages_out.dim() != 2 or pages_out.shape[1] * PAGE < keep:
+            raise ValueError("pages_out must be [B, at least %d]" % -(-keep // PAGE))
+        width = pages_out.shape[1]
+        po = _int32(pages_out, (sq.B, width), "pages_out", cache.device)
+    with on as st:
+        kept = torch.empty((sq.B, cache.kv_heads, keep), dtype=torch.int32, device=cache.device)
+        out = torch.empty((sq.B,), dtype=torch.int32, device=cache.device)
+        if sq.B == 0:
+            return kept, out
+        if po is None and workspace is None:
+            n = _lib().sage_cache_evict_workspace_bytes(sq.B, cache.kv_heads, cache.head_dim, keep)
+            workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=cache.device)
+        if workspace is not None and (workspace.device != cache.device or
+                                      not workspace.is_contiguous()):
+            raise ValueError("workspace must be a contiguous tensor on %s" % cache.device)
+        _check(_lib().sage_cache_evict(
+            ctypes.byref(cache.struct()), ctypes.byref(sq), keep, sink, recent, po, width,
+            kept.data_ptr(), out.data_ptr(), None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), st),
+            "sage_cache_evict")
+    return kept, out

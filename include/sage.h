@@ -540,6 +540,186 @@ sage_status sage_ceiling(int kind, int iters, int n, void *scratch, size_t scrat
 /* SAGE_ABI_VERSION of the loaded library. */
 int sage_abi_version(void);
 
+/* ---------------------------------------------------------------- rotary positions
+ *
+ * sage_rope turns the channel pairs of query or key heads by their tokens'
+ * positions: pair p of a token at position n by the angle n * inv_freq[p],
+ * scaled by `amplitude`:
+ *   y0 = amplitude * (x0 cos - x1 sin), y1 = amplitude * (x0 sin + x1 cos).
+ * Pairs are channels (2p, 2p + 1) (half = 0) or (p, p + R/2) (half = 1) of the
+ * first R channels; channels R .. D - 1 pass through unchanged.  inverse = 1
+ * turns by the negative angles: the transposed map, which is the gradient of
+ * the forward one.  Angles and their whole turns are taken in fp64 (positions
+ * far out keep their phase); cos and sin are fp32, the products fp32, the
+ * result rounded once.
+ *   x, y             device, type 0 bf16, 1 fp16, 2 fp32: [B, H, N, D] with
+ *                    unit channel stride and the given strides (elements) of
+ *                    B, H and N; y may be x itself (same strides)
+ *   positions        device int64 (positions_64 = 1) or int32: N of them,
+ *                    batch entry b's at b * positions_stride (0: shared)
+ *   inv_freq         device f64 [R / 2], 8-byte aligned
+ * x and y need the alignment of their type; 16-byte aligned rows are faster.
+ * Errors: SAGE_ERR_INVALID_ARG for null or misaligned pointers, bad sizes (B,
+ * H <= 65535, N <= 2^30), odd R or R > D, a negative stride, a non-finite
+ * amplitude; SAGE_ERR_UNSUPPORTED for R > 2048 or D > 65536. */
+sage_status sage_rope(const void *x, void *y, int type, int B, int H, int N, int D, int R,
+                      const long long x_strides[3], const long long y_strides[3],
+                      const void *positions, int positions_64, long long positions_stride,
+                      const double *inv_freq, float amplitude, int half, int inverse,
+                      void *stream);
+
+/* The same angles as tables, f32 [N, R / 2] each: the form sage_quant_qk_rope
+ * and sage_quant_qk_window take (their pairs are interleaved). */
+sage_status sage_rope_tables(int N, int R, const void *positions, int positions_64,
+                             const double *inv_freq, float amplitude, float *cosv, float *sinv,
+                             void *stream);
+
+/* ---------------------------------------------------------------- paged 8-bit cache
+ *
+ * A key/value cache that stays quantized between calls.  Pages hold 64 tokens
+ * of every key/value head; for each page and head there are int8 key codes
+ * with one scale and e4m3 value codes with one power of two -- the formats of
+ * sage_quant_qk, with the scales per block of tokens, so that a token enters
+ * without a pass over the tokens before it:
+ *   k_i8     int8 [n_pages, heads, 64, D]  k = code * k_scale
+ *   k_scale  f32  [n_pages, heads]
+ *   v_f8     e4m3 [n_pages, heads, 64, D]  v = code * 2^v_exp
+ *   v_exp    int8 [n_pages, heads]
+ *   weight   f32  [n_pages, heads, 64]     summed attention weight of each
+ *            token (sage_cache_weights, sage_cache_evict), or NULL
+ * All device, caller-allocated; codes 16-byte aligned.  D is 64 or 128,
+ * heads <= 65535, n_pages * heads <= 2^30 (else SAGE_ERR_UNSUPPORTED). */
+typedef struct {
+    int8_t *k_i8;
+    float *k_scale;
+    uint8_t *v_f8;
+    int8_t *v_exp;
+    float *weight;
+    int n_pages, heads, D;
+} sage_kv_cache;
+
+/* The sequences of a call: token t of sequence b is slot t % 64 of page
+ * pages[b * max_pages + t / 64], t < lengths[b].  Both arrays are device
+ * int32 and read when the kernels run, so a captured step follows them.
+ * Pages may be shared by sequences that only read them; a page that a call
+ * writes must belong to one sequence of that call.  Entries past a sequence's
+ * last page are not read.  A page id outside [0, n_pages) or a length outside
+ * [0, 64 * max_pages] is recorded in the device status word
+ * (SAGE_ERR_INVALID_ARG from sage_sync_status); its tokens count as absent
+ * and the length as clamped. */
+typedef struct {
+    const int32_t *pages;
+    const int32_t *lengths;
+    int B, max_pages;
+} sage_kv_seqs;
+
+/* Append up to n tokens to each sequence: lengths are those BEFORE the call
+ * (the caller advances them).
+ *   k, v      device bf16 (type 0) or fp16 (1): [B, heads, n, D], unit channel
+ *             stride, strides (elements) of B, heads and n
+ *   n_new     device int32 [B]: tokens of each sequence (clamped to [0, n]),
+ *             or NULL for n
+ *   k_shift   device f32 [heads, D] subtracted from every key first (fp32), or
+ *             NULL.  A per-channel constant leaves attention unchanged and
+ *             takes the keys' channel offsets out of the codes' range, as
+ *             sage_quant_qk's K mean does; it must be the same for all tokens
+ *             of a cache.
+ * Per touched page and head: k_scale = max(old, fp32(max |k| / 127)) and codes
+ * round_half_even(k / k_scale); v_exp = max(old, the smallest e >= -40 with
+ * max |v| <= 448 * 2^e) and codes e4m3_rne(v * 2^-e).  `old` is the page's
+ * scale if it holds tokens already; where that grows, the page's codes are
+ * rescaled and rounded to nearest even.  Every rounding is exact (one
+ * round-half-even of the real quotient).  Slots behind the new tokens of a
+ * fresh page become zero, and the new tokens' weights too.  Appending the same
+ * tokens at the same lengths again changes nothing.  Tokens past the page
+ * table are recorded as above and dropped.  Inputs must be finite. */
+sage_status sage_cache_append(const sage_kv_cache *cache, const sage_kv_seqs *seqs,
+                              const void *k, const void *v, int type, int n,
+                              const long long k_strides[3], const long long v_strides[3],
+                              const int32_t *n_new, const float *k_shift, void *stream);
+
+/* Values of n tokens of each sequence from token starts[b] on (NULL: 0), as
+ * the codes stand for them: k (+ k_shift, if given) and v f32 [B, heads, n, D],
+ * weight f32 [B, heads, n] or NULL.  Zero where there is no token. */
+sage_status sage_cache_read(const sage_kv_cache *cache, const sage_kv_seqs *seqs, int n,
+                            const int32_t *starts, const float *k_shift, float *k, float *v,
+                            float *weight, void *stream);
+
+/* The query side of an attention call over the cache: [B, H, Nq, D] rows of
+ * type 0 bf16 or 1 fp16 with unit channel stride; H is a multiple of the
+ * cache's heads, query head h reads key head h / (H / heads).
+ *   q_lens   device int32 [B]: rows of each sequence (the others are neither
+ *            read nor written), or NULL for Nq
+ *   scale    softmax scale, finite and >= 0 (1 / sqrt(D) is usual)
+ *   max_len  host's bound on the lengths, 0 .. 64 * max_pages: it only
+ *            chooses how the work is cut; longer sequences stay right */
+typedef struct {
+    const void *q;
+    long long q_strides[3];
+    const int32_t *q_lens;
+    int type, H, Nq, max_len;
+    float scale;
+} sage_kv_query;
+
+/* Workspace of sage_cache_attn on the current device, bytes (0: invalid). */
+size_t sage_cache_attn_workspace_bytes(int B, int heads, int H, int Nq, int D, int max_len,
+                                       int mask, int mask_block, int win, int sink);
+
+/* softmax(scale Q K^T + mask) V over the cached tokens: the last query row is
+ * the newest token (row i of q_len stands at position lengths + i - q_len).
+ *   mask      0 none; 1 causal; 2 block-causal (mask_block tokens a block);
+ *             3 sliding window of `win` frames of mask_block tokens after a
+ *             reference context of `sink` tokens -- the masks of
+ *             sage_attn_fwd and sage_attn_fwd_window.  mask_block = 1 makes 3
+ *             a window of `win` tokens with `sink` leading ones.
+ *   out       device, the query's type, [B, H, Nq, D] with its own strides
+ *   lse       f32 [B, H, Nq] contiguous, natural log, or NULL.  With a
+ *             shifted cache it is that of the shifted scores.
+ * A row that sees no key (an empty sequence; more query rows than tokens)
+ * gets 0 and lse = -inf.  Q is not quantized; probabilities enter the second
+ * product as fp16 relative to the row's largest term, sums are fp32.
+ * Errors: SAGE_ERR_INVALID_ARG / SAGE_ERR_UNSUPPORTED (more than 2^31 - 1
+ * blocks) before anything is enqueued; SAGE_ERR_CUDA if a launch fails. */
+sage_status sage_cache_attn(const sage_kv_cache *cache, const sage_kv_seqs *seqs,
+                            const sage_kv_query *query, int mask, int mask_block, int win,
+                            int sink, void *out, const long long o_strides[3], float *lse,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* The attention weight every cached token received:
+ *   weight[token] (+)= sum over the query rows of the key head's group of
+ *                      exp(scale q.k - lse[row])   (visible pairs only)
+ * with sage_cache_attn's lse of the same call.  accumulate = 1 adds to
+ * cache->weight, 0 overwrites the weights of all tokens of the sequences.  A
+ * token's sum does not depend on the order of threads; where sequences share
+ * a page their sums are added in no fixed order (accumulate = 1). */
+sage_status sage_cache_weights(const sage_kv_cache *cache, const sage_kv_seqs *seqs,
+                               const sage_kv_query *query, int mask, int mask_block, int win,
+                               int sink, const float *lse, int accumulate, void *stream);
+
+/* Workspace of sage_cache_evict in place, bytes (0: invalid arguments). */
+size_t sage_cache_evict_workspace_bytes(int B, int heads, int D, int keep);
+
+/* Cut every sequence and head to at most `keep` tokens: the first `sink`, the
+ * last `recent` and, of the others, those of largest weight (the lowest index
+ * among equal ones; NaN counts as largest); sink + recent <= keep.  The
+ * survivors keep their order and move to the front of the sequence, every
+ * head its own; their codes are requantized to the new page's scales:
+ *   k_scale = max over its tokens of fp32(scale * fp32(max |code| / 127)),
+ *   v_exp   = the smallest e >= -40 that covers its values,
+ * each code rounded to nearest even once (a page whose tokens all stay keeps
+ * its codes and scales).  Their weights move along.
+ *   pages_out   device int32 [B, out_pages], out_pages >= ceil(keep / 64):
+ *               where they go; these pages must not be among the pages read
+ *               or appear twice.  NULL: the sequence's own first pages,
+ *               through the workspace; sequences of at most `keep` tokens then
+ *               stay as they are.
+ *   kept        int32 [B, heads, keep]: the survivors' old places, then -1
+ *   lengths_out int32 [B]: min(length, keep); must not be seqs->lengths */
+sage_status sage_cache_evict(const sage_kv_cache *cache, const sage_kv_seqs *seqs, int keep,
+                             int sink, int recent, const int32_t *pages_out, int out_pages,
+                             int32_t *kept, int32_t *lengths_out, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
