@@ -62,6 +62,7 @@ sage_status mask_of(int mask, int block, int win, int sink, CacheMask* m) {
 
 // KV ranges of an attention call: pages a range, ranges, floats of workspace.
 struct Plan {
+  bool prefill;  // tcgen05 kernel, else the mma.sync one
   int row_tiles, chunk_pages, chunks;
   size_t rows, ws;
 };
@@ -72,21 +73,43 @@ int visited_pages(const CacheMask& m, int max_len, int tile_tokens) {
   const long long win = static_cast<long long>(m.win) * m.block + m.block + tile_tokens;
   return static_cast<int>(std::min(pages, (m.sink + kPage - 1ll) / kPage + win / kPage + 3));
 }
+// Rows from which a query tile goes to the tcgen05 kernel.
+constexpr long long kPrefillRows = 33;
+
 Plan plan_of(const CacheMask& m, int B, int Hkv, int G, int Nq, int D, int max_len, int sms) {
   Plan p{};
-  p.row_tiles = (static_cast<int>(std::min(static_cast<long long>(Nq) * G, 1ll << 30)) + kDecRows - 1) / kDecRows;
+  const long long qrows = static_cast<long long>(Nq) * G;
+  p.prefill = qrows >= kPrefillRows;
+  const int tile = p.prefill ? kPreRows : kDecRows;
+  p.row_tiles = static_cast<int>((qrows + tile - 1) / tile);
   const long long units = static_cast<long long>(B) * Hkv * p.row_tiles;
-  const int pages = visited_pages(m, max_len, (kDecRows + G - 1) / G + 1);
-  // Ranges so short that the blocks come in about four rounds over the SMs
-  // (uneven sequences then even out), but of four pages at least: one for
-  // each warp of the block.
-  const long long want = std::max(1ll, 4ll * sms / std::max(1ll, units));
-  long long cp = (pages + want - 1) / want;
-  cp = std::max(4ll, (cp + 3) / 4 * 4);
+  const int pages = visited_pages(m, max_len, (tile + G - 1) / G + 1);
+  long long cp = std::max(4, pages);
+  if (p.prefill) {
+    // one block an SM: the fewest ranges whose last round of blocks leaves at
+    // most a tenth of the SMs' time unused, of 16 pages at least
+    double best = 0.0;
+    for (long long n = 1; n <= 64 && (n == 1 || pages / n >= 16); n++) {
+      const double rounds = static_cast<double>(units * n) / sms;
+      const double used = rounds / std::ceil(rounds);
+      if (used > best + 1e-9) {
+        best = used;
+        cp = ((pages + n - 1) / n + 1) / 2 * 2;
+      }
+      if (used >= 0.9) break;
+    }
+    cp = std::max(4ll, cp);
+  } else {
+    // Ranges so short that the blocks come in about four rounds over the SMs
+    // (uneven sequences then even out), but of four pages at least: one for
+    // each warp of the block.
+    const long long want = std::max(1ll, 4ll * sms / std::max(1ll, units));
+    cp = std::max(4ll, ((pages + want - 1) / want + 3) / 4 * 4);
+  }
   while ((pages + cp - 1) / cp > kCacheChunksMax) cp *= 2;
   p.chunk_pages = static_cast<int>(cp);
   p.chunks = static_cast<int>(std::max(1ll, (pages + cp - 1) / cp));
-  p.rows = static_cast<size_t>(B) * Hkv * p.row_tiles * kDecRows;
+  p.rows = static_cast<size_t>(B) * Hkv * p.row_tiles * tile;
   p.ws = p.chunks > 1 ? p.rows * p.chunks * (static_cast<size_t>(D) + 2) * 4 : 0;
   return p;
 }
@@ -286,7 +309,8 @@ SAGE_EXPORT sage_status sage_cache_attn(const sage_kv_cache* cache, const sage_k
   a.chunks = p.chunks;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = a.part_o + p.rows * p.chunks * cache->D;
-  return status_of(launch_cache_decode(maps, a, static_cast<cudaStream_t>(stream)));
+  return status_of(p.prefill ? launch_cache_prefill(a, static_cast<cudaStream_t>(stream))
+                             : launch_cache_decode(maps, a, static_cast<cudaStream_t>(stream)));
 }
 
 SAGE_EXPORT sage_status sage_cache_weights(const sage_kv_cache* cache, const sage_kv_seqs* seqs,

@@ -213,7 +213,10 @@ struct CacheAttnArgs {
 };
 cudaError_t cache_prepare();
 // rows of a query tile of the two attention kernels
-constexpr int kDecRows = 16;
+constexpr int kDecRows = 16, kPreRows = 256;
+cudaError_t cache_prefill_prepare();
+cudaError_t launch_cache_prefill(const CacheAttnArgs& a, cudaStream_t s);
+cudaError_t launch_cache_merge(const CacheAttnArgs& a, int row_tiles, int tile_rows, cudaStream_t s);
 cudaError_t launch_cache_decode(const CacheAttnMaps& m, const CacheAttnArgs& a, cudaStream_t s);
 cudaError_t launch_cache_weights(const CacheAttnMaps& m, const CacheAttnArgs& a, cudaStream_t s);
 

@@ -27,6 +27,7 @@
 #include <cuda_fp16.h>
 
 #include "cache.cuh"
+#include "cache_dev.cuh"
 #include "sm100.cuh"
 
 namespace sage {
@@ -36,7 +37,6 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kWarps = 4;
 constexpr int kStages = 2;
 constexpr float kBoost = 12.0f;
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 
 enum : int { kSiteDecPage = 0x20101, kSiteDecDrain, kSiteWgtPage, kSiteWgtDrain };
@@ -67,18 +67,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Four int8 codes to two fp16 pairs: code + 128 becomes the low mantissa bits
-// of 1024, and 1152 is taken off (exact).
-__device__ __forceinline__ void i8x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t u = w ^ 0x80808080u;
-  const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-  const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
-  const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
-  lo = *reinterpret_cast<const uint32_t*>(&x);
-  hi = *reinterpret_cast<const uint32_t*>(&y);
-}
-
 // Four e4m3 codes to two fp16 pairs, (bytes 0, 2) and (bytes 1, 3).
 __device__ __forceinline__ void f8x4_to_f16(uint32_t w, uint32_t& even, uint32_t& odd) {
   const uint32_t p = __byte_perm(w, 0, 0x3120);
@@ -95,50 +83,6 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, const
       return;
     }
   }
-}
-
-// ---------------------------------------------------------------- query rows
-
-// The power e with amax 2^-e in [2^14, 2^15) (0 for amax = 0; clamped where
-// 2^-e would not be a normal fp32 number).
-__device__ __forceinline__ int row_power(float amax) {
-  const uint32_t u = __float_as_uint(amax);
-  if (u == 0u) return 0;
-  return max(-126, min(static_cast<int>(u >> 23) - 127 - 14, 126));
-}
-
-__device__ __forceinline__ float load_q(const void* q, int type, size_t i) {
-  return type == kTypeBf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(q)[i])
-                           : __half2float(static_cast<const __half*>(q)[i]);
-}
-
-// One query row into shared memory as fp16 (channels in order), by a warp;
-// returns the row's factor 2^e.  A row that is not there becomes zero.
-template <int D>
-__device__ __forceinline__ float stage_row(const CacheAttnArgs& a, int b, int h, int r, int rows,
-                                           __half* dst, int lane) {
-  constexpr int PER = D / 32;
-  float f[PER];
-  float m = 0.0f;
-  if (r < rows) {
-    const size_t base = a.qb * b + a.qh * (static_cast<size_t>(h) * a.G + r % a.G) +
-                        a.qn * (r / a.G) + lane * PER;
-#pragma unroll
-    for (int e = 0; e < PER; e++) {
-      f[e] = load_q(a.q, a.type, base + e);
-      m = fmaxf(m, fabsf(f[e]));
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < PER; e++) f[e] = 0.0f;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-  const int p = row_power(m);
-  const float inv = pow2i(-p);
-#pragma unroll
-  for (int e = 0; e < PER; e++) dst[lane * PER + e] = __float2half_rn(f[e] * inv);
-  return pow2i(p);
 }
 
 // ---------------------------------------------------------------- decode
@@ -169,16 +113,6 @@ __device__ __forceinline__ TileId tile_id(const CacheAttnArgs& a, int row_tiles)
   return t;
 }
 
-__device__ __forceinline__ int query_len(const CacheAttnArgs& a, int b) {
-  if (!a.q_lens) return a.Nq;
-  const int n = __ldg(a.q_lens + b);
-  if (n < 0 || n > a.Nq) {
-    if (atomicCAS(a.c.status, 0, 1) == 0) atomicExch(a.c.status + 1, 0x20004);
-    return n < 0 ? 0 : a.Nq;
-  }
-  return n;
-}
-
 // Two neighbouring channels of one output row.
 __device__ __forceinline__ void store_o2(const CacheAttnArgs& a, size_t i, float x, float y) {
   if (a.type == kTypeBf16) {
@@ -196,6 +130,7 @@ template <int D>
 __global__ void __launch_bounds__(kWarps * 32)
     k_cache_decode(const __grid_constant__ CacheAttnMaps maps, const CacheAttnArgs a, int row_tiles) {
   extern __shared__ __align__(1024) uint8_t raw[];
+  if (smem_misaligned(raw, a.c.status)) return;
   DecSmem<D>& s = *reinterpret_cast<DecSmem<D>*>(raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -451,7 +386,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     if (nch > 1) {
       const size_t pr = urow * a.chunks + id.chunk;
       *reinterpret_cast<float2*>(a.part_o + pr * D + d) = make_float2(ox, oy);
-      if (d == 0) *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(mx, ls);
+      if (d == 0) *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(mx - kBoost, ls);
     } else {
       const float inv = ls > 0.0f ? 1.0f / ls : 0.0f;
       const int rr = r0 + r, tok = rr / a.G, head = id.h * a.G + rr % a.G;
@@ -505,7 +440,7 @@ __global__ void __launch_bounds__(128) k_cache_merge(const CacheAttnArgs a, int 
   for (int e = 0; e < PER; e += 2) store_o2(a, ob + e, o[e] * inv, o[e + 1] * inv);
   if (lane == 0 && a.lse)
     a.lse[(static_cast<size_t>(b) * a.H + head) * a.Nq + tok] =
-        ls > 0.0f ? (mx - kBoost + log2f(ls)) * kLn2 : -INFINITY;
+        ls > 0.0f ? (mx + log2f(ls)) * kLn2 : -INFINITY;
 }
 
 // ---------------------------------------------------------------- weights
@@ -533,6 +468,7 @@ template <int D>
 __global__ void __launch_bounds__(kWgtWarps * 32)
     k_cache_weights(const __grid_constant__ CacheAttnMaps maps, const CacheAttnArgs a, int page_groups) {
   extern __shared__ __align__(1024) uint8_t raw[];
+  if (smem_misaligned(raw, a.c.status)) return;
   WgtSmem<D>& s = *reinterpret_cast<WgtSmem<D>*>(raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -678,7 +614,7 @@ cudaError_t cache_prepare() {
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(k_cache_weights<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(sizeof(WgtSmem<64>)));
-  return e;
+  return e == cudaSuccess ? cache_prefill_prepare() : e;
 }
 
 cudaError_t launch_cache_decode(const CacheAttnMaps& m, const CacheAttnArgs& a, cudaStream_t s) {
@@ -691,9 +627,14 @@ cudaError_t launch_cache_decode(const CacheAttnMaps& m, const CacheAttnArgs& a, 
     k_cache_decode<64><<<grid, kWarps * 32, sizeof(DecSmem<64>), s>>>(m, a, row_tiles);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.chunks == 1) return e;
-  const unsigned mg = static_cast<unsigned>((units * kDecRows + 3) / 4);
-  if (a.c.D == 128) k_cache_merge<128><<<mg, 128, 0, s>>>(a, row_tiles, kDecRows);
-  else k_cache_merge<64><<<mg, 128, 0, s>>>(a, row_tiles, kDecRows);
+  return launch_cache_merge(a, row_tiles, kDecRows, s);
+}
+
+cudaError_t launch_cache_merge(const CacheAttnArgs& a, int row_tiles, int tile_rows, cudaStream_t s) {
+  const long long rows = static_cast<long long>(a.c.B) * a.c.Hkv * row_tiles * tile_rows;
+  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
+  if (a.c.D == 128) k_cache_merge<128><<<grid, 128, 0, s>>>(a, row_tiles, tile_rows);
+  else k_cache_merge<64><<<grid, 128, 0, s>>>(a, row_tiles, tile_rows);
   return cudaGetLastError();
 }
 

@@ -1,0 +1,546 @@
+// cache_prefill.cu -- attention over the paged 8-bit cache for many query
+// rows (prompts, latent frames): the arithmetic of cache_attn.cu on tcgen05.
+//
+// A block owns 256 query rows of one (sequence, key head), two tiles of 128,
+// and walks KV tiles of 128 keys (two pages).  16 warps:
+//   0-3, 4-7   softmax of tile 0 and 1, a thread a row: S from TMEM, running
+//              maximum, y = 2^(t + e - M + 7), fp16(y) back into the TMEM
+//              columns of S, where the second product reads it as operand A.
+//              O is rescaled only when a row's maximum grew by more than 2^8
+//              since its last rescale (y <= 2^15 then still fits fp16).
+//   8-11       codes from global memory to fp16 operands in shared memory, in
+//              the 128-byte swizzle the tensor core reads; K exactly, V
+//              exactly, the next tile's codes already in flight in registers.
+//   12         issues every tcgen05.mma: for each tile in turn O += P V of
+//              one KV tile and S = Q K^T of the next, so one tile's products
+//              run under the other's softmax.
+// What bounds it: 4 D flops a (row, key) on the fp16 tensor pipe and one exp2
+// on the MUFU take the same 2048 clocks a KV tile at D = 128.  fp16 operands
+// rather than the codes' own 8-bit kinds: Q is not quantized, and an int8 or
+// e4m3 product would need it (and P) in two limbs or more, the same tensor
+// time without the exactness.  256 rows a block halve the conversions per
+// row, which then fit the issue slots that the softmax leaves.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cfloat>
+
+#include "cache.cuh"
+#include "cache_dev.cuh"
+#include "sm100.cuh"
+
+namespace sage {
+namespace {
+
+constexpr int BM = 128, BN = 128;
+constexpr int kThreads = 512;
+constexpr int NS = 2;
+constexpr float kBoost = 7.0f;   // y = 2^7 at the reference maximum
+constexpr float kLazy = 8.0f;    // growth of the maximum that forces a rescale
+constexpr int kRegsSoftmax = 184, kRegsConvert = 104, kRegsIssue = 40;
+static_assert(kRegsSoftmax * 256 + kRegsConvert * 128 + kRegsIssue * 128 <= 65536,
+              "register split within the launch's share");
+
+enum : int { kSitePreKEmpty = 0x20201, kSitePreVEmpty, kSitePreK, kSitePreV, kSitePreP, kSitePreS,
+             kSitePreDrain };
+
+template <int D>
+struct alignas(1024) PreSmem {
+  uint8_t q[2][BM * D * 2];   // fp16 [D / 64][128 rows][128 bytes], 128-byte swizzle
+  uint8_t k[NS][BN * D * 2];  // the same over keys (K-major B operand)
+  uint8_t v[NS][BN * D * 2];  // the same (MN-major B operand)
+  float rowf[2 * BM];
+  uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
+  uint64_t s_full[2], p_full[2], drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+// Byte offset of 16-byte chunk `ch` (8 fp16 channels) of row r.
+__device__ __forceinline__ uint32_t op_off(int r, int ch) {
+  return static_cast<uint32_t>((ch >> 3) * (128 * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+}
+
+// MN-major operand of 16-bit elements, 128-byte swizzle: N in runs of 64
+// (128 bytes), `lbo` bytes from run to run; groups of 8 K rows 1024 bytes
+// apart.
+__device__ __forceinline__ uint64_t desc_mn16(uint32_t saddr, uint32_t lbo) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(lbo >> 4) << 16) |
+         (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+constexpr uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+// D[tmem] (+)= A[tmem] B[smem], f16 operands, fp32 accumulator.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void set_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// The KV tile's pages: run entries 2 i and 2 i + 1 of the block's pages.
+struct Group {
+  int j0;    // first key, or -1: no such page (all its keys masked)
+  int unit;  // (page, head) index
+};
+__device__ __forceinline__ Group group_of(const CacheAttnArgs& a, const PageRuns& runs, int b, int h,
+                                          int i, int end) {
+  Group g{-1, 0};
+  if (i < end) {
+    const int blk = runs.page(i);
+    const int pg = __ldg(a.c.pages + static_cast<size_t>(b) * a.c.max_pages + blk);
+    if (static_cast<unsigned>(pg) < static_cast<unsigned>(a.c.n_pages)) {
+      g.j0 = blk * kPage;
+      g.unit = pg * a.c.Hkv + h;
+    }
+  }
+  return g;
+}
+
+// ---------------------------------------------------------------- converters
+
+template <int D>
+__device__ __forceinline__ void load_codes(uint4 (&r)[D / 16], const uint8_t* codes, const Group (&g)[2],
+                                           int tid) {
+#pragma unroll
+  for (int i = 0; i < D / 16; i++) {
+    const int row = tid / (D / 16) + i * (2048 / D), c = tid % (D / 16);
+    const Group& x = g[i / (D / 32)];
+    r[i] = x.j0 < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                    : __ldg(reinterpret_cast<const uint4*>(
+                          codes + (static_cast<size_t>(x.unit) * kPage + (row & 63)) * D + c * 16));
+  }
+}
+// 16 codes to 16 fp16 values, two chunks of a row.  Lanes of the upper half
+// of a 128-channel row store their chunks in the other order, so that eight
+// lanes always hit eight different banks.
+template <int D, bool VALUES>
+__device__ __forceinline__ void store_codes(uint8_t* tile, const uint4 (&r)[D / 16], const Group (&g)[2],
+                                            int len, int tid) {
+#pragma unroll
+  for (int i = 0; i < D / 16; i++) {
+    const int row = tid / (D / 16) + i * (2048 / D), c = tid % (D / 16);
+    const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+    uint32_t o[8];
+    if constexpr (VALUES) {
+#pragma unroll
+      for (int j = 0; j < 4; j++)
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(o[2 * j]), "=r"(o[2 * j + 1]) : "r"(w[j]));
+      // values behind the sequence's end may be any bytes, NaN among them
+      if (g[i / (D / 32)].j0 + (row & 63) >= len) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) o[j] = 0u;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; j++) i8x4_to_f16(w[j], o[2 * j], o[2 * j + 1]);
+    }
+    const int sw = D == 128 ? c >> 2 : 0;
+    const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+    *reinterpret_cast<uint4*>(tile + op_off(row, 2 * c + sw)) = sw ? hi : lo;
+    *reinterpret_cast<uint4*>(tile + op_off(row, 2 * c + (sw ^ 1))) = sw ? lo : hi;
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void convert(PreSmem<D>& s, const CacheAttnArgs& a, const PageRuns& runs, int b,
+                                        int h, int p0, int p1, int nk, int len, const WaitCtx& w) {
+  const int tid = threadIdx.x & 127;
+  const uint8_t* kc = reinterpret_cast<const uint8_t*>(a.c.k_i8);
+  uint4 kr[D / 16], vr[D / 16];
+  Group g[2] = {group_of(a, runs, b, h, p0, p1), group_of(a, runs, b, h, p0 + 1, p1)};
+  load_codes<D>(kr, kc, g, tid);
+  load_codes<D>(vr, a.c.v_f8, g, tid);
+  for (int it = 0; it < nk; it++) {
+    const int st = it % NS;
+    const uint32_t ph = ((it / NS) & 1) ^ 1;
+    const Group n[2] = {group_of(a, runs, b, h, p0 + 2 * it + 2, p1),
+                        group_of(a, runs, b, h, p0 + 2 * it + 3, p1)};
+    if (it >= NS && !__all_sync(0xffffffffu, mbar_wait(&s.k_empty[st], ph, w, kSitePreKEmpty))) return;
+    store_codes<D, false>(s.k[st], kr, g, len, tid);
+    fence_proxy_async_smem();
+    mbar_arrive(&s.k_full[st]);
+    load_codes<D>(kr, kc, n, tid);
+    if (it >= NS && !__all_sync(0xffffffffu, mbar_wait(&s.v_empty[st], ph, w, kSitePreVEmpty))) return;
+    store_codes<D, true>(s.v[st], vr, g, len, tid);
+    fence_proxy_async_smem();
+    mbar_arrive(&s.v_full[st]);
+    load_codes<D>(vr, a.c.v_f8, n, tid);
+    g[0] = n[0];
+    g[1] = n[1];
+  }
+}
+
+// ---------------------------------------------------------------- tensor core
+
+template <int D>
+__device__ __forceinline__ void issue_qk(PreSmem<D>& s, int w, uint32_t tS, int st) {
+  constexpr uint32_t id = idesc_f16(BM, BN);
+  const uint32_t qa = smem_u32(s.q[w]), ka = smem_u32(s.k[st]);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; kk++) {
+    const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
+    mma_f16_ss(tS, smem_desc_kmajor(qa + off, 128), smem_desc_kmajor(ka + off, 128), id, kk > 0);
+  }
+}
+template <int D>
+__device__ __forceinline__ void issue_pv(PreSmem<D>& s, uint32_t tP, uint32_t tO, int st, bool first) {
+  constexpr uint32_t id = idesc_f16(BM, D) | kIdescBMajorMN;
+  const uint32_t va = smem_u32(s.v[st]);
+#pragma unroll
+  for (int kk = 0; kk < BN / 16; kk++)
+    mma_f16_ts(tO, tP + kk * 8, desc_mn16(va + kk * 2048, 128 * 128), id, !first || kk > 0);
+}
+
+template <int D>
+__device__ __forceinline__ void issue(PreSmem<D>& s, uint32_t tmem, int nk, int tiles, const WaitCtx& w) {
+  bool ok = mbar_wait(&s.k_full[0], 0, w, kSitePreK);
+  if (ok) {
+    tc_fence_after();
+    for (int t = 0; t < tiles; t++) {
+      issue_qk<D>(s, t, tmem + t * BN, 0);
+      mma_commit(&s.s_full[t]);
+    }
+    mma_commit(&s.k_empty[0]);
+  }
+  for (int it = 0; ok && it < nk; it++) {
+    const int st = it % NS, sn = (it + 1) % NS;
+    const bool more = it + 1 < nk;
+    ok = mbar_wait(&s.v_full[st], (it / NS) & 1, w, kSitePreV);
+    for (int t = 0; ok && t < tiles; t++) {
+      ok = mbar_wait(&s.p_full[t], it & 1, w, kSitePreP);
+      if (!ok) break;
+      tc_fence_after();
+      issue_pv<D>(s, tmem + t * BN, tmem + 2 * BN + t * D, st, it == 0);
+      if (t == tiles - 1) mma_commit(&s.v_empty[st]);
+      if (more) {
+        if (t == 0) {
+          ok = mbar_wait(&s.k_full[sn], ((it + 1) / NS) & 1, w, kSitePreK);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        issue_qk<D>(s, t, tmem + t * BN, sn);
+        if (t == tiles - 1) mma_commit(&s.k_empty[sn]);
+      }
+      mma_commit(&s.s_full[t]);  // the next S, or the finished O
+    }
+  }
+  // everything issued completes before TMEM is freed
+  mma_commit(&s.drain);
+  const long long t0 = clock64();
+  while (!mbar_try_wait(&s.drain, 0)) {
+    if (clock64() - t0 > w.budget) {
+      record_timeout(w.status, kSitePreDrain);
+      break;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- softmax
+
+template <int D>
+__device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, uint32_t tmem, int b, int h,
+                                        int t, int r0, int r1, const PageRuns& runs, int p0, int p1, int nk,
+                                        int len, long long off, int chunk, int nch, int row_tiles,
+                                        const WaitCtx& w) {
+  constexpr uint32_t kFull = 0xffffffffu, kNegInf = 0xFF800000u;
+  const int quad = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const int r = t * BM + quad * 32 + lane, row = r0 + r;
+  const bool valid = row < r1;
+  const uint32_t lo = static_cast<uint32_t>(quad * 32) << 16;
+  const uint32_t tS = tmem + t * BN + lo, tO = tmem + 2 * BN + t * D + lo;
+  const float f = s.rowf[r];
+  KeyRange kr{0, 0, 0};
+  if (valid) kr = key_range(a.mask, off + row / a.G, len);
+  float m = -INFINITY, l = 0.0f;
+  Group g[2];
+  float ks[2];
+  int ve[2];
+  auto meta = [&](int it, Group (&x)[2], float (&k)[2], int (&e)[2]) {
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      x[i] = group_of(a, runs, b, h, p0 + 2 * it + i, p1);
+      k[i] = x[i].j0 < 0 ? 0.0f : __ldg(a.c.k_scale + x[i].unit);
+      e[i] = x[i].j0 < 0 ? 0 : __ldg(a.c.v_exp + x[i].unit);
+    }
+  };
+  meta(0, g, ks, ve);
+  bool ok = true;
+  for (int it = 0; it < nk; it++) {
+    Group gn[2];
+    float kn[2];
+    int en[2];
+    meta(it + 1, gn, kn, en);  // the next tile's, under this one's work
+    ok = __all_sync(kFull, mbar_wait(&s.s_full[t], it & 1, w, kSitePreS));
+    if (!ok) break;
+    tc_fence_after();
+    uint32_t sv[128];
+    tmem_ld128(tS, sv);
+    // a zero scale must not meet -inf as 0 * inf
+    const float c[2] = {fmaxf(f * ks[0], FLT_MIN), fmaxf(f * ks[1], FLT_MIN)};
+    float tm[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int j0 = g[i].j0;
+      const bool all = j0 >= 0 && (kr.sink >= j0 + kPage || (kr.lo <= j0 && kr.hi >= j0 + kPage));
+      if (!__all_sync(kFull, all)) {
+        const int na = j0 < 0 ? 0 : min(max(kr.sink - j0, 0), kPage);
+        const int nb = min(max(kr.lo - j0, 0), kPage);
+        const int nc = j0 < 0 ? nb : min(max(kr.hi - j0, nb), kPage);
+        const uint32_t nbc = static_cast<uint32_t>(nc - nb);
+#pragma unroll
+        for (int j = 0; j < kPage; j++)
+          sv[i * 64 + j] = (j < na || static_cast<uint32_t>(j - nb) < nbc) ? sv[i * 64 + j] : kNegInf;
+      }
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        const int j = i * 64 + e * 8;
+        x[e] = fmax3(__uint_as_float(sv[j]), __uint_as_float(sv[j + 1]), __uint_as_float(sv[j + 2]));
+        x[e] = fmax3(x[e], __uint_as_float(sv[j + 3]), __uint_as_float(sv[j + 4]));
+        x[e] = fmax3(x[e], __uint_as_float(sv[j + 5]), __uint_as_float(sv[j + 6]));
+        x[e] = fmaxf(x[e], __uint_as_float(sv[j + 7]));
+      }
+      tm[i] = fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
+      tm[i] = fmaf(tm[i], c[i], static_cast<float>(ve[i]));
+    }
+    const float mx = fmaxf(tm[0], tm[1]);
+    if (__any_sync(kFull, mx > m + kLazy)) {
+      const float mn = fmaxf(m, mx);
+      const float al = mn == m ? 1.0f : ex2_approx(m - mn);  // 0 from -inf
+      // O holds the sum of the tiles before: its last product completed
+      // before s_full did
+      if (it > 0) {
+#pragma unroll 1
+        for (int d = 0; d < D; d += 32) {
+          uint32_t o[32];
+          tmem_ld32(tO + d, o);
+#pragma unroll
+          for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+          tmem_st32(tO + d, o);
+        }
+      }
+      l *= al;
+      m = mn;
+    }
+    const float base = m == -INFINITY ? 0.0f : kBoost - m;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const float nm = base + static_cast<float>(ve[i]);
+      const float2 cc = make_float2(c[i], c[i]), nn = make_float2(nm, nm);
+      float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+      for (int j = 0; j < 32; j++) {
+        const int at = i * 64 + j * 2;
+        float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1])), cc, nn);
+        x.x = ex2_approx(x.x);
+        x.y = ex2_approx(x.y);
+        acc[j & 1] = __fadd2_rn(acc[j & 1], x);
+        const __half2 y = __floats2half2_rn(x.x, x.y);
+        sv[i * 32 + j] = *reinterpret_cast<const uint32_t*>(&y);
+      }
+      const float2 sum = __fadd2_rn(acc[0], acc[1]);
+      l = fmaf(sum.x + sum.y, pow2i(min(-ve[i], 127)), l);
+    }
+    uint32_t pk[64];
+#pragma unroll
+    for (int j = 0; j < 64; j++) pk[j] = sv[j];
+    tmem_st64_nowait(tS, pk);
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.p_full[t]);
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      g[i] = gn[i];
+      ks[i] = kn[i];
+      ve[i] = en[i];
+    }
+  }
+  if (!ok) return;
+  if (nk > 0) {
+    if (!__all_sync(kFull, mbar_wait(&s.s_full[t], nk & 1, w, kSitePreS))) return;
+    tc_fence_after();
+  }
+  if (__all_sync(kFull, !valid)) return;
+  const bool part = nch > 1;
+  const size_t urow = (static_cast<size_t>(b) * a.c.Hkv + h) * (static_cast<size_t>(row_tiles) * (2 * BM)) + row;
+  const size_t pr = urow * a.chunks + chunk;
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const int tok = row / a.G, head = h * a.G + row % a.G;
+  const size_t ob = a.ob * b + a.oh * static_cast<size_t>(head) + a.on * static_cast<size_t>(tok);
+  const bool vec = ((reinterpret_cast<uintptr_t>(a.o) | (a.ob * 2) | (a.oh * 2) | (a.on * 2)) & 15) == 0;
+#pragma unroll 1
+  for (int d = 0; d < D; d += 32) {
+    uint32_t o[32];
+    if (nk > 0) {
+      tmem_ld32(tO + d, o);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; e++) o[e] = 0u;
+    }
+    if (!valid) continue;
+    if (part) {
+      float4* dst = reinterpret_cast<float4*>(a.part_o + pr * D + d);
+#pragma unroll
+      for (int e = 0; e < 8; e++)
+        dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                             __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+      continue;
+    }
+    uint32_t y[16];
+#pragma unroll
+    for (int e = 0; e < 16; e++) {
+      const float x0 = __uint_as_float(o[2 * e]) * inv, x1 = __uint_as_float(o[2 * e + 1]) * inv;
+      if (a.type == kTypeBf16) {
+        const __nv_bfloat162 z = __floats2bfloat162_rn(x0, x1);
+        y[e] = *reinterpret_cast<const uint32_t*>(&z);
+      } else {
+        const __half2 z = __floats2half2_rn(x0, x1);
+        y[e] = *reinterpret_cast<const uint32_t*>(&z);
+      }
+    }
+    uint16_t* dst = static_cast<uint16_t*>(a.o) + ob + d;
+    if (vec) {
+#pragma unroll
+      for (int e = 0; e < 4; e++)
+        reinterpret_cast<uint4*>(dst)[e] = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; e++) {
+        dst[2 * e] = static_cast<uint16_t>(y[e]);
+        dst[2 * e + 1] = static_cast<uint16_t>(y[e] >> 16);
+      }
+    }
+  }
+  if (!valid) return;
+  if (part) {
+    *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m - kBoost, l);
+  } else if (a.lse) {
+    a.lse[(static_cast<size_t>(b) * a.H + head) * a.Nq + tok] =
+        l > 0.0f ? (m - kBoost + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) k_cache_prefill(const CacheAttnArgs a, int row_tiles) {
+  extern __shared__ __align__(1024) uint8_t raw[];
+  if (smem_misaligned(raw, a.c.status)) return;
+  PreSmem<D>& s = *reinterpret_cast<PreSmem<D>*>(raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // KV ranges fastest; row tiles from the last to the first (under a causal
+  // mask the last see most)
+  unsigned i = blockIdx.x;
+  const int chunk = static_cast<int>(i % a.chunks);
+  i /= a.chunks;
+  const int h = static_cast<int>(i % a.c.Hkv);
+  i /= a.c.Hkv;
+  const int b = static_cast<int>(i % a.c.B);
+  const int rt = row_tiles - 1 - static_cast<int>(i / a.c.B);
+  const int len = seq_length(a.c, b), qn = query_len(a, b), rows = qn * a.G;
+  const int r0 = rt * (2 * BM);
+  if (r0 >= rows) return;
+  const int r1 = min(rows, r0 + 2 * BM);
+  const long long off = static_cast<long long>(len) - qn;
+  const PageRuns runs = page_runs(a.mask, off + r0 / a.G, off + (r1 - 1) / a.G, len);
+  const int nch = min(a.chunks, (runs.n + a.chunk_pages - 1) / a.chunk_pages);
+  const int p0 = chunk * a.chunk_pages;
+  const int p1 = chunk == a.chunks - 1 ? runs.n : min(runs.n, p0 + a.chunk_pages);
+  if (chunk > 0 && p0 >= runs.n) return;
+  const int nk = p1 > p0 ? (p1 - p0 + 1) / 2 : 0;
+  const int tiles = r1 - r0 > BM ? 2 : 1;
+
+  if (threadIdx.x == 0) {
+    for (int j = 0; j < NS; j++) {
+      mbar_init(&s.k_full[j], 128);
+      mbar_init(&s.k_empty[j], 1);
+      mbar_init(&s.v_full[j], 128);
+      mbar_init(&s.v_empty[j], 1);
+    }
+    for (int j = 0; j < 2; j++) {
+      mbar_init(&s.s_full[j], 1);
+      mbar_init(&s.p_full[j], 4);
+    }
+    mbar_init(&s.drain, 1);
+    s.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(&s.tmem_base, 512);
+    tmem_relinquish();
+  }
+  // query rows to fp16 operands, a warp a row
+  for (int r = warp; r < tiles * BM; r += kThreads / 32) {
+    uint8_t* tile = s.q[r / BM];
+    const float f = stage_row_as<D>(a, b, h, r0 + r, r1, lane, [&](int ch, float x) {
+      *reinterpret_cast<__half*>(tile + op_off(r % BM, ch / 8) + (ch % 8) * 2) = __float2half_rn(x);
+    });
+    if (lane == 0) s.rowf[r] = f * (a.scale * kLog2e);
+  }
+  // a page id that is none is recorded once, by the first range
+  if (chunk == 0)
+    for (int j = threadIdx.x; j < runs.n; j += kThreads) (void)page_id(a.c, b, runs.page(j));
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+  const WaitCtx w{a.budget, a.c.status, &s.abort};
+  if (warp < 8) {
+    set_regs_up<kRegsSoftmax>();
+    const int t = warp >> 2;
+    if (t < tiles)
+      softmax<D>(s, a, tmem, b, h, t, r0, r1, runs, p0, p1, nk, len, off, chunk, nch, row_tiles, w);
+  } else if (warp < 12) {
+    set_regs_down<kRegsConvert>();
+    convert<D>(s, a, runs, b, h, p0, p1, nk, len, w);
+  } else {
+    set_regs_down<kRegsIssue>();
+    if (warp == 12 && lane == 0 && nk > 0) issue<D>(s, tmem, nk, tiles, w);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace
+
+cudaError_t cache_prefill_prepare() {
+  cudaError_t e = cudaFuncSetAttribute(k_cache_prefill<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(sizeof(PreSmem<128>)));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k_cache_prefill<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(sizeof(PreSmem<64>)));
+  return e;
+}
+
+cudaError_t launch_cache_prefill(const CacheAttnArgs& a, cudaStream_t s) {
+  const int row_tiles = (a.Nq * a.G + kPreRows - 1) / kPreRows;
+  const long long units = static_cast<long long>(a.c.B) * a.c.Hkv * row_tiles;
+  const unsigned grid = static_cast<unsigned>(units * a.chunks);
+  if (a.c.D == 128) k_cache_prefill<128><<<grid, kThreads, sizeof(PreSmem<128>), s>>>(a, row_tiles);
+  else k_cache_prefill<64><<<grid, kThreads, sizeof(PreSmem<64>), s>>>(a, row_tiles);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || a.chunks == 1) return e;
+  return launch_cache_merge(a, row_tiles, kPreRows, s);
+}
+
+}  // namespace sage

@@ -23,6 +23,16 @@ _MASKS = "mask must be None, 'causal', ('block_causal', n) or " \
          "('window', frame_len, window_frames, sink_tokens)"
 
 
+_TYPES = {}  # torch dtype -> type code
+
+
+def _type(t):
+    if not _TYPES:
+        import torch
+        _TYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    return _TYPES.get(t.dtype, -1)
+
+
 class _Cache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k_i8", "k_scale", "v_f8", "v_exp", "weight")] + \
                [(n, ctypes.c_int) for n in ("n_pages", "heads", "D")]
@@ -44,6 +54,8 @@ _Strides = ctypes.c_longlong * 3
 
 def declare(L):
     """Result and argument types of the library's functions (called by lib())."""
+    global _L
+    _L = L
     P, I, SZ, LL, F = (ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong,
                        ctypes.c_float)
     L.sage_rope.restype = I
@@ -66,9 +78,14 @@ def declare(L):
     L.sage_cache_evict.argtypes = [P, P, I, I, I, P, I, P, P, P, SZ, P]
 
 
+_L = None  # the library, once declare() has seen it
+
+
 def _lib():
-    from . import lib
-    return lib()
+    if _L is None:
+        from . import lib
+        lib()
+    return _L
 
 
 def _check(code, what):
@@ -77,60 +94,58 @@ def _check(code, what):
         raise SageError(code, what)
 
 
-def _type(t):
+def _here(t, stream):
+    """The current stream's handle if the call can run as it is: `t` on the
+    current device, no other stream asked for.  None otherwise."""
     import torch
-    return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(t.dtype, -1)
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    if stream is None and dev == torch._C._cuda_getDevice():
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return None
 
 
-class _On:
-    """The device of `t` made current, and a stream of it: `stream`, or the
-    device's current one.  Tensors allocated inside belong to that stream."""
+class _There:
+    """`t`'s device made current, and `stream` (or the device's current one):
+    what is allocated inside belongs to that stream."""
 
     def __init__(self, t, stream):
         import torch
-        if not t.is_cuda:
-            raise ValueError("tensors must be CUDA tensors")
-        self.other = None
-        if t.device.index != torch.cuda.current_device():
-            self.other = torch.cuda.device(t.device)
-        self.given = None if stream is None else torch.cuda.stream(stream)
         if stream is not None and stream.device != t.device:
             raise ValueError("the stream belongs to %s, the tensors to %s" % (stream.device,
                                                                               t.device))
+        self.device = torch.cuda.device(t.device)
+        self.stream = torch.cuda.stream(stream)  # of None: no change
 
     def __enter__(self):
-        import torch
-        if self.other is not None:
-            self.other.__enter__()
-        if self.given is not None:
-            self.given.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+        self.device.__enter__()
+        self.stream.__enter__()
 
     def __exit__(self, *exc):
-        if self.given is not None:
-            self.given.__exit__(*exc)
-        if self.other is not None:
-            self.other.__exit__(*exc)
+        self.stream.__exit__(*exc)
+        self.device.__exit__(*exc)
 
 
 def _strides(t):
-    s = t.stride()
-    if s[3] != 1 and t.shape[3] > 1:
+    b, h, n, c = t.stride()
+    B, H, N, C = t.shape
+    if c != 1 and C > 1:
         raise ValueError("the last dimension must have unit stride")
-    return _Strides(*[0 if t.shape[i] == 1 else s[i] for i in range(3)])
+    return _Strides(b if B > 1 else 0, h if H > 1 else 0, n if N > 1 else 0)
 
 
 def _out_strides(t):
-    if any(t.shape[i] > 1 and t.stride(i) == 0 for i in range(3)):
+    if 0 in t.stride() and any(t.shape[i] > 1 and t.stride(i) == 0 for i in range(3)):
         raise ValueError("out must not be an expanded tensor")
     return _strides(t)
 
 
 def _int32(t, shape, what, dev):
     import torch
-    if t.dtype != torch.int32 or t.device != dev or tuple(t.shape) != shape or \
+    if t.dtype is not torch.int32 or t.get_device() != dev or t.shape != shape or \
             not t.is_contiguous():
-        raise ValueError("%s must be a contiguous int32 tensor %s on %s" % (what, shape, dev))
+        raise ValueError("%s must be a contiguous int32 tensor %s on cuda:%d" % (what, shape, dev))
     return t.data_ptr()
 
 
@@ -178,20 +193,20 @@ def rope_freqs(dim, theta=10000.0, scaling=None, device="cuda"):
 
 def _positions(positions, N, B, dev):
     import torch
-    if positions.dtype not in (torch.int32, torch.int64) or positions.device != dev or \
+    if positions.dtype not in (torch.int64, torch.int32) or positions.get_device() != dev or \
             not positions.is_contiguous():
-        raise ValueError("positions must be a contiguous int32 or int64 tensor on %s" % dev)
-    if tuple(positions.shape) not in ((N,), (B, N)):
+        raise ValueError("positions must be a contiguous int32 or int64 tensor on cuda:%d" % dev)
+    if positions.shape != (N,) and positions.shape != (B, N):
         raise ValueError("positions must be [N] or [B, N]")
-    return positions.data_ptr(), int(positions.dtype == torch.int64), \
+    return positions.data_ptr(), int(positions.dtype is torch.int64), \
         (N if positions.dim() == 2 else 0)
 
 
 def _freqs(inv_freq, dev):
     import torch
-    if inv_freq.dtype != torch.float64 or inv_freq.device != dev or inv_freq.dim() != 1 or \
-            not inv_freq.is_contiguous():
-        raise ValueError("inv_freq must be a contiguous float64 vector on %s" % dev)
+    if inv_freq.dtype is not torch.float64 or inv_freq.get_device() != dev or \
+            inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous float64 vector on cuda:%d" % dev)
     return inv_freq.data_ptr(), 2 * inv_freq.numel()
 
 
@@ -208,23 +223,24 @@ def rope(x, positions, inv_freq, layout="interleaved", amplitude=1.0, inverse=Fa
         raise ValueError("x must be a bf16, fp16 or fp32 tensor [B, H, N, D]")
     if layout not in ("interleaved", "half"):
         raise ValueError("layout must be 'interleaved' or 'half'")
+    st = _here(x, stream)
+    if st is None:
+        with _There(x, stream):
+            return rope(x, positions, inv_freq, layout, amplitude, inverse, out)
     B, H, N, D = x.shape
-    on = _On(x, stream)
-    pos, p64, pstride = _positions(positions, N, B, x.device)
-    freq, R = _freqs(inv_freq, x.device)
+    dev = x.get_device()
+    pos, p64, pstride = _positions(positions, N, B, dev)
+    freq, R = _freqs(inv_freq, dev)
     if R > D:
         raise ValueError("inv_freq has more pairs than the heads")
-    if out is not None and (out.shape != x.shape or out.dtype != x.dtype or
-                            out.device != x.device):
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
         raise ValueError("out must have x's shape, type and device")
-    with on as st:
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if x.numel() == 0:
-            return out
+    if x.numel():
         _check(_lib().sage_rope(x.data_ptr(), out.data_ptr(), _type(x), B, H, N, D, R, _strides(x),
-                                _out_strides(out), pos, p64, pstride, freq, float(amplitude),
-                                int(layout == "half"), int(bool(inverse)), st), "sage_rope")
+                                _out_strides(out), pos, p64, pstride, freq, amplitude,
+                                layout == "half", bool(inverse), st), "sage_rope")
     return out
 
 
@@ -232,18 +248,21 @@ def rope_tables(positions, inv_freq, amplitude=1.0, stream=None):
     """sage_rope_tables: (cos, sin), f32 [N, R / 2], the tables quant_qk and
     quant_qk_window take (R = D, interleaved pairs)."""
     import torch
-    on = _On(positions, stream)
-    N = positions.shape[0]
-    pos, p64, _ = _positions(positions, N, 1, positions.device)
+    st = _here(positions, stream)
+    if st is None:
+        with _There(positions, stream):
+            return rope_tables(positions, inv_freq, amplitude)
+    dev = positions.get_device()
     if positions.dim() != 1:
         raise ValueError("positions must be [N]")
-    freq, R = _freqs(inv_freq, positions.device)
-    with on as st:
-        c = torch.empty((N, R // 2), dtype=torch.float32, device=positions.device)
-        s = torch.empty_like(c)
-        if c.numel():
-            _check(_lib().sage_rope_tables(N, R, pos, p64, freq, float(amplitude), c.data_ptr(),
-                                           s.data_ptr(), st), "sage_rope_tables")
+    N = positions.shape[0]
+    pos, p64, _ = _positions(positions, N, 1, dev)
+    freq, R = _freqs(inv_freq, dev)
+    c = torch.empty((N, R // 2), dtype=torch.float32, device=positions.device)
+    s = torch.empty_like(c)
+    if c.numel():
+        _check(_lib().sage_rope_tables(N, R, pos, p64, freq, amplitude, c.data_ptr(), s.data_ptr(),
+                                       st), "sage_rope_tables")
     return c, s
 
 
@@ -290,7 +309,7 @@ class KVCache8:
         self.k_i8, self.k_scale, self.v_f8, self.v_exp, self.weight = (k_i8, k_scale, v_f8, v_exp,
                                                                         weight)
         self.num_pages, self.kv_heads, self.head_dim = P, h, D
-        self.device = k_i8.device
+        self.device, self.index = k_i8.device, k_i8.get_device()
 
     def struct(self, weight=None):
         w = self.weight if weight is None else weight
@@ -300,12 +319,11 @@ class KVCache8:
 
 
 def _seqs(cache, pages, lengths):
-    import torch
     if pages.dim() != 2:
         raise ValueError("pages must be [B, max_pages]")
     B, width = pages.shape
-    return _Seqs(_int32(pages, (B, width), "pages", cache.device),
-                 _int32(lengths, (B,), "lengths", cache.device), B, width)
+    return _Seqs(_int32(pages, (B, width), "pages", cache.index),
+                 _int32(lengths, (B,), "lengths", cache.index), B, width)
 
 
 def cache_append(cache, k, v, pages, lengths, n_new=None, k_shift=None, stream=None):
@@ -314,7 +332,10 @@ def cache_append(cache, k, v, pages, lengths, n_new=None, k_shift=None, stream=N
     advances lengths.  n_new: int32 [B], tokens of each sequence (None: n).
     k_shift: f32 [heads, D] subtracted from the keys, or None."""
     import torch
-    on = _On(cache.k_i8, stream)
+    st = _here(cache.k_i8, stream)
+    if st is None:
+        with _There(cache.k_i8, stream):
+            return cache_append(cache, k, v, pages, lengths, n_new, k_shift)
     sq = _seqs(cache, pages, lengths)
     if k.dim() != 4 or k.shape[0] != sq.B or k.shape[1] != cache.kv_heads or \
             k.shape[3] != cache.head_dim or v.shape != k.shape:
@@ -323,14 +344,13 @@ def cache_append(cache, k, v, pages, lengths, n_new=None, k_shift=None, stream=N
             k.device != cache.device or v.device != cache.device:
         raise ValueError("k and v must be bf16 or fp16 tensors on %s" % cache.device)
     _shift_ok(cache, k_shift)
-    nn = None if n_new is None else _int32(n_new, (sq.B,), "n_new", cache.device)
+    nn = None if n_new is None else _int32(n_new, (sq.B,), "n_new", cache.index)
     if k.shape[2] == 0 or sq.B == 0:
         return
-    with on as st:
-        _check(_lib().sage_cache_append(
-            ctypes.byref(cache.struct()), ctypes.byref(sq), k.data_ptr(), v.data_ptr(), _type(k),
-            k.shape[2], _strides(k), _strides(v), nn,
-            None if k_shift is None else k_shift.data_ptr(), st), "sage_cache_append")
+    _check(_lib().sage_cache_append(
+        ctypes.byref(cache.struct()), ctypes.byref(sq), k.data_ptr(), v.data_ptr(), _type(k),
+        k.shape[2], _strides(k), _strides(v), nn,
+        None if k_shift is None else k_shift.data_ptr(), st), "sage_cache_append")
 
 
 def _shift_ok(cache, k_shift):
@@ -347,22 +367,24 @@ def cache_read(cache, pages, lengths, n, starts=None, k_shift=None, weights=Fals
     sequence from token starts[b] (int32 [B]; None: 0) on, zero where there is
     none; with `weights` also their summed weights, f32 [B, heads, n]."""
     import torch
-    on = _On(cache.k_i8, stream)
+    st = _here(cache.k_i8, stream)
+    if st is None:
+        with _There(cache.k_i8, stream):
+            return cache_read(cache, pages, lengths, n, starts, k_shift, weights)
     sq = _seqs(cache, pages, lengths)
     _shift_ok(cache, k_shift)
-    sp = None if starts is None else _int32(starts, (sq.B,), "starts", cache.device)
+    sp = None if starts is None else _int32(starts, (sq.B,), "starts", cache.index)
     if weights and cache.weight is None:
         raise ValueError("the cache keeps no weights")
-    with on as st:
-        k = torch.empty((sq.B, cache.kv_heads, n, cache.head_dim), dtype=torch.float32,
-                        device=cache.device)
-        v = torch.empty_like(k)
-        w = torch.empty(k.shape[:3], dtype=torch.float32, device=cache.device) if weights else None
-        if k.numel():
-            _check(_lib().sage_cache_read(
-                ctypes.byref(cache.struct()), ctypes.byref(sq), n, sp,
-                None if k_shift is None else k_shift.data_ptr(), k.data_ptr(), v.data_ptr(),
-                None if w is None else w.data_ptr(), st), "sage_cache_read")
+    k = torch.empty((sq.B, cache.kv_heads, n, cache.head_dim), dtype=torch.float32,
+                    device=cache.device)
+    v = torch.empty_like(k)
+    w = torch.empty(k.shape[:3], dtype=torch.float32, device=cache.device) if weights else None
+    if k.numel():
+        _check(_lib().sage_cache_read(
+            ctypes.byref(cache.struct()), ctypes.byref(sq), n, sp,
+            None if k_shift is None else k_shift.data_ptr(), k.data_ptr(), v.data_ptr(),
+            None if w is None else w.data_ptr(), st), "sage_cache_read")
     return (k, v, w) if weights else (k, v)
 
 
@@ -379,23 +401,23 @@ def _mask(mask):
 
 
 def _query(q, cache, sq, q_lens, max_len, scale):
-    import torch
     if q.dim() != 4 or q.shape[0] != sq.B or q.shape[3] != cache.head_dim or \
             q.shape[1] % cache.kv_heads:
         raise ValueError("q must be [B, H, Nq, %d], H a multiple of %d" % (cache.head_dim,
                                                                          cache.kv_heads))
-    if q.dtype not in (torch.bfloat16, torch.float16) or q.device != cache.device:
+    kind = _type(q)
+    if kind not in (0, 1) or q.get_device() != cache.index:
         raise ValueError("q must be a bf16 or fp16 tensor on %s" % cache.device)
     cap = sq.max_pages * PAGE
     return _Query(q.data_ptr(), _strides(q),
-                  None if q_lens is None else _int32(q_lens, (sq.B,), "q_lens", cache.device),
-                  _type(q), q.shape[1], q.shape[2], cap if max_len is None else min(int(max_len), cap),
+                  None if q_lens is None else _int32(q_lens, (sq.B,), "q_lens", cache.index),
+                  kind, q.shape[1], q.shape[2], cap if max_len is None else min(int(max_len), cap),
                   cache.head_dim ** -0.5 if scale is None else float(scale))
 
 
 def cache_attn_workspace_bytes(cache, B, H, Nq, max_len, mask=None):
     """sage_cache_attn_workspace_bytes on the cache's device."""
-    with _On(cache.k_i8, None):
+    with _There(cache.k_i8, None):
         n = _lib().sage_cache_attn_workspace_bytes(B, cache.kv_heads, H, Nq, cache.head_dim,
                                                    int(max_len), *_mask(mask))
     if n == 0:
@@ -414,7 +436,11 @@ def cache_attn(q, cache, pages, lengths, mask=None, q_lens=None, max_len=None, s
     bound on the lengths known to the host (None: what the page table holds);
     it only chooses how the work is cut.  scale: None is 1 / sqrt(D)."""
     import torch
-    on = _On(cache.k_i8, stream)
+    st = _here(cache.k_i8, stream)
+    if st is None:
+        with _There(cache.k_i8, stream):
+            return cache_attn(q, cache, pages, lengths, mask, q_lens, max_len, scale, out, lse,
+                              return_lse, workspace)
     sq = _seqs(cache, pages, lengths)
     qs = _query(q, cache, sq, q_lens, max_len, scale)
     m = _mask(mask)
@@ -424,23 +450,22 @@ def cache_attn(q, cache, pages, lengths, mask=None, q_lens=None, max_len=None, s
     if lse is not None and (lse.shape != q.shape[:3] or lse.dtype != torch.float32 or
                             lse.device != q.device or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 tensor [B, H, Nq]")
-    with on as st:
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if lse is None and return_lse:
-            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-        if q.numel():
-            if workspace is None:
-                n = _lib().sage_cache_attn_workspace_bytes(
-                    sq.B, cache.kv_heads, qs.H, qs.Nq, cache.head_dim, qs.max_len, *m)
-                workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
-            elif workspace.device != q.device or not workspace.is_contiguous():
-                raise ValueError("workspace must be a contiguous tensor on %s" % q.device)
-            _check(_lib().sage_cache_attn(
-                ctypes.byref(cache.struct()), ctypes.byref(sq), ctypes.byref(qs), *m,
-                out.data_ptr(), _out_strides(out), None if lse is None else lse.data_ptr(),
-                workspace.data_ptr(), workspace.numel() * workspace.element_size(), st),
-                "sage_cache_attn")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if lse is None and return_lse:
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    if q.numel():
+        if workspace is None:
+            n = _lib().sage_cache_attn_workspace_bytes(
+                sq.B, cache.kv_heads, qs.H, qs.Nq, cache.head_dim, qs.max_len, *m)
+            workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+        elif workspace.device != q.device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on %s" % q.device)
+        _check(_lib().sage_cache_attn(
+            ctypes.byref(cache.struct()), ctypes.byref(sq), ctypes.byref(qs), *m,
+            out.data_ptr(), _out_strides(out), None if lse is None else lse.data_ptr(),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), st),
+            "sage_cache_attn")
     return (out, lse) if return_lse else out
 
 
@@ -451,7 +476,11 @@ def cache_weights(q, cache, lse, pages, lengths, mask=None, q_lens=None, max_len
     accumulate=False, written over) cache.weight -- or `weight`, a float32
     tensor [pages, heads, 64].  Returns that tensor."""
     import torch
-    on = _On(cache.k_i8, stream)
+    st = _here(cache.k_i8, stream)
+    if st is None:
+        with _There(cache.k_i8, stream):
+            return cache_weights(q, cache, lse, pages, lengths, mask, q_lens, max_len, scale, weight,
+                                 accumulate)
     sq = _seqs(cache, pages, lengths)
     qs = _query(q, cache, sq, q_lens, max_len, scale)
     if lse.shape != q.shape[:3] or lse.dtype != torch.float32 or lse.device != q.device or \
@@ -465,10 +494,9 @@ def cache_weights(q, cache, lse, pages, lengths, mask=None, q_lens=None, max_len
         raise ValueError("weight must be a contiguous float32 tensor [pages, heads, %d]" % PAGE)
     if sq.B == 0 or q.shape[1] == 0 or q.shape[2] == 0:
         return w
-    with on as st:
-        _check(_lib().sage_cache_weights(
-            ctypes.byref(cache.struct(w)), ctypes.byref(sq), ctypes.byref(qs), *_mask(mask),
-            lse.data_ptr(), int(bool(accumulate)), st), "sage_cache_weights")
+    _check(_lib().sage_cache_weights(
+        ctypes.byref(cache.struct(w)), ctypes.byref(sq), ctypes.byref(qs), *_mask(mask),
+        lse.data_ptr(), bool(accumulate), st), "sage_cache_weights")
     return w
 
 
@@ -480,7 +508,10 @@ def cache_evict(cache, pages, lengths, keep, sink=0, recent=0, pages_out=None, w
     >= ceil(keep / 64)], pages the survivors go to (none of them in `pages`);
     None: the sequences' own first pages."""
     import torch
-    on = _On(cache.k_i8, stream)
+    st = _here(cache.k_i8, stream)
+    if st is None:
+        with _There(cache.k_i8, stream):
+            return cache_evict(cache, pages, lengths, keep, sink, recent, pages_out, workspace)
     sq = _seqs(cache, pages, lengths)
     keep, sink, recent = int(keep), int(sink), int(recent)
     if cache.weight is None:
@@ -492,21 +523,20 @@ def cache_evict(cache, pages, lengths, keep, sink=0, recent=0, pages_out=None, w
         if pages_out.dim() != 2 or pages_out.shape[1] * PAGE < keep:
             raise ValueError("pages_out must be [B, at least %d]" % -(-keep // PAGE))
         width = pages_out.shape[1]
-        po = _int32(pages_out, (sq.B, width), "pages_out", cache.device)
-    with on as st:
-        kept = torch.empty((sq.B, cache.kv_heads, keep), dtype=torch.int32, device=cache.device)
-        out = torch.empty((sq.B,), dtype=torch.int32, device=cache.device)
-        if sq.B == 0:
-            return kept, out
-        if po is None and workspace is None:
-            n = _lib().sage_cache_evict_workspace_bytes(sq.B, cache.kv_heads, cache.head_dim, keep)
-            workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=cache.device)
-        if workspace is not None and (workspace.device != cache.device or
-                                      not workspace.is_contiguous()):
-            raise ValueError("workspace must be a contiguous tensor on %s" % cache.device)
-        _check(_lib().sage_cache_evict(
-            ctypes.byref(cache.struct()), ctypes.byref(sq), keep, sink, recent, po, width,
-            kept.data_ptr(), out.data_ptr(), None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), st),
-            "sage_cache_evict")
+        po = _int32(pages_out, (sq.B, width), "pages_out", cache.index)
+    kept = torch.empty((sq.B, cache.kv_heads, keep), dtype=torch.int32, device=cache.device)
+    out = torch.empty((sq.B,), dtype=torch.int32, device=cache.device)
+    if sq.B == 0:
+        return kept, out
+    if po is None and workspace is None:
+        n = _lib().sage_cache_evict_workspace_bytes(sq.B, cache.kv_heads, cache.head_dim, keep)
+        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=cache.device)
+    if workspace is not None and (workspace.device != cache.device or
+                                  not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on %s" % cache.device)
+    _check(_lib().sage_cache_evict(
+        ctypes.byref(cache.struct()), ctypes.byref(sq), keep, sink, recent, po, width,
+        kept.data_ptr(), out.data_ptr(), None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), st),
+        "sage_cache_evict")
     return kept, out
