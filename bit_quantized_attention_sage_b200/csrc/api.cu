@@ -214,8 +214,9 @@ int* api_status_word() {
   return d ? d->status : nullptr;
 }
 long long api_wait_budget() { return kWaitBudget; }
-bool api_tile_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t tiles, uint32_t D) {
-  return encode_u8_3d(m, base, D, rows, tiles, D, static_cast<uint32_t>(rows),
+bool api_tile_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t tiles, uint32_t D,
+                  uint32_t box_rows) {
+  return encode_u8_3d(m, base, D, rows, tiles, D, box_rows,
                       D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 }  // namespace sage

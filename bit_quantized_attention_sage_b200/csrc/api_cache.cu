@@ -100,11 +100,11 @@ Plan plan_of(const CacheMask& m, int B, int Hkv, int G, int Nq, int D, int max_l
     }
     cp = std::max(4ll, cp);
   } else {
-    // Ranges so short that the blocks come in about four rounds over the SMs
-    // (uneven sequences then even out), but of four pages at least: one for
-    // each warp of the block.
-    const long long want = std::max(1ll, 4ll * sms / std::max(1ll, units));
-    cp = std::max(4ll, ((pages + want - 1) / want + 3) / 4 * 4);
+    // Two blocks an SM: ranges so short that the blocks come in about four
+    // rounds (uneven sequences then even out), but of four pages at least,
+    // two half pages for each warp of the block.
+    const long long want = std::max(1ll, 8ll * sms / std::max(1ll, units));
+    cp = std::max(4ll, ((pages + want - 1) / want + 1) / 2 * 2);
   }
   while ((pages + cp - 1) / cp > kCacheChunksMax) cp *= 2;
   p.chunk_pages = static_cast<int>(cp);
@@ -127,8 +127,14 @@ bool attn_shape_ok(const sage_kv_cache* c, const sage_kv_seqs* s, int H, int Nq,
   return static_cast<long long>(H / c->heads) * Nq <= (1 << 28);
 }
 
+bool maps_of(const sage_kv_cache* c, CacheAttnMaps* m) {
+  const uint64_t tiles = static_cast<uint64_t>(c->n_pages) * c->heads;
+  return api_tile_map(&m->k, c->k_i8, kPage, tiles, c->D, kPage / 2) &&
+         api_tile_map(&m->v, c->v_f8, kPage, tiles, c->D, kPage / 2);
+}
+
 sage_status attn_common(const sage_kv_cache* c, const sage_kv_seqs* s, const sage_kv_query* q, int mask,
-                        int mask_block, int win, int sink, CacheAttnArgs* a, CacheAttnMaps* maps) {
+                        int mask_block, int win, int sink, CacheAttnArgs* a) {
   if (!cache_ok(c) || !seqs_ok(s) || !q) return SAGE_ERR_INVALID_ARG;
   if (!attn_shape_ok(c, s, q->H, q->Nq, q->max_len)) return SAGE_ERR_INVALID_ARG;
   if (q->type != kTypeBf16 && q->type != kTypeF16) return SAGE_ERR_INVALID_ARG;
@@ -149,13 +155,10 @@ sage_status attn_common(const sage_kv_cache* c, const sage_kv_seqs* s, const sag
   a->qb = q->q_strides[0];
   a->qh = q->q_strides[1];
   a->qn = q->q_strides[2];
+  a->q_vec = al(q->q, 16) && ((a->qb | a->qh | a->qn) & 7) == 0;
   a->q_lens = q->q_lens;
   a->scale = q->scale;
   a->budget = api_wait_budget();
-  const uint64_t tiles = static_cast<uint64_t>(c->n_pages) * c->heads;
-  if (!api_tile_map(&maps->k, c->k_i8, kPage, tiles, c->D) ||
-      !api_tile_map(&maps->v, c->v_f8, kPage, tiles, c->D))
-    return SAGE_ERR_CUDA;
   return SAGE_OK;
 }
 
@@ -292,8 +295,7 @@ SAGE_EXPORT sage_status sage_cache_attn(const sage_kv_cache* cache, const sage_k
                                         void* workspace, size_t workspace_bytes, void* stream) {
   if (!al(out, 2) || !strides_ok(o_strides) || (lse && !al(lse, 4))) return SAGE_ERR_INVALID_ARG;
   CacheAttnArgs a{};
-  CacheAttnMaps maps;
-  const sage_status st = attn_common(cache, seqs, query, mask, mask_block, win, sink, &a, &maps);
+  const sage_status st = attn_common(cache, seqs, query, mask, mask_block, win, sink, &a);
   if (st != SAGE_OK) return st;
   const int sms = sm_count();
   if (!sms) return SAGE_ERR_CUDA;
@@ -309,8 +311,10 @@ SAGE_EXPORT sage_status sage_cache_attn(const sage_kv_cache* cache, const sage_k
   a.chunks = p.chunks;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = a.part_o + p.rows * p.chunks * cache->D;
-  return status_of(p.prefill ? launch_cache_prefill(a, static_cast<cudaStream_t>(stream))
-                             : launch_cache_decode(maps, a, static_cast<cudaStream_t>(stream)));
+  if (p.prefill) return status_of(launch_cache_prefill(a, static_cast<cudaStream_t>(stream)));
+  CacheAttnMaps maps;
+  if (!maps_of(cache, &maps)) return SAGE_ERR_CUDA;
+  return status_of(launch_cache_decode(maps, a, static_cast<cudaStream_t>(stream)));
 }
 
 SAGE_EXPORT sage_status sage_cache_weights(const sage_kv_cache* cache, const sage_kv_seqs* seqs,
@@ -318,17 +322,27 @@ SAGE_EXPORT sage_status sage_cache_weights(const sage_kv_cache* cache, const sag
                                            int sink, const float* lse, int accumulate, void* stream) {
   if (!al(lse, 4) || !cache_ok(cache) || !cache->weight) return SAGE_ERR_INVALID_ARG;
   CacheAttnArgs a{};
-  CacheAttnMaps maps;
-  const sage_status st = attn_common(cache, seqs, query, mask, mask_block, win, sink, &a, &maps);
+  const sage_status st = attn_common(cache, seqs, query, mask, mask_block, win, sink, &a);
   if (st != SAGE_OK) return st;
   a.lse_in = lse;
   a.accumulate = accumulate != 0;
-  const int pages = (query->max_len + kPage - 1) / kPage;
-  if (pages == 0) return SAGE_OK;
-  a.chunks = (pages + 3) / 4;
-  if (static_cast<long long>(seqs->B) * cache->heads * a.chunks > (1ll << 31) - 1)
-    return SAGE_ERR_UNSUPPORTED;
-  return status_of(launch_cache_weights(maps, a, static_cast<cudaStream_t>(stream)));
+  const int sms = sm_count();
+  if (!sms) return SAGE_ERR_CUDA;
+  const int pages = std::max(1, (query->max_len + kPage - 1) / kPage);
+  const long long units = static_cast<long long>(seqs->B) * cache->heads;
+  // Two blocks an SM, each with query rows to stage before its first key: as
+  // many keys a block as leave four rounds of blocks (uneven sequences then
+  // even out).
+  const long long want = std::max(1ll, 8ll * sms / units);
+  a.chunk_pages = static_cast<int>(((pages + want - 1) / want + 3) / 4 * 4);
+  a.chunks = (pages + a.chunk_pages - 1) / a.chunk_pages;
+  if (units * a.chunks > (1ll << 31) - 1) return SAGE_ERR_UNSUPPORTED;
+  // up to 16 query rows the keys stream past one mma.sync tile
+  if (static_cast<long long>(a.Nq) * a.G > kDecRows)
+    return status_of(launch_cache_weights(a, static_cast<cudaStream_t>(stream)));
+  CacheAttnMaps maps;
+  if (!maps_of(cache, &maps)) return SAGE_ERR_CUDA;
+  return status_of(launch_cache_weights_few(maps, a, static_cast<cudaStream_t>(stream)));
 }
 
 SAGE_EXPORT size_t sage_cache_evict_workspace_bytes(int B, int heads, int D, int keep) {

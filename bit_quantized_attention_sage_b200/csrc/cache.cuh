@@ -192,13 +192,14 @@ size_t cache_evict_ws_bytes(int B, int Hkv, int D, int keep);
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s);
 
 struct CacheAttnMaps {
-  CUtensorMap k, v;  // uint8 [pages * heads][64][D], box D x 64
+  CUtensorMap k, v;  // uint8 [pages * heads][64][D], box D x 32
 };
 struct CacheAttnArgs {
   CacheView c;
   const void* q;
   void* o;
   int type, H, G, Nq;
+  int q_vec;         // query rows are 16-byte aligned
   long long qb, qh, qn, ob, oh, on;  // strides, elements
   const int* q_lens;                 // [B] or null
   CacheMask mask;
@@ -206,7 +207,7 @@ struct CacheAttnArgs {
   float* lse;        // f32 [B][H][Nq] or null
   const float* lse_in;
   int accumulate;    // cache_weights: add to the weights, or overwrite them
-  // partial results of KV ranges
+  // KV ranges (cache_attn: with partial results)
   int chunk_pages, chunks;
   float *part_o, *part_ml;
   long long budget;
@@ -218,6 +219,8 @@ cudaError_t cache_prefill_prepare();
 cudaError_t launch_cache_prefill(const CacheAttnArgs& a, cudaStream_t s);
 cudaError_t launch_cache_merge(const CacheAttnArgs& a, int row_tiles, int tile_rows, cudaStream_t s);
 cudaError_t launch_cache_decode(const CacheAttnMaps& m, const CacheAttnArgs& a, cudaStream_t s);
-cudaError_t launch_cache_weights(const CacheAttnMaps& m, const CacheAttnArgs& a, cudaStream_t s);
+cudaError_t cache_weights_prepare();
+cudaError_t launch_cache_weights_few(const CacheAttnMaps& m, const CacheAttnArgs& a, cudaStream_t s);
+cudaError_t launch_cache_weights(const CacheAttnArgs& a, cudaStream_t s);
 
 }  // namespace sage

@@ -1,6 +1,6 @@
 // cache_attn.cu -- attention over the paged 8-bit cache for few query rows
-// (single tokens, grouped heads), the merge of its KV ranges, and the
-// attention weight that each cached key received.
+// (single tokens, grouped heads), the merge of KV ranges, and, in the same
+// stream of keys, the attention weight that each cached key received.
 //
 // The query heads that share a key head are rows of one tile: row r of
 // (sequence b, key head h) is token r / G, head h G + r % G.
@@ -10,21 +10,27 @@
 // row's maximum.  int8 key codes are exact in fp16, so the products are exact
 // and only the fp32 accumulation rounds; the page's key scale, the row's
 // power and log2(e) * softmax scale multiply the sum.
-// Probabilities.  y = 2^(t + e - M + 12), t the score in log2 units, e the
-// page's value exponent, M the running maximum of t + e: fp16(y) is off by at
-// most 2^-11 of each weight down to 2^-26 of the largest term, where fp16's
-// subnormal range begins.  The sum L
-// takes y 2^-e in fp32 before that rounding.  e4m3 value codes are exact in
-// fp16.  O = (sum y code) / L; the value scales need no multiplication.
+// Probabilities.  y = 2^(t + e - M + 7), t the score in log2 units, e the
+// page's value exponent, M a reference maximum of t + e that follows the
+// running one in steps of at least 2^8: y <= 2^15, and fp16(y) is off by at
+// most 2^-11 of each weight down to 2^-21 of the largest term, where fp16's
+// subnormal range begins.  The sum L takes y 2^-e in fp32 before that
+// rounding.  e4m3 value codes are exact in fp16.  O = (sum y code) / L; the
+// value scales need no multiplication.
 //
 // What bounds it: the codes, read once (2 D bytes a key and head).  Every
-// warp walks pages of its own through a private two-stage ring of TMA loads
-// (32 KB in flight a warp at D = 128), so no barrier joins the warps until
-// the end; 16-row tiles on mma.sync keep the tensor work (a sixteenth used
-// for one row) under the load time, where a 128-row tcgen05 tile would not
-// fit the registers and shared memory of that many loads.
+// warp walks half pages of its own (32 keys) through a private ring of three
+// TMA loads (24 KB in flight a warp at D = 128, 192 KB an SM with two blocks),
+// so no barrier joins the warps until the end.  Page ids, key scales and
+// value exponents of a warp's next 32 half pages are fetched at once, one a
+// lane; taken one by one inside the loop, their three dependent loads cost
+// more than the tile.  16-row tiles on mma.sync (a sixteenth used for one
+// row) keep the issue slots at about a third of the load time; a 128-row
+// tcgen05 tile would need its codes converted through shared memory first.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <cfloat>
 
 #include "cache.cuh"
 #include "cache_dev.cuh"
@@ -35,11 +41,13 @@ namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kWarps = 4;
-constexpr int kStages = 2;
-constexpr float kBoost = 12.0f;
+constexpr int kStages = 3;
+constexpr int kHalf = 32;      // keys a tile
+constexpr float kBoost = 7.0f;  // y = 2^7 at the reference maximum
+constexpr float kLazy = 8.0f;   // growth of the maximum that moves the reference
 constexpr float kLn2 = 0.69314718055994531f;
 
-enum : int { kSiteDecPage = 0x20101, kSiteDecDrain, kSiteWgtPage, kSiteWgtDrain };
+enum : int { kSiteDecPage = 0x20101, kSiteDecDrain };
 
 // ---------------------------------------------------------------- tile access
 
@@ -87,12 +95,21 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, const
 
 // ---------------------------------------------------------------- decode
 
+// A tile of the ring: half a page.
+struct TileMeta {
+  float ks;  // key scale
+  int ve;    // value exponent
+  int j0;    // first key, or -1: no page
+  int unit;  // (page, head)
+};
+
 template <int D>
 struct alignas(1024) DecSmem {
-  uint8_t kv[kWarps][kStages][2][kPage * D];  // TMA tiles: K, V
+  uint8_t kv[kWarps][kStages][2][kHalf * D];  // TMA tiles: K, V
   __half q[kDecRows][D + 16];                 // padded: 8-byte reads of 4 rows on different banks
   float rowf[kDecRows];                       // 2^e * scale * log2(e) of each row
   float ml[kWarps][kDecRows][2];
+  TileMeta meta[kWarps][kStages];
   uint64_t full[kWarps][kStages];
   int abort;
 };
@@ -126,8 +143,10 @@ __device__ __forceinline__ void store_o2(const CacheAttnArgs& a, size_t i, float
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32)
+// WEIGHTS: instead of attending, w[key] (+)= sum over the tile's rows of
+// exp(s - lse), with the rows' lse given (at most 16 rows: one tile).
+template <int D, bool WEIGHTS>
+__global__ void __launch_bounds__(kWarps * 32, 2)
     k_cache_decode(const __grid_constant__ CacheAttnMaps maps, const CacheAttnArgs a, int row_tiles) {
   extern __shared__ __align__(1024) uint8_t raw[];
   if (smem_misaligned(raw, a.c.status)) return;
@@ -137,42 +156,66 @@ __global__ void __launch_bounds__(kWarps * 32)
   const TileId id = tile_id(a, row_tiles);
   const int len = seq_length(a.c, id.b), qn = query_len(a, id.b);
   const int rows = qn * a.G, r0 = id.rt * kDecRows;
-  if (r0 >= rows) return;
+  if (r0 >= rows && !WEIGHTS) return;
   const int r1 = min(rows, r0 + kDecRows);
   const long long off = static_cast<long long>(len) - qn;  // position of token 0
-  const PageRuns runs = page_runs(a.mask, off + r0 / a.G, off + (r1 - 1) / a.G, len);
+  PageRuns runs;
+  if constexpr (WEIGHTS) {  // every page: those that no row sees get 0
+    runs.n = runs.ns = (len + kPage - 1) / kPage;
+    runs.gap = 0;
+  } else {
+    runs = page_runs(a.mask, off + r0 / a.G, off + (r1 - 1) / a.G, len);
+  }
   // the last range takes whatever a sequence longer than announced adds
   const int p0 = id.chunk * a.chunk_pages;
   const int p1 = id.chunk == a.chunks - 1 ? runs.n : min(runs.n, p0 + a.chunk_pages);
-  if (id.chunk > 0 && p0 >= runs.n) return;  // range 0 also serves an empty sequence
+  // range 0 also serves an empty sequence
+  if (p0 >= runs.n && (WEIGHTS || id.chunk > 0)) return;
 
-  if (threadIdx.x == 0) {
-    for (int w = 0; w < kWarps; w++)
-      for (int i = 0; i < kStages; i++) mbar_init(&s.full[w][i], 1);
-    s.abort = 0;
+  if (lane == 0) {
+    for (int i = 0; i < kStages; i++) mbar_init(&s.full[warp][i], 1);
+    if (warp == 0) s.abort = 0;
     fence_mbar_init();
   }
   __syncthreads();
   const WaitCtx wc{a.budget, a.c.status, &s.abort};
-  // this warp's pages: p0 + warp, p0 + warp + kWarps, ...; loads that the
-  // ring holds are issued before the query rows are read
-  const int mine = p0 + warp < p1 ? (p1 - p0 - warp + kWarps - 1) / kWarps : 0;
-  auto issue = [&](int i) {  // lane 0: K and V of the warp's i-th page
-    const int blk = runs.page(p0 + warp + i * kWarps);
-    const int pg = page_id(a.c, id.b, blk);
-    uint64_t* bar = &s.full[warp][i % kStages];
-    if (pg < 0) {  // no page: nothing to load, the keys are masked below
-      mbar_arrive(bar);
-      return;
-    }
-    mbar_arrive_expect_tx(bar, 2 * kPage * D);
-    const int z = pg * a.c.Hkv + id.h;
-    tma_load_3d(s.kv[warp][i % kStages][0], &maps.k, bar, 0, 0, z);
-    tma_load_3d(s.kv[warp][i % kStages][1], &maps.v, bar, 0, 0, z);
-  };
+  // this warp's half pages: warp, warp + kWarps, ... of the range's
+  const int halves = max(0, 2 * (p1 - p0));
+  const int mine = warp < halves ? (halves - warp + kWarps - 1) / kWarps : 0;
+  TileMeta next{0.0f, 0, -1, 0};  // lane's tile of the current 32
   int issued = 0;
-  if (lane == 0)
-    for (; issued < min(mine, kStages); issued++) issue(issued);
+  auto issue = [&]() {  // the whole warp: the load of tile `issued`
+    if ((issued & 31) == 0) {
+      const int q = warp + (issued + lane) * kWarps;
+      next = TileMeta{0.0f, 0, -1, 0};
+      if (q < halves) {
+        const int blk = runs.page(p0 + q / 2);
+        const int pg = page_id(a.c, id.b, blk);
+        if (pg >= 0) {
+          next.unit = pg * a.c.Hkv + id.h;
+          next.j0 = blk * kPage + (q & 1) * kHalf;
+          next.ks = __ldg(a.c.k_scale + next.unit);
+          if (!WEIGHTS) next.ve = __ldg(a.c.v_exp + next.unit);
+        }
+      }
+    }
+    if (lane == (issued & 31)) {
+      const int st = issued % kStages;
+      uint64_t* bar = &s.full[warp][st];
+      if (next.j0 >= len) next.j0 = -1;  // the half behind the end
+      s.meta[warp][st] = next;
+      if (next.j0 < 0) {
+        mbar_arrive(bar);  // nothing to load
+      } else {
+        mbar_arrive_expect_tx(bar, (WEIGHTS ? 1 : 2) * kHalf * D);
+        const int y = next.j0 & (kPage - 1);
+        tma_load_3d(s.kv[warp][st][0], &maps.k, bar, 0, y, next.unit);
+        if (!WEIGHTS) tma_load_3d(s.kv[warp][st][1], &maps.v, bar, 0, y, next.unit);
+      }
+    }
+    issued++;
+  };
+  while (issued < min(mine, kStages)) issue();
   for (int r = warp; r < kDecRows; r += kWarps) {
     const float f = stage_row<D>(a, id.b, id.h, r0 + r, r1, s.q[r], lane);
     if (lane == 0) s.rowf[r] = f * (a.scale * kLog2e);
@@ -193,11 +236,18 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
   const float f0 = s.rowf[g], f1 = s.rowf[g + 8];
   KeyRange kr[2];
+  float nl[2] = {-INFINITY, -INFINITY};  // WEIGHTS: -lse log2(e); -inf: weight 0
 #pragma unroll
   for (int i = 0; i < 2; i++) {
     const int r = r0 + g + 8 * i;
-    kr[i] = key_range(a.mask, off + r / a.G, len);
-    if (r >= r1) kr[i] = KeyRange{0, 0, 0};
+    kr[i] = KeyRange{0, 0, 0};
+    if (r < r1) {
+      kr[i] = key_range(a.mask, off + r / a.G, len);
+      if (WEIGHTS) {
+        const float v = __ldg(a.lse_in + (static_cast<size_t>(id.b) * a.H + id.h * a.G + r % a.G) * a.Nq + r / a.G);
+        if (v != -INFINITY) nl[i] = -v * kLog2e;
+      }
+    }
   }
   float o[D / 8][4];
 #pragma unroll
@@ -211,30 +261,25 @@ __global__ void __launch_bounds__(kWarps * 32)
     const int st = i % kStages;
     ok = __all_sync(kFull, mbar_wait(&s.full[warp][st], (i / kStages) & 1, wc, kSiteDecPage));
     if (!ok) break;
-    const int blk = runs.page(p0 + warp + i * kWarps), j0 = blk * kPage;
-    const int pg = __ldg(a.c.pages + static_cast<size_t>(id.b) * a.c.max_pages + blk);
-    const bool there = static_cast<unsigned>(pg) < static_cast<unsigned>(a.c.n_pages);
-    if (there) {
-      const size_t unit = static_cast<size_t>(pg) * a.c.Hkv + id.h;
-      const float ks = __ldg(a.c.k_scale + unit);
-      const int vexp = __ldg(a.c.v_exp + unit);
-      const float ve = static_cast<float>(vexp);
+    const TileMeta md = s.meta[warp][st];
+    const int j0 = md.j0;
+    if (j0 >= 0) {
       const uint32_t kb = smem_u32(s.kv[warp][st][0]), vb = smem_u32(s.kv[warp][st][1]);
-      if (j0 + kPage > len) {
-        // the sequence ends inside this page: values behind it may be any
+      if (!WEIGHTS && j0 + kHalf > len) {
+        // the sequence ends inside this tile: values behind it may be any
         // bytes (NaN among them), and zero weight times NaN is NaN.  The last
-        // page of the warp, so no later TMA load meets these writes.
-        for (int x = lane; x < kPage * D / 16; x += 32) {
+        // tile that this warp loads, so no later TMA load meets these writes.
+        for (int x = lane; x < kHalf * D / 16; x += 32) {
           const int r = x / (D / 16);
           if (j0 + r >= len)
             *reinterpret_cast<uint4*>(s.kv[warp][st][1] + swz<D>(r, x % (D / 16))) = make_uint4(0, 0, 0, 0);
         }
         __syncwarp();
       }
-      // scores: 8 tiles of 8 keys
-      float sc[8][4];
+      // scores: 4 tiles of 8 keys
+      float sc[4][4];
 #pragma unroll
-      for (int nt = 0; nt < 8; nt++) {
+      for (int nt = 0; nt < 4; nt++) {
 #pragma unroll
         for (int e = 0; e < 4; e++) sc[nt][e] = 0.0f;
 #pragma unroll
@@ -249,22 +294,15 @@ __global__ void __launch_bounds__(kWarps * 32)
           }
         }
       }
-      const float c0 = f0 * ks, c1 = f1 * ks;
-#pragma unroll
-      for (int nt = 0; nt < 8; nt++) {
-        sc[nt][0] *= c0;
-        sc[nt][1] *= c0;
-        sc[nt][2] *= c1;
-        sc[nt][3] *= c1;
-      }
-      // keys [na, nb) of the page are masked for a row unless in its ranges
+      // a zero scale must not meet -inf as 0 * inf
+      const float c0 = fmaxf(f0 * md.ks, FLT_MIN), c1 = fmaxf(f1 * md.ks, FLT_MIN);
       bool all = true;
 #pragma unroll
       for (int i2 = 0; i2 < 2; i2++)
-        all = all && (kr[i2].sink >= j0 + kPage || (kr[i2].lo <= j0 && kr[i2].hi >= j0 + kPage));
+        all = all && (kr[i2].sink >= j0 + kHalf || (kr[i2].lo <= j0 && kr[i2].hi >= j0 + kHalf));
       if (!__all_sync(kFull, all)) {
 #pragma unroll
-        for (int nt = 0; nt < 8; nt++)
+        for (int nt = 0; nt < 4; nt++)
 #pragma unroll
           for (int e = 0; e < 4; e++) {
             const KeyRange& k = kr[e >> 1];
@@ -272,63 +310,95 @@ __global__ void __launch_bounds__(kWarps * 32)
             if (!(j < k.sink || (j >= k.lo && j < k.hi))) sc[nt][e] = -INFINITY;
           }
       }
-      float pm[2] = {-INFINITY, -INFINITY};
+      if constexpr (WEIGHTS) {
 #pragma unroll
-      for (int nt = 0; nt < 8; nt++) {
-        pm[0] = fmax3(pm[0], sc[nt][0], sc[nt][1]);
-        pm[1] = fmax3(pm[1], sc[nt][2], sc[nt][3]);
-      }
-      const float un = pow2i(min(-vexp, 127));
-      float nm[2];
+        for (int nt = 0; nt < 4; nt++) {
+          float w[2];
 #pragma unroll
-      for (int i2 = 0; i2 < 2; i2++) {
-        pm[i2] = fmaxf(pm[i2], __shfl_xor_sync(kFull, pm[i2], 1));
-        pm[i2] = fmaxf(pm[i2], __shfl_xor_sync(kFull, pm[i2], 2));
-        const float mn = fmaxf(m[i2], pm[i2] + ve);
-        const float al = m[i2] == mn ? 1.0f : ex2_approx(m[i2] - mn);  // 0 from -inf
-        m[i2] = mn;
-        nm[i2] = mn == -INFINITY ? 0.0f : kBoost + ve - mn;
-        l[i2] *= al;
+          for (int e = 0; e < 2; e++) {
+            w[e] = ex2_approx(fmaf(sc[nt][e], c0, nl[0])) + ex2_approx(fmaf(sc[nt][2 + e], c1, nl[1]));
+            w[e] += __shfl_xor_sync(kFull, w[e], 4);
+            w[e] += __shfl_xor_sync(kFull, w[e], 8);
+            w[e] += __shfl_xor_sync(kFull, w[e], 16);
+          }
+          if (g == (nt & 7)) {
+            float* dst = a.c.weight + static_cast<size_t>(md.unit) * kPage + (j0 & (kPage - 1)) + nt * 8 + t * 2;
 #pragma unroll
-        for (int d = 0; d < D / 8; d++) {
-          o[d][2 * i2] *= al;
-          o[d][2 * i2 + 1] *= al;
+            for (int e = 0; e < 2; e++) {
+              if (j0 + nt * 8 + t * 2 + e < len) {
+                if (a.accumulate) atomicAdd(dst + e, w[e]);  // a page may serve two sequences
+                else dst[e] = w[e];
+              }
+            }
+          }
         }
-      }
-      float rs[2] = {0.0f, 0.0f};
-      uint32_t pa[4][4];
+      } else {
+        const float ve = static_cast<float>(md.ve);
+        float pm[2];
+        pm[0] = fmax3(fmax3(sc[0][0], sc[0][1], sc[1][0]), fmax3(sc[1][1], sc[2][0], sc[2][1]),
+                      fmaxf(sc[3][0], sc[3][1]));
+        pm[1] = fmax3(fmax3(sc[0][2], sc[0][3], sc[1][2]), fmax3(sc[1][3], sc[2][2], sc[2][3]),
+                      fmaxf(sc[3][2], sc[3][3]));
+        bool grow = false;
 #pragma unroll
-      for (int nt = 0; nt < 8; nt++) {
-        const float y0 = ex2_approx(sc[nt][0] + nm[0]), y1 = ex2_approx(sc[nt][1] + nm[0]);
-        const float y2 = ex2_approx(sc[nt][2] + nm[1]), y3 = ex2_approx(sc[nt][3] + nm[1]);
-        rs[0] += y0 + y1;
-        rs[1] += y2 + y3;
-        const __half2 h0 = __floats2half2_rn(y0, y1), h1 = __floats2half2_rn(y2, y3);
-        pa[nt / 2][(nt & 1) * 2] = *reinterpret_cast<const uint32_t*>(&h0);
-        pa[nt / 2][(nt & 1) * 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
-      }
-      l[0] = fmaf(rs[0], un, l[0]);
-      l[1] = fmaf(rs[1], un, l[1]);
-      // O += P V: per 32 channels, 16 keys at a time
+        for (int i2 = 0; i2 < 2; i2++) {
+          pm[i2] = fmaxf(pm[i2], __shfl_xor_sync(kFull, pm[i2], 1));
+          pm[i2] = fmaxf(pm[i2], __shfl_xor_sync(kFull, pm[i2], 2));
+          pm[i2] = fmaf(pm[i2], i2 ? c1 : c0, ve);
+          grow = grow || pm[i2] > m[i2] + kLazy;
+        }
+        if (__any_sync(kFull, grow)) {
 #pragma unroll
-      for (int kk = 0; kk < 4; kk++) {
+          for (int i2 = 0; i2 < 2; i2++) {
+            const float mn = fmaxf(m[i2], pm[i2]);
+            const float al = m[i2] == mn ? 1.0f : ex2_approx(m[i2] - mn);  // 0 from -inf
+            m[i2] = mn;
+            l[i2] *= al;
 #pragma unroll
-        for (int d2 = 0; d2 < D / 32; d2++) {
-          uint32_t vr[4];  // keys 0-7 / 8-15 of two 16-channel chunks
-          ldsm4t(vb + swz<D>(kk * 16 + (lane & 15), d2 * 2 + (lane >> 4)), vr);
+            for (int d = 0; d < D / 8; d++) {
+              o[d][2 * i2] *= al;
+              o[d][2 * i2 + 1] *= al;
+            }
+          }
+        }
+        const float nm0 = m[0] == -INFINITY ? 0.0f : kBoost + ve - m[0];
+        const float nm1 = m[1] == -INFINITY ? 0.0f : kBoost + ve - m[1];
+        float rs[2] = {0.0f, 0.0f};
+        uint32_t pa[2][4];
 #pragma unroll
-          for (int c = 0; c < 2; c++) {
-            uint32_t e0, o0, e1, o1;
-            f8x4_to_f16(vr[2 * c], e0, o0);
-            f8x4_to_f16(vr[2 * c + 1], e1, o1);
-            mma16816(o[(d2 * 2 + c) * 2], pa[kk], e0, e1);
-            mma16816(o[(d2 * 2 + c) * 2 + 1], pa[kk], o0, o1);
+        for (int nt = 0; nt < 4; nt++) {
+          const float y0 = ex2_approx(fmaf(sc[nt][0], c0, nm0)), y1 = ex2_approx(fmaf(sc[nt][1], c0, nm0));
+          const float y2 = ex2_approx(fmaf(sc[nt][2], c1, nm1)), y3 = ex2_approx(fmaf(sc[nt][3], c1, nm1));
+          rs[0] += y0 + y1;
+          rs[1] += y2 + y3;
+          const __half2 h0 = __floats2half2_rn(y0, y1), h1 = __floats2half2_rn(y2, y3);
+          pa[nt / 2][(nt & 1) * 2] = *reinterpret_cast<const uint32_t*>(&h0);
+          pa[nt / 2][(nt & 1) * 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+        }
+        const float un = pow2i(min(-md.ve, 127));
+        l[0] = fmaf(rs[0], un, l[0]);
+        l[1] = fmaf(rs[1], un, l[1]);
+        // O += P V: per 32 channels, 16 keys at a time
+#pragma unroll
+        for (int kk = 0; kk < 2; kk++) {
+#pragma unroll
+          for (int d2 = 0; d2 < D / 32; d2++) {
+            uint32_t vr[4];  // keys 0-7 / 8-15 of two 16-channel chunks
+            ldsm4t(vb + swz<D>(kk * 16 + (lane & 15), d2 * 2 + (lane >> 4)), vr);
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+              uint32_t e0, o0, e1, o1;
+              f8x4_to_f16(vr[2 * c], e0, o0);
+              f8x4_to_f16(vr[2 * c + 1], e1, o1);
+              mma16816(o[(d2 * 2 + c) * 2], pa[kk], e0, e1);
+              mma16816(o[(d2 * 2 + c) * 2 + 1], pa[kk], o0, o1);
+            }
           }
         }
       }
     }
     __syncwarp();
-    if (lane == 0 && issued < mine) issue(issued++);
+    if (issued < mine) issue();
   }
   if (!ok) {  // a wait ran out (recorded): let the loads in flight land, then leave
     if (lane == 0)
@@ -336,6 +406,7 @@ __global__ void __launch_bounds__(kWarps * 32)
         drain_wait(&s.full[warp][i % kStages], (i / kStages) & 1, wc, kSiteDecDrain);
     __syncwarp();
   }
+  if constexpr (WEIGHTS) return;
   // row sums over the four lanes of a row
 #pragma unroll
   for (int i = 0; i < 2; i++) {
@@ -347,7 +418,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   __syncthreads();
   if (s.abort) return;
   float* part = reinterpret_cast<float*>(s.kv[warp][0][0]);
-  static_assert(kStages * 2 * kPage * D >= kDecRows * D * 4, "a warp's ring holds its partial rows");
+  static_assert(kStages * 2 * kHalf * D >= kDecRows * D * 4, "a warp's ring holds its partial rows");
 #pragma unroll
   for (int d = 0; d < D / 16; d++) {
     // tiles 2 d and 2 d + 1 hold channels 16 d + 4 t + {0, 2} and + {1, 3}
@@ -364,7 +435,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
   __syncthreads();
   const int nch = min(a.chunks, (runs.n + a.chunk_pages - 1) / a.chunk_pages);
-  constexpr size_t kWarpFloats = kStages * 2 * kPage * D / 4;
+  constexpr size_t kWarpFloats = kStages * 2 * kHalf * D / 4;
   for (int x = threadIdx.x; x < kDecRows * D / 2; x += kWarps * 32) {
     const int r = x / (D / 2), d = x % (D / 2) * 2;
     if (r0 + r >= r1) break;
@@ -443,191 +514,43 @@ __global__ void __launch_bounds__(128) k_cache_merge(const CacheAttnArgs a, int 
         ls > 0.0f ? (mx + log2f(ls)) * kLn2 : -INFINITY;
 }
 
-// ---------------------------------------------------------------- weights
+}  // namespace
 
-// w[key] (+)= sum over the query rows of exp(s - lse): scores as in the
-// attention kernel, with the row's statistics known.  A warp owns a page (its
-// keys are the columns of the score tiles, so a key's sum stays in one warp:
-// no order of atomics enters it), 16 keys of it at a time as fp16 fragments
-// in registers, over which all query rows of the block pass; the rows lie in
-// shared memory, 128 at a time.
-constexpr int kWgtWarps = 4;
-constexpr int kWgtRows = 128;
-
-template <int D>
-struct alignas(1024) WgtSmem {
-  uint8_t k[kWgtWarps][kPage * D];
-  __half q[kWgtRows][D + 16];
-  float2 row[kWgtRows];  // 2^e * scale * log2(e); lse * log2(e)
-  KeyRange kr[kWgtRows];
-  uint64_t full[kWgtWarps];
-  int abort;
-};
-
-template <int D>
-__global__ void __launch_bounds__(kWgtWarps * 32)
-    k_cache_weights(const __grid_constant__ CacheAttnMaps maps, const CacheAttnArgs a, int page_groups) {
-  extern __shared__ __align__(1024) uint8_t raw[];
-  if (smem_misaligned(raw, a.c.status)) return;
-  WgtSmem<D>& s = *reinterpret_cast<WgtSmem<D>*>(raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3;
-  const int bh = blockIdx.x / page_groups;
-  const int b = bh / a.c.Hkv, h = bh % a.c.Hkv;
-  const int len = seq_length(a.c, b), qn = query_len(a, b), rows = qn * a.G;
-  const int n_blk = (len + kPage - 1) / kPage;
-  int blk0 = static_cast<int>(blockIdx.x % page_groups) * kWgtWarps;
-  if (blk0 >= n_blk) return;
-  const long long off = static_cast<long long>(len) - qn;
-  if (threadIdx.x == 0) {
-    for (int w = 0; w < kWgtWarps; w++) mbar_init(&s.full[w], 1);
-    s.abort = 0;
-    fence_mbar_init();
-  }
-  __syncthreads();
-  const WaitCtx wc{a.budget, a.c.status, &s.abort};
-  int loads = 0;  // page loads of this warp so far: the barrier's phase
-  // one group of pages a block, more only where the sequence is longer than
-  // announced
-  for (; blk0 < n_blk; blk0 += page_groups * kWgtWarps) {
-    const int blk = blk0 + warp, j0 = blk * kPage;
-    int pg = -1;
-    if (blk < n_blk) pg = page_id(a.c, b, blk);
-    const bool mine = pg >= 0;
-    const size_t unit = static_cast<size_t>(mine ? pg : 0) * a.c.Hkv + h;
-    if (mine && lane == 0) {
-      mbar_arrive_expect_tx(&s.full[warp], kPage * D);
-      tma_load_3d(s.k[warp], &maps.k, &s.full[warp], 0, 0, static_cast<int>(unit));
-    }
-    const float ks = mine ? __ldg(a.c.k_scale + unit) : 0.0f;
-    const uint32_t kb = smem_u32(s.k[warp]);
-    float acc[8][2];  // keys 8 nt + 2 t, + 1
-#pragma unroll
-    for (int i = 0; i < 8; i++) acc[i][0] = acc[i][1] = 0.0f;
-    bool ok = __all_sync(kFull, !s.abort);
-    for (int rb = 0; rb < rows; rb += kWgtRows) {
-      const int nr = min(kWgtRows, rows - rb), nr16 = (nr + 15) / 16 * 16;
-      __syncthreads();
-      for (int r = warp; r < nr16; r += kWgtWarps) {
-        const float f = stage_row<D>(a, b, h, rb + r, rows, s.q[r], lane);
-        if (lane == 0) {
-          float l2 = INFINITY;  // a row that saw nothing, or is not there: weight 0
-          KeyRange k{0, 0, 0};
-          if (r < nr) {
-            const int rr = rb + r, tok = rr / a.G, head = h * a.G + rr % a.G;
-            const float v = a.lse_in[(static_cast<size_t>(b) * a.H + head) * a.Nq + tok];
-            if (v != -INFINITY) l2 = v * kLog2e;
-            k = key_range(a.mask, off + tok, len);
-          }
-          s.row[r] = make_float2(f * (a.scale * kLog2e), l2);
-          s.kr[r] = k;
-        }
-      }
-      __syncthreads();
-      if (!mine || !ok) continue;
-      if (rb == 0) {
-        ok = __all_sync(kFull, mbar_wait(&s.full[warp], loads & 1, wc, kSiteWgtPage));
-        if (!ok) continue;
-      }
-#pragma unroll 1
-      for (int n2 = 0; n2 < 4; n2++) {  // 16 keys
-        uint32_t kf[2][D / 16][2];
-#pragma unroll
-        for (int x = 0; x < 2; x++)
-#pragma unroll
-          for (int c4 = 0; c4 < D / 64; c4++) {
-            uint32_t r4[4];
-            ldsm4(kb + swz<D>((n2 * 2 + x) * 8 + (lane & 7), c4 * 4 + (lane >> 3)), r4);
-#pragma unroll
-            for (int c = 0; c < 4; c++) i8x4_to_f16(r4[c], kf[x][c4 * 4 + c][0], kf[x][c4 * 4 + c][1]);
-          }
-        float sum[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
-        for (int rt = 0; rt < nr16; rt += 16) {
-          float sc[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-#pragma unroll
-          for (int kk = 0; kk < D / 16; kk++) {
-            const uint2 x = *reinterpret_cast<const uint2*>(&s.q[rt + g][kk * 16 + t * 4]);
-            const uint2 y = *reinterpret_cast<const uint2*>(&s.q[rt + g + 8][kk * 16 + t * 4]);
-            const uint32_t qa[4] = {x.x, y.x, x.y, y.y};
-            mma16816(sc[0], qa, kf[0][kk][0], kf[0][kk][1]);
-            mma16816(sc[1], qa, kf[1][kk][0], kf[1][kk][1]);
-          }
-#pragma unroll
-          for (int i = 0; i < 2; i++) {
-            const float2 rw = s.row[rt + g + 8 * i];
-            const KeyRange k = s.kr[rt + g + 8 * i];
-            const float c = rw.x * ks;
-#pragma unroll
-            for (int x = 0; x < 2; x++)
-#pragma unroll
-              for (int e = 0; e < 2; e++) {
-                const int j = j0 + (n2 * 2 + x) * 8 + t * 2 + e;
-                const float y = ex2_approx(fmaf(sc[x][2 * i + e], c, -rw.y));
-                if (j < k.sink || (j >= k.lo && j < k.hi)) sum[x][e] += y;
-              }
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-          if (i == n2) {
-            acc[2 * i][0] += sum[0][0];
-            acc[2 * i][1] += sum[0][1];
-            acc[2 * i + 1][0] += sum[1][0];
-            acc[2 * i + 1][1] += sum[1][1];
-          }
-      }
-    }
-    if (!mine) continue;
-    if (lane == 0) drain_wait(&s.full[warp], loads & 1, wc, kSiteWgtDrain);
-    __syncwarp();
-    loads++;
-    if (!ok) continue;
-#pragma unroll
-    for (int i = 0; i < 8; i++)
-#pragma unroll
-      for (int e = 0; e < 2; e++) {
-        float v = acc[i][e];
-        v += __shfl_xor_sync(kFull, v, 4);
-        v += __shfl_xor_sync(kFull, v, 8);
-        v += __shfl_xor_sync(kFull, v, 16);
-        const int j = i * 8 + t * 2 + e;
-        if (g == 0 && j0 + j < len) {
-          float* w = a.c.weight + unit * kPage + j;
-          if (a.accumulate) atomicAdd(w, v);  // a page may serve two sequences
-          else *w = v;
-        }
-      }
-  }
+namespace {
+template <int D, bool WEIGHTS>
+cudaError_t prepare_one() {
+  return cudaFuncSetAttribute(k_cache_decode<D, WEIGHTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(sizeof(DecSmem<D>)));
 }
-
+template <int D, bool WEIGHTS>
+cudaError_t launch_one(const CacheAttnMaps& m, const CacheAttnArgs& a, int row_tiles, cudaStream_t s) {
+  const long long units = static_cast<long long>(a.c.B) * a.c.Hkv * row_tiles;
+  const unsigned grid = static_cast<unsigned>(units * a.chunks);
+  k_cache_decode<D, WEIGHTS><<<grid, kWarps * 32, sizeof(DecSmem<D>), s>>>(m, a, row_tiles);
+  return cudaGetLastError();
+}
 }  // namespace
 
 cudaError_t cache_prepare() {
-  cudaError_t e = cudaFuncSetAttribute(k_cache_decode<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(sizeof(DecSmem<128>)));
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(k_cache_decode<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(sizeof(DecSmem<64>)));
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(k_cache_weights<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(sizeof(WgtSmem<128>)));
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(k_cache_weights<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(sizeof(WgtSmem<64>)));
-  return e == cudaSuccess ? cache_prefill_prepare() : e;
+  cudaError_t e = prepare_one<128, false>();
+  if (e == cudaSuccess) e = prepare_one<64, false>();
+  if (e == cudaSuccess) e = prepare_one<128, true>();
+  if (e == cudaSuccess) e = prepare_one<64, true>();
+  if (e == cudaSuccess) e = cache_prefill_prepare();
+  if (e == cudaSuccess) e = cache_weights_prepare();
+  return e;
 }
 
 cudaError_t launch_cache_decode(const CacheAttnMaps& m, const CacheAttnArgs& a, cudaStream_t s) {
   const int row_tiles = (a.Nq * a.G + kDecRows - 1) / kDecRows;
-  const long long units = static_cast<long long>(a.c.B) * a.c.Hkv * row_tiles;
-  const unsigned grid = static_cast<unsigned>(units * a.chunks);
-  if (a.c.D == 128)
-    k_cache_decode<128><<<grid, kWarps * 32, sizeof(DecSmem<128>), s>>>(m, a, row_tiles);
-  else
-    k_cache_decode<64><<<grid, kWarps * 32, sizeof(DecSmem<64>), s>>>(m, a, row_tiles);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = a.c.D == 128 ? launch_one<128, false>(m, a, row_tiles, s)
+                                     : launch_one<64, false>(m, a, row_tiles, s);
   if (e != cudaSuccess || a.chunks == 1) return e;
   return launch_cache_merge(a, row_tiles, kDecRows, s);
+}
+
+cudaError_t launch_cache_weights_few(const CacheAttnMaps& m, const CacheAttnArgs& a, cudaStream_t s) {
+  return a.c.D == 128 ? launch_one<128, true>(m, a, 1, s) : launch_one<64, true>(m, a, 1, s);
 }
 
 cudaError_t launch_cache_merge(const CacheAttnArgs& a, int row_tiles, int tile_rows, cudaStream_t s) {
@@ -635,16 +558,6 @@ cudaError_t launch_cache_merge(const CacheAttnArgs& a, int row_tiles, int tile_r
   const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
   if (a.c.D == 128) k_cache_merge<128><<<grid, 128, 0, s>>>(a, row_tiles, tile_rows);
   else k_cache_merge<64><<<grid, 128, 0, s>>>(a, row_tiles, tile_rows);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_cache_weights(const CacheAttnMaps& m, const CacheAttnArgs& a, cudaStream_t s) {
-  const int groups = a.chunks;  // page groups of kWgtWarps pages, set by the caller
-  const unsigned grid = static_cast<unsigned>(static_cast<long long>(a.c.B) * a.c.Hkv * groups);
-  if (a.c.D == 128)
-    k_cache_weights<128><<<grid, kWgtWarps * 32, sizeof(WgtSmem<128>), s>>>(m, a, groups);
-  else
-    k_cache_weights<64><<<grid, kWgtWarps * 32, sizeof(WgtSmem<64>), s>>>(m, a, groups);
   return cudaGetLastError();
 }
 

@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 
 #include "cache.cuh"
+#include "sm100.cuh"
 
 namespace sage {
 
@@ -76,6 +77,103 @@ template <int D>
 __device__ __forceinline__ float stage_row(const CacheAttnArgs& a, int b, int h, int r, int rows,
                                            __half* dst, int lane) {
   return stage_row_as<D>(a, b, h, r, rows, lane, [&](int ch, float x) { dst[ch] = __float2half_rn(x); });
+}
+
+// ---------------------------------------------------------------- tcgen05 operands
+
+// fp16 operand tiles: [D / 64][128 rows][128 bytes], 128-byte swizzle.  Byte
+// offset of 16-byte chunk `ch` (8 channels) of row r.
+__device__ __forceinline__ uint32_t op_off(int r, int ch) {
+  return static_cast<uint32_t>((ch >> 3) * (128 * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+}
+// Instruction descriptor of kind::f16 with f16 operands, fp32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+// D[tmem] = A B^T over D channels of two K-major operand tiles.
+template <int D>
+__device__ __forceinline__ void mma_rows(uint32_t tmem, uint32_t a, uint32_t b, uint32_t idesc) {
+#pragma unroll
+  for (int kk = 0; kk < D / 16; kk++) {
+    const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
+    mma_f16_ss(tmem, smem_desc_kmajor(a + off, 128), smem_desc_kmajor(b + off, 128), idesc, kk > 0);
+  }
+}
+
+// Eight channels of the query as fp32.
+__device__ __forceinline__ void load_q8(const CacheAttnArgs& a, size_t i, float (&f)[8]) {
+  if (a.q_vec) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + i));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      if (a.type == kTypeBf16) {
+        f[2 * j] = __uint_as_float(w[j] << 16);
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      } else {
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+        f[2 * j] = x.x;
+        f[2 * j + 1] = x.y;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; j++) f[j] = load_q(a.q, a.type, i + j);
+  }
+}
+
+// Query rows r0 .. r0 + n - 1 (n <= 128; those from `rows` on become zero) to
+// an fp16 operand tile; factor[i] = the row's power of two.  By NT threads,
+// `tid` in [0, NT); n * D / 8 must be a multiple of 32.
+template <int D, int NT>
+__device__ __forceinline__ void stage_rows(const CacheAttnArgs& a, int b, int h, int r0, int rows, int n,
+                                           uint8_t* tile, float* factor, int tid) {
+  constexpr int CH = D / 8, UN = 4;
+  for (int i0 = tid; i0 < n * CH; i0 += NT * UN) {
+    float f[UN][8];
+#pragma unroll
+    for (int u = 0; u < UN; u++) {
+      const int i = i0 + u * NT, r = r0 + i / CH;
+      if (i < n * CH && r < rows) {
+        load_q8(a, a.qb * b + a.qh * (static_cast<size_t>(h) * a.G + r % a.G) + a.qn * (r / a.G) + i % CH * 8,
+                f[u]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; e++) f[u][e] = 0.0f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < UN; u++) {
+      const int i = i0 + u * NT;
+      if (i - (tid & 31) >= n * CH) break;  // whole warps
+      float m = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(f[u][e]));
+#pragma unroll
+      for (int o = CH / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const int p = row_power(m);
+      const float inv = pow2i(-p);
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const __half2 x = __floats2half2_rn(f[u][2 * j] * inv, f[u][2 * j + 1] * inv);
+        w[j] = *reinterpret_cast<const uint32_t*>(&x);
+      }
+      *reinterpret_cast<uint4*>(tile + op_off(i / CH, i % CH)) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (i % CH == 0) factor[i / CH] = pow2i(p);
+    }
+  }
+}
+
+// 16 codes of a row's chunk pair 2 c, 2 c + 1.  Lanes of the upper half of a
+// 128-channel row store their chunks in the other order, so that eight lanes
+// always hit eight different banks.
+template <int D>
+__device__ __forceinline__ void store_pair(uint8_t* tile, int row, int c, const uint32_t (&o)[8]) {
+  const int sw = D == 128 ? c >> 2 : 0;
+  const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+  *reinterpret_cast<uint4*>(tile + op_off(row, 2 * c + sw)) = sw ? hi : lo;
+  *reinterpret_cast<uint4*>(tile + op_off(row, 2 * c + (sw ^ 1))) = sw ? lo : hi;
 }
 
 __device__ __forceinline__ int query_len(const CacheAttnArgs& a, int b) {

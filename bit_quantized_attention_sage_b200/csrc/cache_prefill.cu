@@ -56,20 +56,12 @@ struct alignas(1024) PreSmem {
   int abort;
 };
 
-// Byte offset of 16-byte chunk `ch` (8 fp16 channels) of row r.
-__device__ __forceinline__ uint32_t op_off(int r, int ch) {
-  return static_cast<uint32_t>((ch >> 3) * (128 * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
-}
-
 // MN-major operand of 16-bit elements, 128-byte swizzle: N in runs of 64
 // (128 bytes), `lbo` bytes from run to run; groups of 8 K rows 1024 bytes
 // apart.
 __device__ __forceinline__ uint64_t desc_mn16(uint32_t saddr, uint32_t lbo) {
   return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(lbo >> 4) << 16) |
          (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
-constexpr uint32_t idesc_f16(int M, int N) {
-  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 // D[tmem] (+)= A[tmem] B[smem], f16 operands, fp32 accumulator.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
@@ -123,9 +115,7 @@ __device__ __forceinline__ void load_codes(uint4 (&r)[D / 16], const uint8_t* co
                           codes + (static_cast<size_t>(x.unit) * kPage + (row & 63)) * D + c * 16));
   }
 }
-// 16 codes to 16 fp16 values, two chunks of a row.  Lanes of the upper half
-// of a 128-channel row store their chunks in the other order, so that eight
-// lanes always hit eight different banks.
+// 16 codes to 16 fp16 values, two chunks of a row.
 template <int D, bool VALUES>
 __device__ __forceinline__ void store_codes(uint8_t* tile, const uint4 (&r)[D / 16], const Group (&g)[2],
                                             int len, int tid) {
@@ -149,10 +139,7 @@ __device__ __forceinline__ void store_codes(uint8_t* tile, const uint4 (&r)[D / 
 #pragma unroll
       for (int j = 0; j < 4; j++) i8x4_to_f16(w[j], o[2 * j], o[2 * j + 1]);
     }
-    const int sw = D == 128 ? c >> 2 : 0;
-    const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-    *reinterpret_cast<uint4*>(tile + op_off(row, 2 * c + sw)) = sw ? hi : lo;
-    *reinterpret_cast<uint4*>(tile + op_off(row, 2 * c + (sw ^ 1))) = sw ? lo : hi;
+    store_pair<D>(tile, row, c, o);
   }
 }
 
@@ -189,13 +176,7 @@ __device__ __forceinline__ void convert(PreSmem<D>& s, const CacheAttnArgs& a, c
 
 template <int D>
 __device__ __forceinline__ void issue_qk(PreSmem<D>& s, int w, uint32_t tS, int st) {
-  constexpr uint32_t id = idesc_f16(BM, BN);
-  const uint32_t qa = smem_u32(s.q[w]), ka = smem_u32(s.k[st]);
-#pragma unroll
-  for (int kk = 0; kk < D / 16; kk++) {
-    const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-    mma_f16_ss(tS, smem_desc_kmajor(qa + off, 128), smem_desc_kmajor(ka + off, 128), id, kk > 0);
-  }
+  mma_rows<D>(tS, smem_u32(s.q[w]), smem_u32(s.k[st]), idesc_f16(BM, BN));
 }
 template <int D>
 __device__ __forceinline__ void issue_pv(PreSmem<D>& s, uint32_t tP, uint32_t tO, int st, bool first) {
@@ -263,7 +244,7 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
   const bool valid = row < r1;
   const uint32_t lo = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t tS = tmem + t * BN + lo, tO = tmem + 2 * BN + t * D + lo;
-  const float f = s.rowf[r];
+  const float f = s.rowf[r] * (a.scale * kLog2e);
   KeyRange kr{0, 0, 0};
   if (valid) kr = key_range(a.mask, off + row / a.G, len);
   float m = -INFINITY, l = 0.0f;
@@ -483,14 +464,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_prefill(const CacheAttnAr
     tmem_alloc(&s.tmem_base, 512);
     tmem_relinquish();
   }
-  // query rows to fp16 operands, a warp a row
-  for (int r = warp; r < tiles * BM; r += kThreads / 32) {
-    uint8_t* tile = s.q[r / BM];
-    const float f = stage_row_as<D>(a, b, h, r0 + r, r1, lane, [&](int ch, float x) {
-      *reinterpret_cast<__half*>(tile + op_off(r % BM, ch / 8) + (ch % 8) * 2) = __float2half_rn(x);
-    });
-    if (lane == 0) s.rowf[r] = f * (a.scale * kLog2e);
-  }
+  for (int t = 0; t < tiles; t++)
+    stage_rows<D, kThreads>(a, b, h, r0 + t * BM, r1, BM, s.q[t], s.rowf + t * BM, threadIdx.x);
   // a page id that is none is recorded once, by the first range
   if (chunk == 0)
     for (int j = threadIdx.x; j < runs.n; j += kThreads) (void)page_id(a.c, b, runs.page(j));
