@@ -60,11 +60,13 @@ sage_status mask_of(int mask, int block, int win, int sink, CacheMask* m) {
   return SAGE_OK;
 }
 
-// KV ranges of an attention call: pages a range, ranges, floats of workspace.
+// How an attention call is cut, and the floats of its partial results.
 struct Plan {
   bool prefill;  // tcgen05 kernel, else the mma.sync one
-  int row_tiles, chunk_pages, chunks;
-  size_t rows, ws;
+  int chunk_pages, chunks, whole;
+  long long blocks;
+  size_t rows;   // of partial results
+  size_t ws;
 };
 // Pages that one query tile of `tile_tokens` tokens visits at most.
 int visited_pages(const CacheMask& m, int max_len, int tile_tokens) {
@@ -73,21 +75,29 @@ int visited_pages(const CacheMask& m, int max_len, int tile_tokens) {
   const long long win = static_cast<long long>(m.win) * m.block + m.block + tile_tokens;
   return static_cast<int>(std::min(pages, (m.sink + kPage - 1ll) / kPage + win / kPage + 3));
 }
-// Rows from which a query tile goes to the tcgen05 kernel.
-constexpr long long kPrefillRows = 33;
+// Blocks that share `pages` pages of every head: two an SM, with eight pages
+// (four tiles a warp) each at least; a block a head where a head has no more.
+void plan_decode(long long units, int pages, int sms, int* chunks, int* whole) {
+  *whole = pages <= 8;
+  *chunks = static_cast<int>(*whole ? units : std::min(2ll * sms, (units * pages + 7) / 8));
+}
 
 Plan plan_of(const CacheMask& m, int B, int Hkv, int G, int Nq, int D, int max_len, int sms) {
   Plan p{};
   const long long qrows = static_cast<long long>(Nq) * G;
-  p.prefill = qrows >= kPrefillRows;
-  const int tile = p.prefill ? kPreRows : kDecRows;
-  p.row_tiles = static_cast<int>((qrows + tile - 1) / tile);
-  const long long units = static_cast<long long>(B) * Hkv * p.row_tiles;
-  const int pages = visited_pages(m, max_len, (tile + G - 1) / G + 1);
-  long long cp = std::max(4, pages);
-  if (p.prefill) {
+  p.prefill = qrows > kDecRows;
+  if (!p.prefill) {
+    const long long units = static_cast<long long>(B) * Hkv;
+    plan_decode(units, visited_pages(m, max_len, Nq), sms, &p.chunks, &p.whole);
+    p.blocks = p.chunks;
+    p.rows = p.whole ? 0 : 2ull * p.chunks * decode_tile_rows(Nq, G);
+  } else {
+    const int row_tiles = static_cast<int>((qrows + kPreRows - 1) / kPreRows);
+    const long long units = static_cast<long long>(B) * Hkv * row_tiles;
+    const int pages = visited_pages(m, max_len, (kPreRows + G - 1) / G + 1);
     // one block an SM: the fewest ranges whose last round of blocks leaves at
     // most a tenth of the SMs' time unused, of 16 pages at least
+    long long cp = std::max(4, pages);
     double best = 0.0;
     for (long long n = 1; n <= 64 && (n == 1 || pages / n >= 16); n++) {
       const double rounds = static_cast<double>(units * n) / sms;
@@ -98,19 +108,12 @@ Plan plan_of(const CacheMask& m, int B, int Hkv, int G, int Nq, int D, int max_l
       }
       if (used >= 0.9) break;
     }
-    cp = std::max(4ll, cp);
-  } else {
-    // Two blocks an SM: ranges so short that the blocks come in about four
-    // rounds (uneven sequences then even out), but of four pages at least,
-    // two half pages for each warp of the block.
-    const long long want = std::max(1ll, 8ll * sms / std::max(1ll, units));
-    cp = std::max(4ll, ((pages + want - 1) / want + 1) / 2 * 2);
+    p.chunk_pages = static_cast<int>(std::max(4ll, cp));
+    p.chunks = static_cast<int>(std::max(1ll, (pages + p.chunk_pages - 1ll) / p.chunk_pages));
+    p.blocks = units * p.chunks;
+    p.rows = p.chunks > 1 ? static_cast<size_t>(units) * kPreRows * p.chunks : 0;
   }
-  while ((pages + cp - 1) / cp > kCacheChunksMax) cp *= 2;
-  p.chunk_pages = static_cast<int>(cp);
-  p.chunks = static_cast<int>(std::max(1ll, (pages + cp - 1) / cp));
-  p.rows = static_cast<size_t>(B) * Hkv * p.row_tiles * tile;
-  p.ws = p.chunks > 1 ? p.rows * p.chunks * (static_cast<size_t>(D) + 2) * 4 : 0;
+  p.ws = p.rows * (static_cast<size_t>(D) + 2) * 4;
   return p;
 }
 int sm_count() {
@@ -300,7 +303,7 @@ SAGE_EXPORT sage_status sage_cache_attn(const sage_kv_cache* cache, const sage_k
   const int sms = sm_count();
   if (!sms) return SAGE_ERR_CUDA;
   const Plan p = plan_of(a.mask, seqs->B, cache->heads, a.G, a.Nq, cache->D, query->max_len, sms);
-  if (static_cast<long long>(p.rows / kDecRows) * p.chunks > (1ll << 31) - 1) return SAGE_ERR_UNSUPPORTED;
+  if (p.blocks > (1ll << 31) - 1) return SAGE_ERR_UNSUPPORTED;
   if (p.ws && (!al(workspace, 16) || workspace_bytes < p.ws)) return SAGE_ERR_INVALID_ARG;
   a.o = out;
   a.ob = o_strides[0];
@@ -310,7 +313,8 @@ SAGE_EXPORT sage_status sage_cache_attn(const sage_kv_cache* cache, const sage_k
   a.chunk_pages = p.chunk_pages;
   a.chunks = p.chunks;
   a.part_o = static_cast<float*>(workspace);
-  a.part_ml = a.part_o + p.rows * p.chunks * cache->D;
+  a.whole = p.whole;
+  a.part_ml = a.part_o + p.rows * cache->D;
   if (p.prefill) return status_of(launch_cache_prefill(a, static_cast<cudaStream_t>(stream)));
   CacheAttnMaps maps;
   if (!maps_of(cache, &maps)) return SAGE_ERR_CUDA;
@@ -330,16 +334,18 @@ SAGE_EXPORT sage_status sage_cache_weights(const sage_kv_cache* cache, const sag
   if (!sms) return SAGE_ERR_CUDA;
   const int pages = std::max(1, (query->max_len + kPage - 1) / kPage);
   const long long units = static_cast<long long>(seqs->B) * cache->heads;
-  // Two blocks an SM, each with query rows to stage before its first key: as
-  // many keys a block as leave four rounds of blocks (uneven sequences then
-  // even out).
-  const long long want = std::max(1ll, 8ll * sms / units);
-  a.chunk_pages = static_cast<int>(((pages + want - 1) / want + 3) / 4 * 4);
-  a.chunks = (pages + a.chunk_pages - 1) / a.chunk_pages;
-  if (units * a.chunks > (1ll << 31) - 1) return SAGE_ERR_UNSUPPORTED;
-  // up to 16 query rows the keys stream past one mma.sync tile
-  if (static_cast<long long>(a.Nq) * a.G > kDecRows)
+  if (static_cast<long long>(a.Nq) * a.G > kDecRows) {
+    // Two blocks an SM, each with query rows to stage before its first key:
+    // ranges that leave two rounds of blocks.
+    const long long want = std::max(1ll, 4ll * sms / units);
+    a.chunk_pages = static_cast<int>(((pages + want - 1) / want + 3) / 4 * 4);
+    a.chunks = (pages + a.chunk_pages - 1) / a.chunk_pages;
+    if (units * a.chunks > (1ll << 31) - 1) return SAGE_ERR_UNSUPPORTED;
     return status_of(launch_cache_weights(a, static_cast<cudaStream_t>(stream)));
+  }
+  // up to 16 query rows the keys stream past one mma.sync tile
+  if (units > (1ll << 31) - 1) return SAGE_ERR_UNSUPPORTED;
+  plan_decode(units, pages, sms, &a.chunks, &a.whole);
   CacheAttnMaps maps;
   if (!maps_of(cache, &maps)) return SAGE_ERR_CUDA;
   return status_of(launch_cache_weights_few(maps, a, static_cast<cudaStream_t>(stream)));

@@ -207,17 +207,20 @@ struct CacheAttnArgs {
   float* lse;        // f32 [B][H][Nq] or null
   const float* lse_in;
   int accumulate;    // cache_weights: add to the weights, or overwrite them
-  // KV ranges (cache_attn: with partial results)
-  int chunk_pages, chunks;
+  // how the keys are cut: `chunks` ranges of `chunk_pages` pages of each query
+  // tile; for at most 16 rows `chunks` blocks with equal shares of all pages,
+  // or (`whole`) a block for every head
+  int chunk_pages, chunks, whole;
   float *part_o, *part_ml;
   long long budget;
 };
 cudaError_t cache_prepare();
-// rows of a query tile of the two attention kernels
+// rows of a query tile of the two attention kernels (the first: at most; one
+// of eight rows where they suffice)
 constexpr int kDecRows = 16, kPreRows = 256;
+inline int decode_tile_rows(long long Nq, int G) { return Nq * G <= 8 ? 8 : kDecRows; }
 cudaError_t cache_prefill_prepare();
 cudaError_t launch_cache_prefill(const CacheAttnArgs& a, cudaStream_t s);
-cudaError_t launch_cache_merge(const CacheAttnArgs& a, int row_tiles, int tile_rows, cudaStream_t s);
 cudaError_t launch_cache_decode(const CacheAttnMaps& m, const CacheAttnArgs& a, cudaStream_t s);
 cudaError_t cache_weights_prepare();
 cudaError_t launch_cache_weights_few(const CacheAttnMaps& m, const CacheAttnArgs& a, cudaStream_t s);

@@ -5,11 +5,14 @@
 // The query heads that share a key head are rows of one tile: row r of
 // (sequence b, key head h) is token r / G, head h G + r % G.
 //
-// Scores.  Q goes to fp16 with a power of two per row (its largest element
-// lands in [2^14, 2^15)): exact for bf16 and fp16 inputs down to 2^-31 of the
-// row's maximum.  int8 key codes are exact in fp16, so the products are exact
-// and only the fp32 accumulation rounds; the page's key scale, the row's
-// power and log2(e) * softmax scale multiply the sum.
+// Scores.  A query row becomes 22-bit integers v (a power of two puts its
+// largest element into [2^21, 2^22)), exact for bf16 down to 2^-14 and fp16
+// down to 2^-11 of the row's maximum and off by at most 2^-22 of it below, and
+// those three int8 limbs, so Q K^T is three int8 products on the key codes as
+// they lie in the cache: exact int32, no conversion of the codes (five
+// instructions per four of them to fp16, half of the loop's issue slots).
+// The limbs join in fp32, rounded once; the page's key scale, the row's power
+// and log2(e) * softmax scale multiply the sum.
 // Probabilities.  y = 2^(t + e - M + 7), t the score in log2 units, e the
 // page's value exponent, M a reference maximum of t + e that follows the
 // running one in steps of at least 2^8: y <= 2^15, and fp16(y) is off by at
@@ -24,8 +27,9 @@
 // so no barrier joins the warps until the end.  Page ids, key scales and
 // value exponents of a warp's next 32 half pages are fetched at once, one a
 // lane; taken one by one inside the loop, their three dependent loads cost
-// more than the tile.  16-row tiles on mma.sync (a sixteenth used for one
-// row) keep the issue slots at about a third of the load time; a 128-row
+// more than the tile.  Keys are the 16 rows of the mma.sync tiles and query
+// rows their 8 columns (S^T = K Q^T, O^T = V^T P^T): one head group of up to
+// eight wastes no column, and a product covers 256 bytes of codes.  A 128-row
 // tcgen05 tile would need its codes converted through shared memory first.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -67,6 +71,20 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
+// D (int32 16x8) += A (int8 16x32) B (int8 32x8)
+__device__ __forceinline__ void mma16832(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Transpose of an 8x8 matrix of 16-bit elements held by the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
 // D (fp32 16x8) += A (fp16 16x16) B (fp16 16x8)
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -103,84 +121,168 @@ struct TileMeta {
   int unit;  // (page, head)
 };
 
+struct PlaceSmem {
+  long long sum[kWarps];
+  long long before;
+  int b;
+};
 template <int D>
 struct alignas(1024) DecSmem {
   uint8_t kv[kWarps][kStages][2][kHalf * D];  // TMA tiles: K, V
-  __half q[kDecRows][D + 16];                 // padded: 8-byte reads of 4 rows on different banks
-  float rowf[kDecRows];                       // 2^e * scale * log2(e) of each row
+  int8_t q[3][kDecRows][D];                   // limbs of the query rows, low to high
+  float rowf[kDecRows];                       // power of two * scale * log2(e) of each row
   float ml[kWarps][kDecRows][2];
   TileMeta meta[kWarps][kStages];
+  PlaceSmem place;
   uint64_t full[kWarps][kStages];
   int abort;
 };
 
-struct TileId {
-  int b, h, rt, chunk;
-};
-__device__ __forceinline__ TileId tile_id(const CacheAttnArgs& a, int row_tiles) {
-  // row tiles fastest (they read the same pages), then KV ranges
-  unsigned i = blockIdx.x;
-  TileId t;
-  t.rt = i % row_tiles;
-  i /= row_tiles;
-  t.chunk = i % a.chunks;
-  i /= a.chunks;
-  t.h = i % a.c.Hkv;
-  t.b = i / a.c.Hkv;
-  return t;
-}
-
-// Two neighbouring channels of one output row.
-__device__ __forceinline__ void store_o2(const CacheAttnArgs& a, size_t i, float x, float y) {
-  if (a.type == kTypeBf16) {
-    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.o) + i;
-    p[0] = __float2bfloat16_rn(x);
-    p[1] = __float2bfloat16_rn(y);
-  } else {
-    __half* p = static_cast<__half*>(a.o) + i;
-    p[0] = __float2half_rn(x);
-    p[1] = __float2half_rn(y);
+// The first n query rows (from `rows` on: zero) as limbs.
+template <int D>
+__device__ __forceinline__ void stage_limbs(DecSmem<D>& s, const CacheAttnArgs& a, int b, int h, int rows,
+                                            int n) {
+  constexpr int CH = D / 8;
+  for (int i = threadIdx.x; i < n * CH; i += kWarps * 32) {
+    const int r = i / CH, c = i % CH;
+    float f[8];
+    if (r < rows) {
+      load_q8(a, a.qb * b + a.qh * (static_cast<size_t>(h) * a.G + r % a.G) + a.qn * (r / a.G) + c * 8, f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; e++) f[e] = 0.0f;
+    }
+    float m = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(f[e]));
+#pragma unroll
+    for (int o = CH / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    const int p = max(row_power(m) - 7, -126);  // m 2^-p in [2^21, 2^22)
+    const float inv = pow2i(-p);
+    uint32_t w[3][2] = {{0u, 0u}, {0u, 0u}, {0u, 0u}};
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+      int v = __float2int_rn(f[e] * inv);
+#pragma unroll
+      for (int x = 0; x < 3; x++) {
+        const int lo = static_cast<int8_t>(v);
+        w[x][e >> 2] |= static_cast<uint32_t>(lo & 0xFF) << (8 * (e & 3));
+        v = (v - lo) >> 8;
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 3; x++)
+      *reinterpret_cast<uint2*>(&s.q[x][r][c * 8]) = make_uint2(w[x][0], w[x][1]);
+    if (c == 0) s.rowf[r] = pow2i(p) * (a.scale * kLog2e);
   }
 }
 
-// WEIGHTS: instead of attending, w[key] (+)= sum over the tile's rows of
-// exp(s - lse), with the rows' lse given (at most 16 rows: one tile).
-template <int D, bool WEIGHTS>
-__global__ void __launch_bounds__(kWarps * 32, 2)
-    k_cache_decode(const __grid_constant__ CacheAttnMaps maps, const CacheAttnArgs a, int row_tiles) {
-  extern __shared__ __align__(1024) uint8_t raw[];
-  if (smem_misaligned(raw, a.c.status)) return;
-  DecSmem<D>& s = *reinterpret_cast<DecSmem<D>*>(raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3;
-  const TileId id = tile_id(a, row_tiles);
-  const int len = seq_length(a.c, id.b), qn = query_len(a, id.b);
-  const int rows = qn * a.G, r0 = id.rt * kDecRows;
-  if (r0 >= rows && !WEIGHTS) return;
-  const int r1 = min(rows, r0 + kDecRows);
-  const long long off = static_cast<long long>(len) - qn;  // position of token 0
-  PageRuns runs;
+// ---------------------------------------------------------------- shares of the work
+//
+// The work of a call is a line of pages: sequences in order, in each the key
+// heads, in each head the pages its rows visit.  Block c of C takes the c-th
+// of C equal stretches of it, so uneven sequences cost no tail and a block's
+// start (its first dependent loads and tile, some 4 us) is paid once, not
+// once for every range of a fixed length.  A stretch cuts at most two heads:
+// the partial result of a head begun by an earlier block goes to slot 2 c,
+// that of one a later block finishes to slot 2 c + 1.
+
+// Pages of sequence b that count (0: nothing to do; at least 1 where rows
+// have to be written).
+template <bool WEIGHTS>
+__device__ __forceinline__ PageRuns seq_runs(const CacheAttnArgs& a, int b, int len, int qn) {
+  PageRuns r;
   if constexpr (WEIGHTS) {  // every page: those that no row sees get 0
-    runs.n = runs.ns = (len + kPage - 1) / kPage;
-    runs.gap = 0;
+    r.n = r.ns = (len + kPage - 1) / kPage;
+    r.gap = 0;
   } else {
-    runs = page_runs(a.mask, off + r0 / a.G, off + (r1 - 1) / a.G, len);
+    const long long off = static_cast<long long>(len) - qn;
+    r = page_runs(a.mask, off, off + max(qn - 1, 0), len);
   }
-  // the last range takes whatever a sequence longer than announced adds
-  const int p0 = id.chunk * a.chunk_pages;
-  const int p1 = id.chunk == a.chunks - 1 ? runs.n : min(runs.n, p0 + a.chunk_pages);
-  // range 0 also serves an empty sequence
-  if (p0 >= runs.n && (WEIGHTS || id.chunk > 0)) return;
+  return r;
+}
+template <bool WEIGHTS>
+__device__ __forceinline__ int seq_work(const CacheAttnArgs& a, int b) {
+  const int len = seq_length(a.c, b), qn = query_len(a, b);
+  if (WEIGHTS) return seq_runs<WEIGHTS>(a, b, len, qn).n;
+  return qn == 0 ? 0 : max(1, seq_runs<WEIGHTS>(a, b, len, qn).n);
+}
 
-  if (lane == 0) {
-    for (int i = 0; i < kStages; i++) mbar_init(&s.full[warp][i], 1);
-    if (warp == 0) s.abort = 0;
-    fence_mbar_init();
+__device__ __forceinline__ long long share_start(long long work, int c, int n) { return work * c / n; }
+// The block whose stretch holds position x.
+__device__ __forceinline__ int share_of(long long work, long long x, int n) {
+  return static_cast<int>(((x + 1) * n - 1) / work);
+}
+
+struct Place {
+  long long work;    // of the whole call, pages
+  long long before;  // pages of one head before sequence b
+  int b;
+};
+// By a block of kWarps * 32 threads: the whole work, and the sequence that
+// position x (a function of the work) lies in.
+template <bool WEIGHTS, typename X>
+__device__ __forceinline__ Place locate(PlaceSmem& s, const CacheAttnArgs& a, X x) {
+  constexpr int NT = kWarps * 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int first = tid < a.c.B ? seq_work<WEIGHTS>(a, tid) : 0;
+  long long mine = first;
+  for (int b = tid + NT; b < a.c.B; b += NT) mine += seq_work<WEIGHTS>(a, b);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(kFull, mine, o);
+  if (lane == 0) s.sum[warp] = mine;
+  if (tid == 0) s.b = a.c.B;
+  __syncthreads();
+  Place p{0, 0, 0};
+#pragma unroll
+  for (int w = 0; w < kWarps; w++) p.work += s.sum[w];
+  p.work *= a.c.Hkv;
+  const long long at = x(p.work);
+  long long base = 0;  // of the 128 sequences from b0 on
+  for (int b0 = 0; b0 < a.c.B; b0 += NT) {
+    const int n = b0 == 0 ? first : b0 + tid < a.c.B ? seq_work<WEIGHTS>(a, b0 + tid) : 0;
+    long long run = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(kFull, run, o);
+      if (lane >= o) run += v;
+    }
+    __syncthreads();
+    if (lane == 31) s.sum[warp] = run;
+    __syncthreads();
+    long long all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) {
+      if (w < warp) run += s.sum[w];
+      all += s.sum[w];
+    }
+    if ((base + run - n) * a.c.Hkv <= at && at < (base + run) * a.c.Hkv) {
+      s.b = b0 + tid;
+      s.before = base + run - n;
+    }
+    base += all;
+    if (base * a.c.Hkv > at) break;
   }
   __syncthreads();
-  const WaitCtx wc{a.budget, a.c.status, &s.abort};
-  // this warp's half pages: warp, warp + kWarps, ... of the range's
-  const int halves = max(0, 2 * (p1 - p0));
+  p.b = s.b;
+  p.before = s.before;
+  return p;
+}
+
+
+// One head's pages [p0, p1) (of the runs its rows visit): attention, or the
+// weights.  `seen` counts the warp's tiles so far (the ring's phase).
+template <int D, int NT, bool WEIGHTS>
+__device__ __forceinline__ void decode_head(DecSmem<D>& s, const CacheAttnMaps& maps, const CacheAttnArgs& a,
+                                            int b, int h, int len, int qn, const PageRuns& runs, int p0,
+                                            int p1, int np, int& seen, const WaitCtx& wc) {
+  constexpr int ROWS = 8 * NT;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int rows = qn * a.G;
+  const long long off = static_cast<long long>(len) - qn;  // position of token 0
+  // this warp's half pages: warp, warp + kWarps, ... of the stretch's
+  const int halves = 2 * (min(p1, runs.n) - p0);
   const int mine = warp < halves ? (halves - warp + kWarps - 1) / kWarps : 0;
   TileMeta next{0.0f, 0, -1, 0};  // lane's tile of the current 32
   int issued = 0;
@@ -190,19 +292,19 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       next = TileMeta{0.0f, 0, -1, 0};
       if (q < halves) {
         const int blk = runs.page(p0 + q / 2);
-        const int pg = page_id(a.c, id.b, blk);
-        if (pg >= 0) {
-          next.unit = pg * a.c.Hkv + id.h;
-          next.j0 = blk * kPage + (q & 1) * kHalf;
+        const int pg = page_id(a.c, b, blk);
+        const int j0 = blk * kPage + (q & 1) * kHalf;
+        if (pg >= 0 && j0 < len) {  // else: no page, or the half behind the end
+          next.unit = pg * a.c.Hkv + h;
+          next.j0 = j0;
           next.ks = __ldg(a.c.k_scale + next.unit);
           if (!WEIGHTS) next.ve = __ldg(a.c.v_exp + next.unit);
         }
       }
     }
     if (lane == (issued & 31)) {
-      const int st = issued % kStages;
+      const int st = (seen + issued) % kStages;
       uint64_t* bar = &s.full[warp][st];
-      if (next.j0 >= len) next.j0 = -1;  // the half behind the end
       s.meta[warp][st] = next;
       if (next.j0 < 0) {
         mbar_arrive(bar);  // nothing to load
@@ -216,50 +318,64 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     issued++;
   };
   while (issued < min(mine, kStages)) issue();
-  for (int r = warp; r < kDecRows; r += kWarps) {
-    const float f = stage_row<D>(a, id.b, id.h, r0 + r, r1, s.q[r], lane);
-    if (lane == 0) s.rowf[r] = f * (a.scale * kLog2e);
-  }
+  stage_limbs<D>(s, a, b, h, rows, ROWS);
   __syncthreads();
-  // A fragments of Q: k slots 2t, 2t + 1, 2t + 8, 2t + 9 of step kk are
-  // channels 16 kk + 4 t .. + 3, the order in which ldmatrix hands out the
-  // key codes' bytes
-  uint32_t qa[D / 16][4];
+  // B fragments of Q^T: channels 32 kk + 4 t .. + 3 and 16 on, of row g
+  uint32_t qb[NT][D / 32][3][2];
+  float f[NT][2];
+  KeyRange kr[NT][2];
+  float nl[NT][2];  // WEIGHTS: -lse log2(e); -inf: weight 0
 #pragma unroll
-  for (int kk = 0; kk < D / 16; kk++) {
-    const uint2 x = *reinterpret_cast<const uint2*>(&s.q[g][kk * 16 + t * 4]);
-    const uint2 y = *reinterpret_cast<const uint2*>(&s.q[g + 8][kk * 16 + t * 4]);
-    qa[kk][0] = x.x;
-    qa[kk][2] = x.y;
-    qa[kk][1] = y.x;
-    qa[kk][3] = y.y;
-  }
-  const float f0 = s.rowf[g], f1 = s.rowf[g + 8];
-  KeyRange kr[2];
-  float nl[2] = {-INFINITY, -INFINITY};  // WEIGHTS: -lse log2(e); -inf: weight 0
+  for (int n = 0; n < NT; n++) {
 #pragma unroll
-  for (int i = 0; i < 2; i++) {
-    const int r = r0 + g + 8 * i;
-    kr[i] = KeyRange{0, 0, 0};
-    if (r < r1) {
-      kr[i] = key_range(a.mask, off + r / a.G, len);
-      if (WEIGHTS) {
-        const float v = __ldg(a.lse_in + (static_cast<size_t>(id.b) * a.H + id.h * a.G + r % a.G) * a.Nq + r / a.G);
-        if (v != -INFINITY) nl[i] = -v * kLog2e;
+    for (int kk = 0; kk < D / 32; kk++)
+#pragma unroll
+      for (int x = 0; x < 3; x++)
+#pragma unroll
+        for (int e = 0; e < 2; e++)
+          qb[n][kk][x][e] = *reinterpret_cast<const uint32_t*>(&s.q[x][n * 8 + g][kk * 32 + e * 16 + t * 4]);
+#pragma unroll
+    for (int e = 0; e < 2; e++) {  // rows that this lane's columns are
+      const int r = n * 8 + t * 2 + e;
+      f[n][e] = s.rowf[n * 8 + t * 2 + e];
+      kr[n][e] = KeyRange{0, 0, 0};
+      nl[n][e] = -INFINITY;
+      if (r < rows) {
+        kr[n][e] = key_range(a.mask, off + r / a.G, len);
+        if (WEIGHTS) {
+          const float v = __ldg(a.lse_in + (static_cast<size_t>(b) * a.H + h * a.G + r % a.G) * a.Nq + r / a.G);
+          if (v != -INFINITY) nl[n][e] = -v * kLog2e;
+        }
       }
     }
   }
-  float o[D / 8][4];
+  // keys [full_lo, full_hi) and those below full_sink are seen by every row
+  // that is there: tiles inside need no mask.  Rows that are not there see
+  // whatever those do and are never stored.
+  const KeyRange ra = key_range(a.mask, off, len);
+  const KeyRange rz = key_range(a.mask, off + max(qn - 1, 0), len);
+  const int full_sink = min(ra.sink, rz.sink), full_lo = rz.lo, full_hi = min(ra.hi, rz.hi);
+
+  float o[D / 16][NT][4];
 #pragma unroll
-  for (int i = 0; i < D / 8; i++)
+  for (int i = 0; i < D / 16; i++)
 #pragma unroll
-    for (int e = 0; e < 4; e++) o[i][e] = 0.0f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) o[i][n][e] = 0.0f;
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; n++)
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+      m[n][e] = -INFINITY;
+      l[n][e] = 0.0f;
+    }
 
   bool ok = true;
   for (int i = 0; i < mine; i++) {
-    const int st = i % kStages;
-    ok = __all_sync(kFull, mbar_wait(&s.full[warp][st], (i / kStages) & 1, wc, kSiteDecPage));
+    const int st = (seen + i) % kStages;
+    ok = __all_sync(kFull, mbar_wait(&s.full[warp][st], ((seen + i) / kStages) & 1, wc, kSiteDecPage));
     if (!ok) break;
     const TileMeta md = s.meta[warp][st];
     const int j0 = md.j0;
@@ -268,7 +384,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       if (!WEIGHTS && j0 + kHalf > len) {
         // the sequence ends inside this tile: values behind it may be any
         // bytes (NaN among them), and zero weight times NaN is NaN.  The last
-        // tile that this warp loads, so no later TMA load meets these writes.
+        // tile of this head that the warp loads: the next head's loads come
+        // after the block's fence.
         for (int x = lane; x < kHalf * D / 16; x += 32) {
           const int r = x / (D / 16);
           if (j0 + r >= len)
@@ -276,109 +393,126 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         }
         __syncwarp();
       }
-      // scores: 4 tiles of 8 keys
-      float sc[4][4];
+      // scores of two tiles of 16 keys: keys g and g + 8, rows 2 t and 2 t + 1
+      float sc[2][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < 4; nt++) {
+      for (int mt = 0; mt < 2; mt++) {
+        int acc[NT][3][4];
 #pragma unroll
-        for (int e = 0; e < 4; e++) sc[nt][e] = 0.0f;
+        for (int n = 0; n < NT; n++)
 #pragma unroll
-        for (int c4 = 0; c4 < D / 64; c4++) {
-          uint32_t kr4[4];
-          ldsm4(kb + swz<D>(nt * 8 + (lane & 7), c4 * 4 + (lane >> 3)), kr4);
+          for (int x = 0; x < 3; x++)
 #pragma unroll
-          for (int c = 0; c < 4; c++) {
-            uint32_t b0, b1;
-            i8x4_to_f16(kr4[c], b0, b1);
-            mma16816(sc[nt], qa[c4 * 4 + c], b0, b1);
-          }
+            for (int e = 0; e < 4; e++) acc[n][x][e] = 0;
+#pragma unroll
+        for (int kk = 0; kk < D / 32; kk++) {
+          uint32_t ka[4];  // keys 0-7 / 8-15 of chunk 2 kk, then of 2 kk + 1
+          ldsm4(kb + swz<D>(mt * 16 + (lane & 15), kk * 2 + (lane >> 4)), ka);
+#pragma unroll
+          for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int x = 0; x < 3; x++) mma16832(acc[n][x], ka, qb[n][kk][x][0], qb[n][kk][x][1]);
         }
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            sc[mt][n][e] = fmaf(static_cast<float>(acc[n][2][e]), 65536.0f,
+                                static_cast<float>(acc[n][1][e] * 256 + acc[n][0][e]));
+      }
+      if (!(j0 + kHalf <= full_sink || (j0 >= full_lo && j0 + kHalf <= full_hi))) {
+#pragma unroll
+        for (int mt = 0; mt < 2; mt++)
+#pragma unroll
+          for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+              const KeyRange& k = kr[n][e & 1];
+              const int j = j0 + mt * 16 + g + (e >> 1) * 8;
+              if (!(j < k.sink || (j >= k.lo && j < k.hi))) sc[mt][n][e] = -INFINITY;
+            }
       }
       // a zero scale must not meet -inf as 0 * inf
-      const float c0 = fmaxf(f0 * md.ks, FLT_MIN), c1 = fmaxf(f1 * md.ks, FLT_MIN);
-      bool all = true;
+      float c[NT][2];
 #pragma unroll
-      for (int i2 = 0; i2 < 2; i2++)
-        all = all && (kr[i2].sink >= j0 + kHalf || (kr[i2].lo <= j0 && kr[i2].hi >= j0 + kHalf));
-      if (!__all_sync(kFull, all)) {
+      for (int n = 0; n < NT; n++)
 #pragma unroll
-        for (int nt = 0; nt < 4; nt++)
-#pragma unroll
-          for (int e = 0; e < 4; e++) {
-            const KeyRange& k = kr[e >> 1];
-            const int j = j0 + nt * 8 + t * 2 + (e & 1);
-            if (!(j < k.sink || (j >= k.lo && j < k.hi))) sc[nt][e] = -INFINITY;
-          }
-      }
+        for (int e = 0; e < 2; e++) c[n][e] = fmaxf(f[n][e] * md.ks, FLT_MIN);
       if constexpr (WEIGHTS) {
+        float w[4];  // keys g, g + 8, g + 16, g + 24
 #pragma unroll
-        for (int nt = 0; nt < 4; nt++) {
-          float w[2];
+        for (int k = 0; k < 4; k++) {
+          w[k] = 0.0f;
 #pragma unroll
-          for (int e = 0; e < 2; e++) {
-            w[e] = ex2_approx(fmaf(sc[nt][e], c0, nl[0])) + ex2_approx(fmaf(sc[nt][2 + e], c1, nl[1]));
-            w[e] += __shfl_xor_sync(kFull, w[e], 4);
-            w[e] += __shfl_xor_sync(kFull, w[e], 8);
-            w[e] += __shfl_xor_sync(kFull, w[e], 16);
-          }
-          if (g == (nt & 7)) {
-            float* dst = a.c.weight + static_cast<size_t>(md.unit) * kPage + (j0 & (kPage - 1)) + nt * 8 + t * 2;
+          for (int n = 0; n < NT; n++)
 #pragma unroll
-            for (int e = 0; e < 2; e++) {
-              if (j0 + nt * 8 + t * 2 + e < len) {
-                if (a.accumulate) atomicAdd(dst + e, w[e]);  // a page may serve two sequences
-                else dst[e] = w[e];
-              }
-            }
-          }
+            for (int e = 0; e < 2; e++)
+              w[k] += ex2_approx(fmaf(sc[k >> 1][n][(k & 1) * 2 + e], c[n][e], nl[n][e]));
+          w[k] += __shfl_xor_sync(kFull, w[k], 1);
+          w[k] += __shfl_xor_sync(kFull, w[k], 2);
+        }
+        // lane (g, t) writes key 8 t + g
+        const float v = t == 0 ? w[0] : t == 1 ? w[1] : t == 2 ? w[2] : w[3];
+        const int j = j0 + t * 8 + g;
+        if (j < len) {
+          float* dst = a.c.weight + static_cast<size_t>(md.unit) * kPage + (j & (kPage - 1));
+          if (a.accumulate) atomicAdd(dst, v);  // a page may serve two sequences
+          else *dst = v;
         }
       } else {
         const float ve = static_cast<float>(md.ve);
-        float pm[2];
-        pm[0] = fmax3(fmax3(sc[0][0], sc[0][1], sc[1][0]), fmax3(sc[1][1], sc[2][0], sc[2][1]),
-                      fmaxf(sc[3][0], sc[3][1]));
-        pm[1] = fmax3(fmax3(sc[0][2], sc[0][3], sc[1][2]), fmax3(sc[1][3], sc[2][2], sc[2][3]),
-                      fmaxf(sc[3][2], sc[3][3]));
+        float pm[NT][2];
         bool grow = false;
 #pragma unroll
-        for (int i2 = 0; i2 < 2; i2++) {
-          pm[i2] = fmaxf(pm[i2], __shfl_xor_sync(kFull, pm[i2], 1));
-          pm[i2] = fmaxf(pm[i2], __shfl_xor_sync(kFull, pm[i2], 2));
-          pm[i2] = fmaf(pm[i2], i2 ? c1 : c0, ve);
-          grow = grow || pm[i2] > m[i2] + kLazy;
-        }
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            float x = fmax3(fmaxf(sc[0][n][e], sc[0][n][e + 2]), sc[1][n][e], sc[1][n][e + 2]);
+            x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
+            pm[n][e] = fmaf(x, c[n][e], ve);
+            grow = grow || pm[n][e] > m[n][e] + kLazy;
+          }
         if (__any_sync(kFull, grow)) {
 #pragma unroll
-          for (int i2 = 0; i2 < 2; i2++) {
-            const float mn = fmaxf(m[i2], pm[i2]);
-            const float al = m[i2] == mn ? 1.0f : ex2_approx(m[i2] - mn);  // 0 from -inf
-            m[i2] = mn;
-            l[i2] *= al;
+          for (int n = 0; n < NT; n++)
 #pragma unroll
-            for (int d = 0; d < D / 8; d++) {
-              o[d][2 * i2] *= al;
-              o[d][2 * i2 + 1] *= al;
+            for (int e = 0; e < 2; e++) {
+              const float mn = fmaxf(m[n][e], pm[n][e]);
+              const float al = m[n][e] == mn ? 1.0f : ex2_approx(m[n][e] - mn);  // 0 from -inf
+              m[n][e] = mn;
+              l[n][e] *= al;
+#pragma unroll
+              for (int d = 0; d < D / 16; d++) {
+                o[d][n][e] *= al;
+                o[d][n][e + 2] *= al;
+              }
             }
-          }
-        }
-        const float nm0 = m[0] == -INFINITY ? 0.0f : kBoost + ve - m[0];
-        const float nm1 = m[1] == -INFINITY ? 0.0f : kBoost + ve - m[1];
-        float rs[2] = {0.0f, 0.0f};
-        uint32_t pa[2][4];
-#pragma unroll
-        for (int nt = 0; nt < 4; nt++) {
-          const float y0 = ex2_approx(fmaf(sc[nt][0], c0, nm0)), y1 = ex2_approx(fmaf(sc[nt][1], c0, nm0));
-          const float y2 = ex2_approx(fmaf(sc[nt][2], c1, nm1)), y3 = ex2_approx(fmaf(sc[nt][3], c1, nm1));
-          rs[0] += y0 + y1;
-          rs[1] += y2 + y3;
-          const __half2 h0 = __floats2half2_rn(y0, y1), h1 = __floats2half2_rn(y2, y3);
-          pa[nt / 2][(nt & 1) * 2] = *reinterpret_cast<const uint32_t*>(&h0);
-          pa[nt / 2][(nt & 1) * 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
         }
         const float un = pow2i(min(-md.ve, 127));
-        l[0] = fmaf(rs[0], un, l[0]);
-        l[1] = fmaf(rs[1], un, l[1]);
-        // O += P V: per 32 channels, 16 keys at a time
+        uint32_t pb[2][NT][2];  // B fragments of P^T, 16 keys each
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+          float nm[2], rs[2] = {0.0f, 0.0f};
+#pragma unroll
+          for (int e = 0; e < 2; e++) nm[e] = m[n][e] == -INFINITY ? 0.0f : kBoost + ve - m[n][e];
+#pragma unroll
+          for (int mt = 0; mt < 2; mt++)
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+              const float y0 = ex2_approx(fmaf(sc[mt][n][k * 2], c[n][0], nm[0]));
+              const float y1 = ex2_approx(fmaf(sc[mt][n][k * 2 + 1], c[n][1], nm[1]));
+              rs[0] += y0;
+              rs[1] += y1;
+              const __half2 y = __floats2half2_rn(y0, y1);
+              pb[mt][n][k] = transpose8(*reinterpret_cast<const uint32_t*>(&y));
+            }
+          l[n][0] = fmaf(rs[0], un, l[n][0]);
+          l[n][1] = fmaf(rs[1], un, l[n][1]);
+        }
+        // O^T += V^T P^T: tiles of 16 channels, 16 keys at a time.  Row g of
+        // the tile is channel 2 g, row g + 8 channel 2 g + 1.
 #pragma unroll
         for (int kk = 0; kk < 2; kk++) {
 #pragma unroll
@@ -386,12 +520,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
             uint32_t vr[4];  // keys 0-7 / 8-15 of two 16-channel chunks
             ldsm4t(vb + swz<D>(kk * 16 + (lane & 15), d2 * 2 + (lane >> 4)), vr);
 #pragma unroll
-            for (int c = 0; c < 2; c++) {
-              uint32_t e0, o0, e1, o1;
-              f8x4_to_f16(vr[2 * c], e0, o0);
-              f8x4_to_f16(vr[2 * c + 1], e1, o1);
-              mma16816(o[(d2 * 2 + c) * 2], pa[kk], e0, e1);
-              mma16816(o[(d2 * 2 + c) * 2 + 1], pa[kk], o0, o1);
+            for (int x = 0; x < 2; x++) {
+              uint32_t va[4];
+              f8x4_to_f16(vr[2 * x], va[0], va[1]);
+              f8x4_to_f16(vr[2 * x + 1], va[2], va[3]);
+#pragma unroll
+              for (int n = 0; n < NT; n++) mma16816(o[d2 * 2 + x][n], va, pb[kk][n][0], pb[kk][n][1]);
             }
           }
         }
@@ -403,42 +537,51 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   if (!ok) {  // a wait ran out (recorded): let the loads in flight land, then leave
     if (lane == 0)
       for (int i = max(0, issued - kStages); i < issued; i++)
-        drain_wait(&s.full[warp][i % kStages], (i / kStages) & 1, wc, kSiteDecDrain);
+        drain_wait(&s.full[warp][(seen + i) % kStages], ((seen + i) / kStages) & 1, wc, kSiteDecDrain);
     __syncwarp();
   }
-  if constexpr (WEIGHTS) return;
-  // row sums over the four lanes of a row
-#pragma unroll
-  for (int i = 0; i < 2; i++) {
-    l[i] += __shfl_xor_sync(kFull, l[i], 1);
-    l[i] += __shfl_xor_sync(kFull, l[i], 2);
+  seen += mine;
+  if constexpr (WEIGHTS) {
+    __syncthreads();  // the query rows in shared memory are free again
+    return;
   }
+  // row sums over the eight lanes of a column
+#pragma unroll
+  for (int n = 0; n < NT; n++)
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+      l[n][e] += __shfl_xor_sync(kFull, l[n][e], 4);
+      l[n][e] += __shfl_xor_sync(kFull, l[n][e], 8);
+      l[n][e] += __shfl_xor_sync(kFull, l[n][e], 16);
+    }
   // join the warps: every tile has landed and been read, so the ring holds
-  // the partial rows, fp32 [16][D] a warp
+  // the partial rows, fp32 [ROWS][D] a warp
   __syncthreads();
   if (s.abort) return;
   float* part = reinterpret_cast<float*>(s.kv[warp][0][0]);
-  static_assert(kStages * 2 * kHalf * D >= kDecRows * D * 4, "a warp's ring holds its partial rows");
+  static_assert(kStages * 2 * kHalf * D >= ROWS * D * 4, "a warp's ring holds its partial rows");
 #pragma unroll
-  for (int d = 0; d < D / 16; d++) {
-    // tiles 2 d and 2 d + 1 hold channels 16 d + 4 t + {0, 2} and + {1, 3}
-    *reinterpret_cast<float4*>(part + g * D + d * 16 + t * 4) =
-        make_float4(o[2 * d][0], o[2 * d + 1][0], o[2 * d][1], o[2 * d + 1][1]);
-    *reinterpret_cast<float4*>(part + (g + 8) * D + d * 16 + t * 4) =
-        make_float4(o[2 * d][2], o[2 * d + 1][2], o[2 * d][3], o[2 * d + 1][3]);
-  }
-  if (t == 0) {
-    s.ml[warp][g][0] = m[0];
-    s.ml[warp][g][1] = l[0];
-    s.ml[warp][g + 8][0] = m[1];
-    s.ml[warp][g + 8][1] = l[1];
+  for (int n = 0; n < NT; n++) {
+#pragma unroll
+    for (int d = 0; d < D / 16; d++)
+#pragma unroll
+      for (int e = 0; e < 2; e++)
+        *reinterpret_cast<float2*>(part + (n * 8 + t * 2 + e) * D + d * 16 + g * 2) =
+            make_float2(o[d][n][e], o[d][n][e + 2]);
+    if (g == 0) {
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        s.ml[warp][n * 8 + t * 2 + e][0] = m[n][e];
+        s.ml[warp][n * 8 + t * 2 + e][1] = l[n][e];
+      }
+    }
   }
   __syncthreads();
-  const int nch = min(a.chunks, (runs.n + a.chunk_pages - 1) / a.chunk_pages);
   constexpr size_t kWarpFloats = kStages * 2 * kHalf * D / 4;
-  for (int x = threadIdx.x; x < kDecRows * D / 2; x += kWarps * 32) {
+  const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + (p0 == 0)) * ROWS;
+  for (int x = threadIdx.x; x < ROWS * D / 2; x += kWarps * 32) {
     const int r = x / (D / 2), d = x % (D / 2) * 2;
-    if (r0 + r >= r1) break;
+    if (r >= rows) break;
     float mx = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; w++) mx = fmaxf(mx, s.ml[w][r][0]);
@@ -453,112 +596,218 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       oy = fmaf(al, v.y, oy);
       ls = fmaf(al, s.ml[w][r][1], ls);
     }
-    const size_t urow = (static_cast<size_t>(id.b) * a.c.Hkv + id.h) * (static_cast<size_t>(row_tiles) * kDecRows) + r0 + r;
-    if (nch > 1) {
-      const size_t pr = urow * a.chunks + id.chunk;
-      *reinterpret_cast<float2*>(a.part_o + pr * D + d) = make_float2(ox, oy);
-      if (d == 0) *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(mx - kBoost, ls);
+    if (p1 - p0 < np) {
+      *reinterpret_cast<float2*>(a.part_o + (slot + r) * D + d) = make_float2(ox, oy);
+      if (d == 0) *reinterpret_cast<float2*>(a.part_ml + (slot + r) * 2) = make_float2(mx - kBoost, ls);
     } else {
       const float inv = ls > 0.0f ? 1.0f / ls : 0.0f;
-      const int rr = r0 + r, tok = rr / a.G, head = id.h * a.G + rr % a.G;
-      store_o2(a, a.ob * id.b + a.oh * head + a.on * tok + d, ox * inv, oy * inv);
+      const int tok = r / a.G, head = h * a.G + r % a.G;
+      store_o2(a, a.ob * b + a.oh * head + a.on * tok + d, ox * inv, oy * inv);
       if (d == 0 && a.lse)
-        a.lse[(static_cast<size_t>(id.b) * a.H + head) * a.Nq + tok] =
+        a.lse[(static_cast<size_t>(b) * a.H + head) * a.Nq + tok] =
             ls > 0.0f ? (mx - kBoost + log2f(ls)) * kLn2 : -INFINITY;
     }
   }
+  // the ring held the partial rows: order them before the next head's loads
+  fence_proxy_async_smem();
+  __syncthreads();
 }
 
-// Join of the KV ranges: one warp per row, in range order.
-template <int D>
-__global__ void __launch_bounds__(128) k_cache_merge(const CacheAttnArgs a, int row_tiles, int tile_rows) {
-  const int lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const long long per = static_cast<long long>(row_tiles) * tile_rows;
-  const long long bh = row / per;
-  if (bh >= static_cast<long long>(a.c.B) * a.c.Hkv) return;
-  const int r = static_cast<int>(row - bh * per), b = static_cast<int>(bh / a.c.Hkv),
-            h = static_cast<int>(bh % a.c.Hkv);
-  const int len = seq_length(a.c, b), qn = query_len(a, b), rows = qn * a.G;
-  if (r >= rows) return;
-  const int r0 = r / tile_rows * tile_rows, r1 = min(rows, r0 + tile_rows);
-  const long long off = static_cast<long long>(len) - qn;
-  const PageRuns runs = page_runs(a.mask, off + r0 / a.G, off + (r1 - 1) / a.G, len);
-  const int nch = min(a.chunks, (runs.n + a.chunk_pages - 1) / a.chunk_pages);
-  if (nch <= 1) return;  // the attention kernel wrote this tile itself
-  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row * a.chunks;
-  float mx = -INFINITY;
-  for (int i = lane; i < nch; i += 32) mx = fmaxf(mx, ml[i].x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-  constexpr int PER = D / 32;
-  float o[PER], ls = 0.0f;
-#pragma unroll
-  for (int e = 0; e < PER; e++) o[e] = 0.0f;
-  const float* po = a.part_o + row * a.chunks * D + lane * PER;
-#pragma unroll 4
-  for (int i = 0; i < nch; i++) {
-    const float2 x = ml[i];
-    const float al = x.x == -INFINITY ? 0.0f : ex2_approx(x.x - mx);
-    ls = fmaf(al, x.y, ls);
-#pragma unroll
-    for (int e = 0; e < PER; e++) o[e] = fmaf(al, po[static_cast<size_t>(i) * D + e], o[e]);
+// NT: query rows in eighths (8 NT rows).  WEIGHTS: instead of attending,
+// w[key] (+)= sum over the rows of exp(s - lse), the rows' lse given.
+template <int D, int NT, bool WEIGHTS>
+__global__ void __launch_bounds__(kWarps * 32, 2)
+    k_cache_decode(const __grid_constant__ CacheAttnMaps maps, const CacheAttnArgs a) {
+  extern __shared__ __align__(1024) uint8_t raw[];
+  if (smem_misaligned(raw, a.c.status)) return;
+  DecSmem<D>& s = *reinterpret_cast<DecSmem<D>*>(raw);
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&maps.k);
+    if (!WEIGHTS) tma_prefetch_desc(&maps.v);
+    for (int w = 0; w < kWarps; w++)
+      for (int i = 0; i < kStages; i++) mbar_init(&s.full[w][i], 1);
+    s.abort = 0;
+    fence_mbar_init();
   }
-  const float inv = ls > 0.0f ? 1.0f / ls : 0.0f;
-  const int tok = r / a.G, head = h * a.G + r % a.G;
-  const size_t ob = a.ob * b + a.oh * head + a.on * tok + lane * PER;
+  const int c = blockIdx.x, n = gridDim.x;
+  const WaitCtx wc{a.budget, a.c.status, &s.abort};
+  int seen = 0;
+  if (a.whole) {
+    __syncthreads();
+    const int b = c / a.c.Hkv, len = seq_length(a.c, b), qn = query_len(a, b);
+    const PageRuns runs = seq_runs<WEIGHTS>(a, b, len, qn);
+    const int np = seq_work<WEIGHTS>(a, b);
+    if (np > 0) decode_head<D, NT, WEIGHTS>(s, maps, a, b, c % a.c.Hkv, len, qn, runs, 0, np, np, seen, wc);
+    return;
+  }
+  // (locate's barriers also publish the ring's)
+  const Place pl = locate<WEIGHTS>(s.place, a, [&](long long w) { return share_start(w, c, n); });
+  if (!WEIGHTS) cudaTriggerProgrammaticLaunchCompletion();
+  long long x = share_start(pl.work, c, n);
+  const long long end = share_start(pl.work, c + 1, n);
+  long long before = pl.before;
+  for (int b = pl.b; x < end && b < a.c.B; b++) {
+    const int np = seq_work<WEIGHTS>(a, b);
+    if (np == 0) continue;
+    const int len = seq_length(a.c, b), qn = query_len(a, b);
+    const PageRuns runs = seq_runs<WEIGHTS>(a, b, len, qn);
+    for (long long rel = x - before * a.c.Hkv; x < end && rel < static_cast<long long>(np) * a.c.Hkv;) {
+      const int h = static_cast<int>(rel / np), p0 = static_cast<int>(rel - static_cast<long long>(h) * np);
+      const int p1 = static_cast<int>(min(static_cast<long long>(np), p0 + (end - x)));
+      decode_head<D, NT, WEIGHTS>(s, maps, a, b, h, len, qn, runs, p0, p1, np, seen, wc);
+      if (s.abort) return;
+      x += p1 - p0;
+      rel += p1 - p0;
+    }
+    before += np;
+  }
+}
+
+// Join of the heads that stretches cut, one block a head; threads (group,
+// row, 4 channels), the groups every GR-th partial in turn, summed in order.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kWarps * 32) k_cache_join(const CacheAttnArgs a, int n) {
+  __shared__ PlaceSmem place;
+  __shared__ float4 sh_o[kWarps * 32];
+  __shared__ float sh_l[kWarps * 32];
+  cudaGridDependencySynchronize();  // launched under the attention kernel's tail
+  const int b = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv;
+  const int np = seq_work<false>(a, b);
+  if (np == 0) return;
+  // pages before b: locate a position of b, found by its own count
+  long long before = 0, work = 0;
+  {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    long long sb = 0, sw = 0;
+    for (int i = tid; i < a.c.B; i += kWarps * 32) {
+      const int v = seq_work<false>(a, i);
+      sw += v;
+      if (i < b) sb += v;
+    }
 #pragma unroll
-  for (int e = 0; e < PER; e += 2) store_o2(a, ob + e, o[e] * inv, o[e + 1] * inv);
-  if (lane == 0 && a.lse)
-    a.lse[(static_cast<size_t>(b) * a.H + head) * a.Nq + tok] =
-        ls > 0.0f ? (mx + log2f(ls)) * kLn2 : -INFINITY;
+    for (int o = 16; o; o >>= 1) {
+      sb += __shfl_xor_sync(kFull, sb, o);
+      sw += __shfl_xor_sync(kFull, sw, o);
+    }
+    if (lane == 0) place.sum[warp] = sb;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) before += place.sum[w];
+    __syncthreads();
+    if (lane == 0) place.sum[warp] = sw;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) work += place.sum[w];
+    work *= a.c.Hkv;
+  }
+  const long long x0 = before * a.c.Hkv + static_cast<long long>(h) * np;
+  const int c0 = share_of(work, x0, n), c1 = share_of(work, x0 + np - 1, n);
+  if (c0 == c1) return;  // one block had the whole head and wrote it
+  const int qn = query_len(a, b), rows = qn * a.G;
+  constexpr int Q = D / 4;
+  const int items = rows * Q;
+  const int groups = max(1, kWarps * 32 / items);
+  const bool split = groups > 1;
+  for (int it0 = 0; it0 < items; it0 += kWarps * 32) {
+    const int grp = split ? threadIdx.x / items : 0, it = split ? threadIdx.x % items : it0 + threadIdx.x;
+    const bool live = grp < groups && it < items;
+    const int r = live ? it / Q : 0, d = it % Q * 4;
+    float mx = -INFINITY, ls = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto slot = [&](int c) {
+      return (2 * static_cast<size_t>(c) + (c == c0)) * ROWS + r;
+    };
+    auto has = [&](int c) { return share_start(work, c, n) < share_start(work, c + 1, n); };
+    if (live) {
+#pragma unroll 4
+      for (int c = c0; c <= c1; c++)
+        if (has(c)) mx = fmaxf(mx, a.part_ml[slot(c) * 2]);
+#pragma unroll 4
+      for (int c = c0 + grp; c <= c1; c += groups) {
+        if (!has(c)) continue;
+        const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + slot(c) * 2);
+        const float4 v = *reinterpret_cast<const float4*>(a.part_o + slot(c) * D + d);
+        const float al = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - mx);
+        ls = fmaf(al, ml.y, ls);
+        o = make_float4(fmaf(al, v.x, o.x), fmaf(al, v.y, o.y), fmaf(al, v.z, o.z), fmaf(al, v.w, o.w));
+      }
+    }
+    if (split) {
+      sh_o[threadIdx.x] = o;
+      sh_l[threadIdx.x] = ls;
+      __syncthreads();
+      if (live && grp == 0) {
+        for (int k = 1; k < groups; k++) {
+          const float4 v = sh_o[k * items + it];
+          o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+          ls += sh_l[k * items + it];
+        }
+      }
+    }
+    if (!live || grp != 0) continue;
+    const float inv = ls > 0.0f ? 1.0f / ls : 0.0f;
+    const int tok = r / a.G, head = h * a.G + r % a.G;
+    const size_t ob = a.ob * b + a.oh * head + a.on * tok + d;
+    store_o2(a, ob, o.x * inv, o.y * inv);
+    store_o2(a, ob + 2, o.z * inv, o.w * inv);
+    if (d == 0 && a.lse)
+      a.lse[(static_cast<size_t>(b) * a.H + head) * a.Nq + tok] =
+          ls > 0.0f ? (mx + log2f(ls)) * kLn2 : -INFINITY;
+  }
 }
 
 }  // namespace
 
 namespace {
-template <int D, bool WEIGHTS>
+template <int D, int NT, bool WEIGHTS>
 cudaError_t prepare_one() {
-  return cudaFuncSetAttribute(k_cache_decode<D, WEIGHTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(k_cache_decode<D, NT, WEIGHTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               static_cast<int>(sizeof(DecSmem<D>)));
 }
+template <int D>
+cudaError_t prepare_d() {
+  cudaError_t e = prepare_one<D, 1, false>();
+  if (e == cudaSuccess) e = prepare_one<D, 2, false>();
+  if (e == cudaSuccess) e = prepare_one<D, 1, true>();
+  if (e == cudaSuccess) e = prepare_one<D, 2, true>();
+  return e;
+}
 template <int D, bool WEIGHTS>
-cudaError_t launch_one(const CacheAttnMaps& m, const CacheAttnArgs& a, int row_tiles, cudaStream_t s) {
-  const long long units = static_cast<long long>(a.c.B) * a.c.Hkv * row_tiles;
-  const unsigned grid = static_cast<unsigned>(units * a.chunks);
-  k_cache_decode<D, WEIGHTS><<<grid, kWarps * 32, sizeof(DecSmem<D>), s>>>(m, a, row_tiles);
-  return cudaGetLastError();
+cudaError_t launch_d(const CacheAttnMaps& m, const CacheAttnArgs& a, cudaStream_t s) {
+  const bool one = decode_tile_rows(a.Nq, a.G) == 8;
+  if (one) k_cache_decode<D, 1, WEIGHTS><<<a.chunks, kWarps * 32, sizeof(DecSmem<D>), s>>>(m, a);
+  else k_cache_decode<D, 2, WEIGHTS><<<a.chunks, kWarps * 32, sizeof(DecSmem<D>), s>>>(m, a);
+  cudaError_t e = cudaGetLastError();
+  if (WEIGHTS || e != cudaSuccess || a.whole) return e;
+  // the join starts while the last attention blocks still run and waits for
+  // them on the device (programmatic dependent launch)
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.c.B) * a.c.Hkv);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return one ? cudaLaunchKernelEx(&cfg, k_cache_join<D, 8>, a, a.chunks)
+             : cudaLaunchKernelEx(&cfg, k_cache_join<D, 16>, a, a.chunks);
 }
 }  // namespace
 
 cudaError_t cache_prepare() {
-  cudaError_t e = prepare_one<128, false>();
-  if (e == cudaSuccess) e = prepare_one<64, false>();
-  if (e == cudaSuccess) e = prepare_one<128, true>();
-  if (e == cudaSuccess) e = prepare_one<64, true>();
+  cudaError_t e = prepare_d<128>();
+  if (e == cudaSuccess) e = prepare_d<64>();
   if (e == cudaSuccess) e = cache_prefill_prepare();
   if (e == cudaSuccess) e = cache_weights_prepare();
   return e;
 }
 
 cudaError_t launch_cache_decode(const CacheAttnMaps& m, const CacheAttnArgs& a, cudaStream_t s) {
-  const int row_tiles = (a.Nq * a.G + kDecRows - 1) / kDecRows;
-  const cudaError_t e = a.c.D == 128 ? launch_one<128, false>(m, a, row_tiles, s)
-                                     : launch_one<64, false>(m, a, row_tiles, s);
-  if (e != cudaSuccess || a.chunks == 1) return e;
-  return launch_cache_merge(a, row_tiles, kDecRows, s);
+  return a.c.D == 128 ? launch_d<128, false>(m, a, s) : launch_d<64, false>(m, a, s);
 }
-
 cudaError_t launch_cache_weights_few(const CacheAttnMaps& m, const CacheAttnArgs& a, cudaStream_t s) {
-  return a.c.D == 128 ? launch_one<128, true>(m, a, 1, s) : launch_one<64, true>(m, a, 1, s);
-}
-
-cudaError_t launch_cache_merge(const CacheAttnArgs& a, int row_tiles, int tile_rows, cudaStream_t s) {
-  const long long rows = static_cast<long long>(a.c.B) * a.c.Hkv * row_tiles * tile_rows;
-  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
-  if (a.c.D == 128) k_cache_merge<128><<<grid, 128, 0, s>>>(a, row_tiles, tile_rows);
-  else k_cache_merge<64><<<grid, 128, 0, s>>>(a, row_tiles, tile_rows);
-  return cudaGetLastError();
+  return a.c.D == 128 ? launch_d<128, true>(m, a, s) : launch_d<64, true>(m, a, s);
 }
 
 }  // namespace sage

@@ -45,38 +45,17 @@ __device__ __forceinline__ float load_q(const void* q, int type, size_t i) {
                            : __half2float(static_cast<const __half*>(q)[i]);
 }
 
-// One query row as fp16 values through put(channel, x 2^-e), by a warp;
-// returns the row's factor 2^e.  A row that is not there becomes zero.
-template <int D, typename Put>
-__device__ __forceinline__ float stage_row_as(const CacheAttnArgs& a, int b, int h, int r, int rows,
-                                              int lane, Put put) {
-  constexpr int PER = D / 32;
-  float f[PER];
-  float m = 0.0f;
-  if (r < rows) {
-    const size_t base = a.qb * b + a.qh * (static_cast<size_t>(h) * a.G + r % a.G) +
-                        a.qn * (r / a.G) + lane * PER;
-#pragma unroll
-    for (int e = 0; e < PER; e++) {
-      f[e] = load_q(a.q, a.type, base + e);
-      m = fmaxf(m, fabsf(f[e]));
-    }
+// Two neighbouring channels of one output row.
+__device__ __forceinline__ void store_o2(const CacheAttnArgs& a, size_t i, float x, float y) {
+  if (a.type == kTypeBf16) {
+    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.o) + i;
+    p[0] = __float2bfloat16_rn(x);
+    p[1] = __float2bfloat16_rn(y);
   } else {
-#pragma unroll
-    for (int e = 0; e < PER; e++) f[e] = 0.0f;
+    __half* p = static_cast<__half*>(a.o) + i;
+    p[0] = __float2half_rn(x);
+    p[1] = __float2half_rn(y);
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const int p = row_power(m);
-  const float inv = pow2i(-p);
-#pragma unroll
-  for (int e = 0; e < PER; e++) put(lane * PER + e, f[e] * inv);
-  return pow2i(p);
-}
-template <int D>
-__device__ __forceinline__ float stage_row(const CacheAttnArgs& a, int b, int h, int r, int rows,
-                                           __half* dst, int lane) {
-  return stage_row_as<D>(a, b, h, r, rows, lane, [&](int ch, float x) { dst[ch] = __float2half_rn(x); });
 }
 
 // ---------------------------------------------------------------- tcgen05 operands

@@ -127,6 +127,14 @@ class _There:
         self.device.__exit__(*exc)
 
 
+def _new(t):
+    """An uninitialised contiguous tensor like `t`, and its strides."""
+    import torch
+    out = torch.empty_like(t) if t.is_contiguous() else \
+        torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return out, _strides(out)
+
+
 def _strides(t):
     b, h, n, c = t.stride()
     B, H, N, C = t.shape
@@ -218,8 +226,8 @@ def rope(x, positions, inv_freq, layout="interleaved", amplitude=1.0, inverse=Fa
     pairs (2p, 2p + 1), "half" pairs (p, p + R/2).  inverse: turn back -- the
     gradient of the forward call with respect to x, from that of its result.
     out: None, a tensor like x, or x itself."""
-    import torch
-    if x.dim() != 4 or _type(x) < 0:
+    kind = _type(x)
+    if x.dim() != 4 or kind < 0:
         raise ValueError("x must be a bf16, fp16 or fp32 tensor [B, H, N, D]")
     if layout not in ("interleaved", "half"):
         raise ValueError("layout must be 'interleaved' or 'half'")
@@ -233,14 +241,17 @@ def rope(x, positions, inv_freq, layout="interleaved", amplitude=1.0, inverse=Fa
     freq, R = _freqs(inv_freq, dev)
     if R > D:
         raise ValueError("inv_freq has more pairs than the heads")
+    xs = _strides(x)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out, ys = _new(x)
     elif out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
         raise ValueError("out must have x's shape, type and device")
-    if x.numel():
-        _check(_lib().sage_rope(x.data_ptr(), out.data_ptr(), _type(x), B, H, N, D, R, _strides(x),
-                                _out_strides(out), pos, p64, pstride, freq, amplitude,
-                                layout == "half", bool(inverse), st), "sage_rope")
+    else:
+        ys = _out_strides(out)
+    if B and H and N and D:
+        _check(_lib().sage_rope(x.data_ptr(), out.data_ptr(), kind, B, H, N, D, R, xs, ys, pos, p64,
+                                pstride, freq, amplitude, layout == "half", bool(inverse), st),
+               "sage_rope")
     return out
 
 
@@ -337,19 +348,21 @@ def cache_append(cache, k, v, pages, lengths, n_new=None, k_shift=None, stream=N
         with _There(cache.k_i8, stream):
             return cache_append(cache, k, v, pages, lengths, n_new, k_shift)
     sq = _seqs(cache, pages, lengths)
-    if k.dim() != 4 or k.shape[0] != sq.B or k.shape[1] != cache.kv_heads or \
-            k.shape[3] != cache.head_dim or v.shape != k.shape:
+    shape = k.shape
+    if len(shape) != 4 or shape[0] != sq.B or shape[1] != cache.kv_heads or \
+            shape[3] != cache.head_dim or v.shape != shape:
         raise ValueError("k and v must be [B, %d, n, %d]" % (cache.kv_heads, cache.head_dim))
-    if k.dtype not in (torch.bfloat16, torch.float16) or v.dtype != k.dtype or \
-            k.device != cache.device or v.device != cache.device:
+    kind = _type(k)
+    if kind not in (0, 1) or v.dtype is not k.dtype or k.get_device() != cache.index or \
+            v.get_device() != cache.index:
         raise ValueError("k and v must be bf16 or fp16 tensors on %s" % cache.device)
     _shift_ok(cache, k_shift)
     nn = None if n_new is None else _int32(n_new, (sq.B,), "n_new", cache.index)
-    if k.shape[2] == 0 or sq.B == 0:
+    if shape[2] == 0 or sq.B == 0:
         return
     _check(_lib().sage_cache_append(
-        ctypes.byref(cache.struct()), ctypes.byref(sq), k.data_ptr(), v.data_ptr(), _type(k),
-        k.shape[2], _strides(k), _strides(v), nn,
+        ctypes.byref(cache.struct()), ctypes.byref(sq), k.data_ptr(), v.data_ptr(), kind,
+        shape[2], _strides(k), _strides(v), nn,
         None if k_shift is None else k_shift.data_ptr(), st), "sage_cache_append")
 
 
@@ -376,10 +389,9 @@ def cache_read(cache, pages, lengths, n, starts=None, k_shift=None, weights=Fals
     sp = None if starts is None else _int32(starts, (sq.B,), "starts", cache.index)
     if weights and cache.weight is None:
         raise ValueError("the cache keeps no weights")
-    k = torch.empty((sq.B, cache.kv_heads, n, cache.head_dim), dtype=torch.float32,
-                    device=cache.device)
+    k = cache.k_scale.new_empty((sq.B, cache.kv_heads, n, cache.head_dim))
     v = torch.empty_like(k)
-    w = torch.empty(k.shape[:3], dtype=torch.float32, device=cache.device) if weights else None
+    w = k.new_empty(k.shape[:3]) if weights else None
     if k.numel():
         _check(_lib().sage_cache_read(
             ctypes.byref(cache.struct()), ctypes.byref(sq), n, sp,
@@ -401,18 +413,18 @@ def _mask(mask):
 
 
 def _query(q, cache, sq, q_lens, max_len, scale):
-    if q.dim() != 4 or q.shape[0] != sq.B or q.shape[3] != cache.head_dim or \
-            q.shape[1] % cache.kv_heads:
+    kind = _type(q)
+    if q.dim() != 4 or kind not in (0, 1) or q.get_device() != cache.index:
+        raise ValueError("q must be a bf16 or fp16 tensor [B, H, Nq, D] on %s" % cache.device)
+    B, H, N, D = q.shape
+    if B != sq.B or D != cache.head_dim or H % cache.kv_heads:
         raise ValueError("q must be [B, H, Nq, %d], H a multiple of %d" % (cache.head_dim,
                                                                          cache.kv_heads))
-    kind = _type(q)
-    if kind not in (0, 1) or q.get_device() != cache.index:
-        raise ValueError("q must be a bf16 or fp16 tensor on %s" % cache.device)
     cap = sq.max_pages * PAGE
     return _Query(q.data_ptr(), _strides(q),
-                  None if q_lens is None else _int32(q_lens, (sq.B,), "q_lens", cache.index),
-                  kind, q.shape[1], q.shape[2], cap if max_len is None else min(int(max_len), cap),
-                  cache.head_dim ** -0.5 if scale is None else float(scale))
+                  None if q_lens is None else _int32(q_lens, (B,), "q_lens", cache.index),
+                  kind, H, N, cap if max_len is None or max_len > cap else max_len,
+                  D ** -0.5 if scale is None else scale)
 
 
 def cache_attn_workspace_bytes(cache, B, H, Nq, max_len, mask=None):
@@ -444,28 +456,33 @@ def cache_attn(q, cache, pages, lengths, mask=None, q_lens=None, max_len=None, s
     sq = _seqs(cache, pages, lengths)
     qs = _query(q, cache, sq, q_lens, max_len, scale)
     m = _mask(mask)
-    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or
-                            out.device != q.device):
-        raise ValueError("out must have q's shape, type and device")
-    if lse is not None and (lse.shape != q.shape[:3] or lse.dtype != torch.float32 or
-                            lse.device != q.device or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous float32 tensor [B, H, Nq]")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if lse is None and return_lse:
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-    if q.numel():
-        if workspace is None:
-            n = _lib().sage_cache_attn_workspace_bytes(
-                sq.B, cache.kv_heads, qs.H, qs.Nq, cache.head_dim, qs.max_len, *m)
-            workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
-        elif workspace.device != q.device or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on %s" % q.device)
-        _check(_lib().sage_cache_attn(
-            ctypes.byref(cache.struct()), ctypes.byref(sq), ctypes.byref(qs), *m,
-            out.data_ptr(), _out_strides(out), None if lse is None else lse.data_ptr(),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), st),
-            "sage_cache_attn")
+        out, os = _new(q)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device:
+        raise ValueError("out must have q's shape, type and device")
+    else:
+        os = _out_strides(out)
+    if lse is None:
+        if return_lse:
+            lse = q.new_empty(q.shape[:3], dtype=torch.float32)
+    elif lse.shape != q.shape[:3] or lse.dtype != torch.float32 or lse.device != q.device or \
+            not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 tensor [B, H, Nq]")
+    if sq.B == 0 or qs.H == 0 or qs.Nq == 0:
+        return (out, lse) if return_lse else out
+    L = _lib()
+    if workspace is None:
+        n = L.sage_cache_attn_workspace_bytes(sq.B, cache.kv_heads, qs.H, qs.Nq, cache.head_dim,
+                                              qs.max_len, *m)
+        if n > 16:  # else: one range a query tile, no partial results
+            workspace = q.new_empty((n,), dtype=torch.uint8)
+    elif workspace.device != q.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % q.device)
+    ws, nb = (None, 0) if workspace is None else (workspace.data_ptr(),
+                                                  workspace.numel() * workspace.element_size())
+    _check(L.sage_cache_attn(ctypes.byref(cache.struct()), ctypes.byref(sq), ctypes.byref(qs), *m,
+                             out.data_ptr(), os, None if lse is None else lse.data_ptr(), ws, nb,
+                             st), "sage_cache_attn")
     return (out, lse) if return_lse else out
 
 
@@ -524,8 +541,8 @@ def cache_evict(cache, pages, lengths, keep, sink=0, recent=0, pages_out=None, w
             raise ValueError("pages_out must be [B, at least %d]" % -(-keep // PAGE))
         width = pages_out.shape[1]
         po = _int32(pages_out, (sq.B, width), "pages_out", cache.index)
-    kept = torch.empty((sq.B, cache.kv_heads, keep), dtype=torch.int32, device=cache.device)
-    out = torch.empty((sq.B,), dtype=torch.int32, device=cache.device)
+    kept = lengths.new_empty((sq.B, cache.kv_heads, keep))
+    out = torch.empty_like(lengths)
     if sq.B == 0:
         return kept, out
     if po is None and workspace is None:
