@@ -79,7 +79,7 @@ int visited_pages(const CacheMask& m, int max_len, int tile_tokens) {
 // (four tiles a warp) each at least; a block a head where a head has no more.
 void plan_decode(long long units, int pages, int sms, int* chunks, int* whole) {
   *whole = pages <= 8;
-  *chunks = static_cast<int>(*whole ? units : std::min(2ll * sms, (units * pages + 7) / 8));
+  *chunks = static_cast<int>(*whole ? units : std::min(std::min<long long>(2ll * sms, kMaxShares), (units * pages + 7) / 8));
 }
 
 Plan plan_of(const CacheMask& m, int B, int Hkv, int G, int Nq, int D, int max_len, int sms) {

@@ -22,7 +22,7 @@ namespace sage {
 
 constexpr int kPage = 64;         // tokens per page
 constexpr int kMinVExp = -40;     // floor of v_exp (also that of an all-zero page)
-constexpr int kCacheChunksMax = 4096;  // KV ranges per query tile, at most
+constexpr int kMaxShares = 320;  // blocks that share a decode call's pages, at most
 
 enum { kTypeBf16 = 0, kTypeF16 = 1, kTypeF32 = 2 };
 

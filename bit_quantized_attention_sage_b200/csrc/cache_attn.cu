@@ -22,8 +22,8 @@
 // value scales need no multiplication.
 //
 // What bounds it: the codes, read once (2 D bytes a key and head).  Every
-// warp walks half pages of its own (32 keys) through a private ring of three
-// TMA loads (24 KB in flight a warp at D = 128, 192 KB an SM with two blocks),
+// warp walks half pages of its own (32 keys) through a private ring of two
+// TMA loads (16 KB in flight a warp at D = 128, 192 KB an SM with two blocks),
 // so no barrier joins the warps until the end.  Page ids, key scales and
 // value exponents of a warp's next 32 half pages are fetched at once, one a
 // lane; taken one by one inside the loop, their three dependent loads cost
@@ -44,8 +44,8 @@ namespace sage {
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kWarps = 4;
-constexpr int kStages = 3;
+constexpr int kWarps = 6;
+constexpr int kStages = 2;
 constexpr int kHalf = 32;      // keys a tile
 constexpr float kBoost = 7.0f;  // y = 2^7 at the reference maximum
 constexpr float kLazy = 8.0f;   // growth of the maximum that moves the reference
@@ -320,20 +320,25 @@ __device__ __forceinline__ void decode_head(DecSmem<D>& s, const CacheAttnMaps& 
   while (issued < min(mine, kStages)) issue();
   stage_limbs<D>(s, a, b, h, rows, ROWS);
   __syncthreads();
-  // B fragments of Q^T: channels 32 kk + 4 t .. + 3 and 16 on, of row g
-  uint32_t qb[NT][D / 32][3][2];
-  float f[NT][2];
-  KeyRange kr[NT][2];
-  float nl[NT][2];  // WEIGHTS: -lse log2(e); -inf: weight 0
-#pragma unroll
-  for (int n = 0; n < NT; n++) {
+  // B fragments of Q^T: channels 32 kk + 4 t .. + 3 and 16 on, of row g.  For
+  // 16 rows they stay in shared memory: 48 registers would spill.
+  auto q_frag = [&](int n, int kk, int x, int e) {
+    return *reinterpret_cast<const uint32_t*>(&s.q[x][n * 8 + g][kk * 32 + e * 16 + t * 4]);
+  };
+  uint32_t qb[D / 32][3][2];
+  if constexpr (NT == 1) {
 #pragma unroll
     for (int kk = 0; kk < D / 32; kk++)
 #pragma unroll
       for (int x = 0; x < 3; x++)
 #pragma unroll
-        for (int e = 0; e < 2; e++)
-          qb[n][kk][x][e] = *reinterpret_cast<const uint32_t*>(&s.q[x][n * 8 + g][kk * 32 + e * 16 + t * 4]);
+        for (int e = 0; e < 2; e++) qb[kk][x][e] = q_frag(0, kk, x, e);
+  }
+  float f[NT][2];
+  KeyRange kr[NT][2];
+  float nl[NT][2];  // WEIGHTS: -lse log2(e); -inf: weight 0
+#pragma unroll
+  for (int n = 0; n < NT; n++) {
 #pragma unroll
     for (int e = 0; e < 2; e++) {  // rows that this lane's columns are
       const int r = n * 8 + t * 2 + e;
@@ -395,30 +400,45 @@ __device__ __forceinline__ void decode_head(DecSmem<D>& s, const CacheAttnMaps& 
       }
       // scores of two tiles of 16 keys: keys g and g + 8, rows 2 t and 2 t + 1
       float sc[2][NT][4];
+      {
+        uint32_t ka[2][D / 32][4];  // keys 0-7 / 8-15 of chunk 2 kk, then of 2 kk + 1
 #pragma unroll
-      for (int mt = 0; mt < 2; mt++) {
-        int acc[NT][3][4];
+        for (int mt = 0; mt < 2; mt++)
 #pragma unroll
-        for (int n = 0; n < NT; n++)
+          for (int kk = 0; kk < D / 32; kk++)
+            ldsm4(kb + swz<D>(mt * 16 + (lane & 15), kk * 2 + (lane >> 4)), ka[mt][kk]);
+        int low[2][NT][4];  // the two lower limbs joined
 #pragma unroll
-          for (int x = 0; x < 3; x++)
+        for (int x = 0; x < 3; x++) {
+          int acc[2][NT][4];
 #pragma unroll
-            for (int e = 0; e < 4; e++) acc[n][x][e] = 0;
+          for (int mt = 0; mt < 2; mt++)
 #pragma unroll
-        for (int kk = 0; kk < D / 32; kk++) {
-          uint32_t ka[4];  // keys 0-7 / 8-15 of chunk 2 kk, then of 2 kk + 1
-          ldsm4(kb + swz<D>(mt * 16 + (lane & 15), kk * 2 + (lane >> 4)), ka);
+            for (int n = 0; n < NT; n++)
 #pragma unroll
-          for (int n = 0; n < NT; n++)
+              for (int e = 0; e < 4; e++) acc[mt][n][e] = 0;
 #pragma unroll
-            for (int x = 0; x < 3; x++) mma16832(acc[n][x], ka, qb[n][kk][x][0], qb[n][kk][x][1]);
+          for (int kk = 0; kk < D / 32; kk++)
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+              const uint32_t b0 = NT == 1 ? qb[kk][x][0] : q_frag(n, kk, x, 0);
+              const uint32_t b1 = NT == 1 ? qb[kk][x][1] : q_frag(n, kk, x, 1);
+#pragma unroll
+              for (int mt = 0; mt < 2; mt++) mma16832(acc[mt][n], ka[mt][kk], b0, b1);
+            }
+#pragma unroll
+          for (int mt = 0; mt < 2; mt++)
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+              for (int e = 0; e < 4; e++) {
+                if (x == 0) low[mt][n][e] = acc[mt][n][e];
+                else if (x == 1) low[mt][n][e] += acc[mt][n][e] * 256;
+                else
+                  sc[mt][n][e] = fmaf(static_cast<float>(acc[mt][n][e]), 65536.0f,
+                                      static_cast<float>(low[mt][n][e]));
+              }
         }
-#pragma unroll
-        for (int n = 0; n < NT; n++)
-#pragma unroll
-          for (int e = 0; e < 4; e++)
-            sc[mt][n][e] = fmaf(static_cast<float>(acc[n][2][e]), 65536.0f,
-                                static_cast<float>(acc[n][1][e] * 256 + acc[n][0][e]));
       }
       if (!(j0 + kHalf <= full_sink || (j0 >= full_lo && j0 + kHalf <= full_hi))) {
 #pragma unroll
@@ -663,96 +683,115 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   }
 }
 
-// Join of the heads that stretches cut, one block a head; threads (group,
-// row, 4 channels), the groups every GR-th partial in turn, summed in order.
+// Join of the heads that stretches cut, one block a head: first the factor of
+// every partial result (2^(its maximum - the largest)), a warp a row; then
+// threads (group, row, 4 channels), each group every so many-th partial, the
+// groups summed in order.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kWarps * 32) k_cache_join(const CacheAttnArgs a, int n) {
-  __shared__ PlaceSmem place;
-  __shared__ float4 sh_o[kWarps * 32];
-  __shared__ float sh_l[kWarps * 32];
-  cudaGridDependencySynchronize();  // launched under the attention kernel's tail
+  constexpr int NT = kWarps * 32, Q = D / 4;
+  __shared__ long long sum[2][kWarps];
+  __shared__ float fac[kMaxShares][ROWS];  // maximum, then factor
+  __shared__ float lsum[kMaxShares][ROWS];
+  __shared__ float tot[2][ROWS];           // largest maximum, joined sum
+  __shared__ float4 sh_o[NT];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv;
   const int np = seq_work<false>(a, b);
   if (np == 0) return;
-  // pages before b: locate a position of b, found by its own count
-  long long before = 0, work = 0;
-  {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long long sb = 0, sw = 0;
-    for (int i = tid; i < a.c.B; i += kWarps * 32) {
-      const int v = seq_work<false>(a, i);
-      sw += v;
-      if (i < b) sb += v;
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      sb += __shfl_xor_sync(kFull, sb, o);
-      sw += __shfl_xor_sync(kFull, sw, o);
-    }
-    if (lane == 0) place.sum[warp] = sb;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; w++) before += place.sum[w];
-    __syncthreads();
-    if (lane == 0) place.sum[warp] = sw;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; w++) work += place.sum[w];
-    work *= a.c.Hkv;
+  long long sb = 0, sw = 0;  // pages of one head before b, and in all
+  for (int i = tid; i < a.c.B; i += NT) {
+    const int v = seq_work<false>(a, i);
+    sw += v;
+    if (i < b) sb += v;
   }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    sb += __shfl_xor_sync(kFull, sb, o);
+    sw += __shfl_xor_sync(kFull, sw, o);
+  }
+  if (lane == 0) {
+    sum[0][warp] = sb;
+    sum[1][warp] = sw;
+  }
+  __syncthreads();
+  long long before = 0, work = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; w++) {
+    before += sum[0][w];
+    work += sum[1][w];
+  }
+  work *= a.c.Hkv;
   const long long x0 = before * a.c.Hkv + static_cast<long long>(h) * np;
   const int c0 = share_of(work, x0, n), c1 = share_of(work, x0 + np - 1, n);
   if (c0 == c1) return;  // one block had the whole head and wrote it
-  const int qn = query_len(a, b), rows = qn * a.G;
-  constexpr int Q = D / 4;
+  const int qn = query_len(a, b), rows = qn * a.G, k = c1 - c0 + 1;
+  cudaGridDependencySynchronize();  // launched under the attention kernel's tail
+  // the first partial of the head lies in slot 2 c + 1, the others in 2 c
+  auto slot = [&](int i) { return (2 * static_cast<size_t>(c0 + i) + (i == 0)) * ROWS; };
+  for (int i = tid; i < k * ROWS; i += NT) {
+    const int p = i / ROWS, r = i % ROWS;
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    // (a block without a page of its own wrote nothing)
+    if (r < rows && share_start(work, c0 + p, n) < share_start(work, c0 + p + 1, n))
+      ml = *reinterpret_cast<const float2*>(a.part_ml + (slot(p) + r) * 2);
+    fac[p][r] = ml.x;
+    lsum[p][r] = ml.y;
+  }
+  __syncthreads();
+  for (int r = warp; r < rows; r += kWarps) {
+    float mx = -INFINITY, ls = 0.0f;
+    for (int p = lane; p < k; p += 32) mx = fmaxf(mx, fac[p][r]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+    for (int p = lane; p < k; p += 32) {
+      const float al = fac[p][r] == -INFINITY ? 0.0f : ex2_approx(fac[p][r] - mx);
+      fac[p][r] = al;
+      ls = fmaf(al, lsum[p][r], ls);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ls += __shfl_xor_sync(kFull, ls, o);
+    if (lane == 0) {
+      tot[0][r] = mx;
+      tot[1][r] = ls;
+    }
+  }
+  __syncthreads();
   const int items = rows * Q;
-  const int groups = max(1, kWarps * 32 / items);
-  const bool split = groups > 1;
-  for (int it0 = 0; it0 < items; it0 += kWarps * 32) {
-    const int grp = split ? threadIdx.x / items : 0, it = split ? threadIdx.x % items : it0 + threadIdx.x;
+  const int groups = max(1, NT / items);
+  for (int it0 = 0; it0 < items; it0 += NT) {
+    const int grp = groups > 1 ? tid / items : 0, it = groups > 1 ? tid % items : it0 + tid;
     const bool live = grp < groups && it < items;
     const int r = live ? it / Q : 0, d = it % Q * 4;
-    float mx = -INFINITY, ls = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    auto slot = [&](int c) {
-      return (2 * static_cast<size_t>(c) + (c == c0)) * ROWS + r;
-    };
-    auto has = [&](int c) { return share_start(work, c, n) < share_start(work, c + 1, n); };
     if (live) {
-#pragma unroll 4
-      for (int c = c0; c <= c1; c++)
-        if (has(c)) mx = fmaxf(mx, a.part_ml[slot(c) * 2]);
-#pragma unroll 4
-      for (int c = c0 + grp; c <= c1; c += groups) {
-        if (!has(c)) continue;
-        const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + slot(c) * 2);
-        const float4 v = *reinterpret_cast<const float4*>(a.part_o + slot(c) * D + d);
-        const float al = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - mx);
-        ls = fmaf(al, ml.y, ls);
-        o = make_float4(fmaf(al, v.x, o.x), fmaf(al, v.y, o.y), fmaf(al, v.z, o.z), fmaf(al, v.w, o.w));
+#pragma unroll 8
+      for (int p = grp; p < k; p += groups) {
+        const float al = fac[p][r];
+        const float4 v = *reinterpret_cast<const float4*>(a.part_o + (slot(p) + r) * D + d);
+        if (al != 0.0f)  // (memory that no block wrote is not used)
+          o = make_float4(fmaf(al, v.x, o.x), fmaf(al, v.y, o.y), fmaf(al, v.z, o.z), fmaf(al, v.w, o.w));
       }
     }
-    if (split) {
-      sh_o[threadIdx.x] = o;
-      sh_l[threadIdx.x] = ls;
+    if (groups > 1) {
+      sh_o[tid] = o;
       __syncthreads();
       if (live && grp == 0) {
-        for (int k = 1; k < groups; k++) {
-          const float4 v = sh_o[k * items + it];
+        for (int x = 1; x < groups; x++) {
+          const float4 v = sh_o[x * items + it];
           o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
-          ls += sh_l[k * items + it];
         }
       }
     }
     if (!live || grp != 0) continue;
-    const float inv = ls > 0.0f ? 1.0f / ls : 0.0f;
+    const float ls = tot[1][r], inv = ls > 0.0f ? 1.0f / ls : 0.0f;
     const int tok = r / a.G, head = h * a.G + r % a.G;
     const size_t ob = a.ob * b + a.oh * head + a.on * tok + d;
     store_o2(a, ob, o.x * inv, o.y * inv);
     store_o2(a, ob + 2, o.z * inv, o.w * inv);
     if (d == 0 && a.lse)
       a.lse[(static_cast<size_t>(b) * a.H + head) * a.Nq + tok] =
-          ls > 0.0f ? (mx + log2f(ls)) * kLn2 : -INFINITY;
+          ls > 0.0f ? (tot[0][r] + log2f(ls)) * kLn2 : -INFINITY;
   }
 }
 
