@@ -34,6 +34,7 @@ namespace {
 
 constexpr int BM = 128, BN = 128;
 constexpr int kThreads = 512;
+constexpr int kConvert = 128;  // of these
 constexpr int NS = 2;
 constexpr float kBoost = 7.0f;   // y = 2^7 at the reference maximum
 constexpr float kLazy = 8.0f;    // growth of the maximum that forces a rescale
@@ -44,12 +45,20 @@ static_assert(kRegsSoftmax * 256 + kRegsConvert * 128 + kRegsIssue * 128 <= 6553
 enum : int { kSitePreKEmpty = 0x20201, kSitePreVEmpty, kSitePreK, kSitePreV, kSitePreP, kSitePreS,
              kSitePreDrain };
 
+// A KV tile's two pages: first key (-1: no page), key scale, value exponent.
+struct TileMeta {
+  int j0[2];
+  float ks[2];
+  int ve[2];
+};
+
 template <int D>
 struct alignas(1024) PreSmem {
   uint8_t q[2][BM * D * 2];   // fp16 [D / 64][128 rows][128 bytes], 128-byte swizzle
   uint8_t k[NS][BN * D * 2];  // the same over keys (K-major B operand)
   uint8_t v[NS][BN * D * 2];  // the same (MN-major B operand)
   float rowf[2 * BM];
+  TileMeta meta[4];  // of KV tile it in slot it % 4
   uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
   uint64_t s_full[2], p_full[2], drain;
   uint32_t tmem_base;
@@ -82,46 +91,72 @@ __device__ __forceinline__ void set_regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// The KV tile's pages: run entries 2 i and 2 i + 1 of the block's pages.
-struct Group {
-  int j0;    // first key, or -1: no such page (all its keys masked)
-  int unit;  // (page, head) index
+// ---------------------------------------------------------------- converters
+
+// Lane l of a converter warp holds page l of the next 32 (16 KV tiles).
+struct PageOf {
+  int j0, unit, ve;
+  float ks;
 };
-__device__ __forceinline__ Group group_of(const CacheAttnArgs& a, const PageRuns& runs, int b, int h,
-                                          int i, int end) {
-  Group g{-1, 0};
+__device__ __forceinline__ PageOf page_of(const CacheAttnArgs& a, const PageRuns& runs, int b, int h, int i,
+                                          int end) {
+  PageOf p{-1, 0, 0, 0.0f};
   if (i < end) {
     const int blk = runs.page(i);
     const int pg = __ldg(a.c.pages + static_cast<size_t>(b) * a.c.max_pages + blk);
     if (static_cast<unsigned>(pg) < static_cast<unsigned>(a.c.n_pages)) {
-      g.j0 = blk * kPage;
-      g.unit = pg * a.c.Hkv + h;
+      p.j0 = blk * kPage;
+      p.unit = pg * a.c.Hkv + h;
+      p.ks = __ldg(a.c.k_scale + p.unit);
+      p.ve = __ldg(a.c.v_exp + p.unit);
     }
   }
-  return g;
+  return p;
 }
 
-// ---------------------------------------------------------------- converters
-
+// A converter thread's chunks (16 codes) of a KV tile: chunk column c and rows
+// row0 + i * STEP.  Eight neighbouring lanes take four chunks of two rows, so
+// that their 16-byte stores hit eight different banks (rows r and r + 1 swizzle
+// to the other half of the banks); a warp still reads whole rows.
 template <int D>
-__device__ __forceinline__ void load_codes(uint4 (&r)[D / 16], const uint8_t* codes, const Group (&g)[2],
-                                           int tid) {
+struct Chunks {
+  static constexpr int CH = D / 16, N = D / 16, STEP = BN / N;
+  static_assert(N * STEP == BN && kConvert * N == BN * CH, "every chunk has its thread");
+  int c, row0;
+  uint32_t off0, off1;  // of chunks 2 c and 2 c + 1 of row0 in an operand tile
+  __device__ __forceinline__ explicit Chunks(int tid) {
+    const int lane = tid & 31, w = tid >> 5;
+    if (D == 128) {
+      c = (lane & 3) | ((lane >> 1) & 4);
+      row0 = w * 4 + ((lane >> 2) & 1) + ((lane >> 3) & 2);
+    } else {
+      c = lane & 3;
+      row0 = w * 8 + (lane >> 2);
+    }
+    off0 = op_off(row0, 2 * c);
+    off1 = op_off(row0, 2 * c + 1);
+  }
+};
+template <int D>
+__device__ __forceinline__ void load_codes(uint4 (&r)[D / 16], const uint8_t* codes, const Chunks<D>& ch,
+                                           const int (&unit)[2], const int (&j0)[2]) {
+  constexpr int N = Chunks<D>::N, STEP = Chunks<D>::STEP;
 #pragma unroll
-  for (int i = 0; i < D / 16; i++) {
-    const int row = tid / (D / 16) + i * (2048 / D), c = tid % (D / 16);
-    const Group& x = g[i / (D / 32)];
-    r[i] = x.j0 < 0 ? make_uint4(0u, 0u, 0u, 0u)
-                    : __ldg(reinterpret_cast<const uint4*>(
-                          codes + (static_cast<size_t>(x.unit) * kPage + (row & 63)) * D + c * 16));
+  for (int g = 0; g < 2; g++) {
+    const uint8_t* p = codes + static_cast<size_t>(unit[g]) * (kPage * D) + ch.row0 * D + ch.c * 16;
+#pragma unroll
+    for (int i = 0; i < N / 2; i++)
+      r[g * (N / 2) + i] = j0[g] < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                                     : __ldg(reinterpret_cast<const uint4*>(p + i * STEP * D));
   }
 }
 // 16 codes to 16 fp16 values, two chunks of a row.
 template <int D, bool VALUES>
-__device__ __forceinline__ void store_codes(uint8_t* tile, const uint4 (&r)[D / 16], const Group (&g)[2],
-                                            int len, int tid) {
+__device__ __forceinline__ void store_codes(uint8_t* tile, const uint4 (&r)[D / 16], const Chunks<D>& ch,
+                                            const int (&j0)[2], int len) {
+  constexpr int N = Chunks<D>::N, STEP = Chunks<D>::STEP;
 #pragma unroll
-  for (int i = 0; i < D / 16; i++) {
-    const int row = tid / (D / 16) + i * (2048 / D), c = tid % (D / 16);
+  for (int i = 0; i < N; i++) {
     const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
     uint32_t o[8];
     if constexpr (VALUES) {
@@ -131,7 +166,8 @@ __device__ __forceinline__ void store_codes(uint8_t* tile, const uint4 (&r)[D / 
             "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
             : "=r"(o[2 * j]), "=r"(o[2 * j + 1]) : "r"(w[j]));
       // values behind the sequence's end may be any bytes, NaN among them
-      if (g[i / (D / 32)].j0 + (row & 63) >= len) {
+      const int g = i / (N / 2);
+      if (j0[g] + kPage > len && j0[g] + ch.row0 + (i % (N / 2)) * STEP >= len) {
 #pragma unroll
         for (int j = 0; j < 8; j++) o[j] = 0u;
       }
@@ -139,36 +175,64 @@ __device__ __forceinline__ void store_codes(uint8_t* tile, const uint4 (&r)[D / 
 #pragma unroll
       for (int j = 0; j < 4; j++) i8x4_to_f16(w[j], o[2 * j], o[2 * j + 1]);
     }
-    store_pair<D>(tile, row, c, o);
+    *reinterpret_cast<uint4*>(tile + ch.off0 + i * STEP * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(tile + ch.off1 + i * STEP * 128) = make_uint4(o[4], o[5], o[6], o[7]);
   }
 }
 
 template <int D>
 __device__ __forceinline__ void convert(PreSmem<D>& s, const CacheAttnArgs& a, const PageRuns& runs, int b,
                                         int h, int p0, int p1, int nk, int len, const WaitCtx& w) {
-  const int tid = threadIdx.x & 127;
+  constexpr uint32_t kFull = 0xffffffffu;
+  const int tid = threadIdx.x & (kConvert - 1), lane = tid & 31;
+  const Chunks<D> ch(tid);
   const uint8_t* kc = reinterpret_cast<const uint8_t*>(a.c.k_i8);
+  PageOf cur = page_of(a, runs, b, h, p0 + lane, p1);
   uint4 kr[D / 16], vr[D / 16];
-  Group g[2] = {group_of(a, runs, b, h, p0, p1), group_of(a, runs, b, h, p0 + 1, p1)};
-  load_codes<D>(kr, kc, g, tid);
-  load_codes<D>(vr, a.c.v_f8, g, tid);
+  int unit[2], j0[2];
+#pragma unroll
+  for (int g = 0; g < 2; g++) {
+    unit[g] = __shfl_sync(kFull, cur.unit, g);
+    j0[g] = __shfl_sync(kFull, cur.j0, g);
+  }
+  load_codes<D>(kr, kc, ch, unit, j0);
+  load_codes<D>(vr, a.c.v_f8, ch, unit, j0);
   for (int it = 0; it < nk; it++) {
-    const int st = it % NS;
+    const int st = it % NS, at = (2 * it) & 31;
     const uint32_t ph = ((it / NS) & 1) ^ 1;
-    const Group n[2] = {group_of(a, runs, b, h, p0 + 2 * it + 2, p1),
-                        group_of(a, runs, b, h, p0 + 2 * it + 3, p1)};
-    if (it >= NS && !__all_sync(0xffffffffu, mbar_wait(&s.k_empty[st], ph, w, kSitePreKEmpty))) return;
-    store_codes<D, false>(s.k[st], kr, g, len, tid);
+    if (it >= NS && !__all_sync(kFull, mbar_wait(&s.k_empty[st], ph, w, kSitePreKEmpty))) return;
+    store_codes<D, false>(s.k[st], kr, ch, j0, len);
+    // the tile's page data for the softmax.  Slot it % 4 was last read by the
+    // softmax of tile it - 4, whose P went into a product issued before the
+    // S of tile it - 2 that k_empty has just reported.
+    if (tid < 32 && (lane & ~1) == at) {
+      TileMeta& m = s.meta[it & 3];
+      m.j0[lane & 1] = cur.j0;
+      m.ks[lane & 1] = cur.ks;
+      m.ve[lane & 1] = cur.ve;
+    }
     fence_proxy_async_smem();
-    mbar_arrive(&s.k_full[st]);
-    load_codes<D>(kr, kc, n, tid);
-    if (it >= NS && !__all_sync(0xffffffffu, mbar_wait(&s.v_empty[st], ph, w, kSitePreVEmpty))) return;
-    store_codes<D, true>(s.v[st], vr, g, len, tid);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.k_full[st]);
+    int un[2], jn[2];
+    if (at == 30) cur = page_of(a, runs, b, h, p0 + 2 * it + 2 + lane, p1);
+#pragma unroll
+    for (int g = 0; g < 2; g++) {
+      un[g] = __shfl_sync(kFull, cur.unit, (at + 2 + g) & 31);
+      jn[g] = __shfl_sync(kFull, cur.j0, (at + 2 + g) & 31);
+    }
+    load_codes<D>(kr, kc, ch, un, jn);
+    if (it >= NS && !__all_sync(kFull, mbar_wait(&s.v_empty[st], ph, w, kSitePreVEmpty))) return;
+    store_codes<D, true>(s.v[st], vr, ch, j0, len);
     fence_proxy_async_smem();
-    mbar_arrive(&s.v_full[st]);
-    load_codes<D>(vr, a.c.v_f8, n, tid);
-    g[0] = n[0];
-    g[1] = n[1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.v_full[st]);
+    load_codes<D>(vr, a.c.v_f8, ch, un, jn);
+#pragma unroll
+    for (int g = 0; g < 2; g++) {
+      unit[g] = un[g];
+      j0[g] = jn[g];
+    }
   }
 }
 
@@ -248,35 +312,20 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
   KeyRange kr{0, 0, 0};
   if (valid) kr = key_range(a.mask, off + row / a.G, len);
   float m = -INFINITY, l = 0.0f;
-  Group g[2];
-  float ks[2];
-  int ve[2];
-  auto meta = [&](int it, Group (&x)[2], float (&k)[2], int (&e)[2]) {
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-      x[i] = group_of(a, runs, b, h, p0 + 2 * it + i, p1);
-      k[i] = x[i].j0 < 0 ? 0.0f : __ldg(a.c.k_scale + x[i].unit);
-      e[i] = x[i].j0 < 0 ? 0 : __ldg(a.c.v_exp + x[i].unit);
-    }
-  };
-  meta(0, g, ks, ve);
   bool ok = true;
   for (int it = 0; it < nk; it++) {
-    Group gn[2];
-    float kn[2];
-    int en[2];
-    meta(it + 1, gn, kn, en);  // the next tile's, under this one's work
     ok = __all_sync(kFull, mbar_wait(&s.s_full[t], it & 1, w, kSitePreS));
     if (!ok) break;
     tc_fence_after();
+    const TileMeta md = s.meta[it & 3];
     uint32_t sv[128];
     tmem_ld128(tS, sv);
     // a zero scale must not meet -inf as 0 * inf
-    const float c[2] = {fmaxf(f * ks[0], FLT_MIN), fmaxf(f * ks[1], FLT_MIN)};
+    const float c[2] = {fmaxf(f * md.ks[0], FLT_MIN), fmaxf(f * md.ks[1], FLT_MIN)};
     float tm[2];
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-      const int j0 = g[i].j0;
+      const int j0 = md.j0[i];
       const bool all = j0 >= 0 && (kr.sink >= j0 + kPage || (kr.lo <= j0 && kr.hi >= j0 + kPage));
       if (!__all_sync(kFull, all)) {
         const int na = j0 < 0 ? 0 : min(max(kr.sink - j0, 0), kPage);
@@ -297,7 +346,7 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
         x[e] = fmaxf(x[e], __uint_as_float(sv[j + 7]));
       }
       tm[i] = fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
-      tm[i] = fmaf(tm[i], c[i], static_cast<float>(ve[i]));
+      tm[i] = fmaf(tm[i], c[i], static_cast<float>(md.ve[i]));
     }
     const float mx = fmaxf(tm[0], tm[1]);
     if (__any_sync(kFull, mx > m + kLazy)) {
@@ -321,7 +370,7 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
     const float base = m == -INFINITY ? 0.0f : kBoost - m;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-      const float nm = base + static_cast<float>(ve[i]);
+      const float nm = base + static_cast<float>(md.ve[i]);
       const float2 cc = make_float2(c[i], c[i]), nn = make_float2(nm, nm);
       float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
@@ -335,7 +384,7 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
         sv[i * 32 + j] = *reinterpret_cast<const uint32_t*>(&y);
       }
       const float2 sum = __fadd2_rn(acc[0], acc[1]);
-      l = fmaf(sum.x + sum.y, pow2i(min(-ve[i], 127)), l);
+      l = fmaf(sum.x + sum.y, pow2i(min(-md.ve[i], 127)), l);
     }
     uint32_t pk[64];
 #pragma unroll
@@ -345,12 +394,6 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.p_full[t]);
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-      g[i] = gn[i];
-      ks[i] = kn[i];
-      ve[i] = en[i];
-    }
   }
   if (!ok) return;
   if (nk > 0) {
@@ -447,9 +490,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_prefill(const CacheAttnAr
 
   if (threadIdx.x == 0) {
     for (int j = 0; j < NS; j++) {
-      mbar_init(&s.k_full[j], 128);
+      mbar_init(&s.k_full[j], kConvert / 32);
       mbar_init(&s.k_empty[j], 1);
-      mbar_init(&s.v_full[j], 128);
+      mbar_init(&s.v_full[j], kConvert / 32);
       mbar_init(&s.v_empty[j], 1);
     }
     for (int j = 0; j < 2; j++) {
