@@ -309,7 +309,9 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
   const uint32_t lo = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t tS = tmem + t * BN + lo, tO = tmem + 2 * BN + t * D + lo;
   const float f = s.rowf[r] * (a.scale * kLog2e);
-  KeyRange kr{0, 0, 0};
+  // a row that is not there sees every key (its scores are 0) and is never
+  // stored: masked, it would send its whole warp through the masking code
+  KeyRange kr{0, 0, 0x7FFFFFFF};
   if (valid) kr = key_range(a.mask, off + row / a.G, len);
   float m = -INFINITY, l = 0.0f;
   bool ok = true;
