@@ -5,9 +5,10 @@
 // and walks KV tiles of 128 keys (two pages).  16 warps:
 //   0-3, 4-7   softmax of tile 0 and 1, a thread a row: S from TMEM, running
 //              maximum, y = 2^(t + e - M + 7), fp16(y) back into the TMEM
-//              columns of S, where the second product reads it as operand A.
-//              O is rescaled only when a row's maximum grew by more than 2^8
-//              since its last rescale (y <= 2^15 then still fits fp16).
+//              columns of S, where the second product reads it as operand A,
+//              64 keys at a time.  M moves, and O is rescaled, only when a
+//              row's maximum grew by more than 2^8 (y <= 2^15 then still fits
+//              fp16), so a tile's maximum is off the path to its exponentials.
 //   8-11       codes from global memory to fp16 operands in shared memory, in
 //              the 128-byte swizzle the tensor core reads; K exactly, V
 //              exactly, the next tile's codes already in flight in registers.
@@ -60,7 +61,7 @@ struct alignas(1024) PreSmem {
   float rowf[2 * BM];
   TileMeta meta[4];  // of KV tile it in slot it % 4
   uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
-  uint64_t s_full[2], p_full[2], drain;
+  uint64_t s_full[2], p_full[2][2], drain;  // p_full[tile][half]: P of 64 keys
   uint32_t tmem_base;
   int abort;
 };
@@ -79,6 +80,16 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdes
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 
@@ -243,12 +254,14 @@ __device__ __forceinline__ void issue_qk(PreSmem<D>& s, int w, uint32_t tS, int 
   mma_rows<D>(tS, smem_u32(s.q[w]), smem_u32(s.k[st]), idesc_f16(BM, BN));
 }
 template <int D>
-__device__ __forceinline__ void issue_pv(PreSmem<D>& s, uint32_t tP, uint32_t tO, int st, bool first) {
+__device__ __forceinline__ void issue_pv(PreSmem<D>& s, uint32_t tP, uint32_t tO, int st, int half, bool first) {
   constexpr uint32_t id = idesc_f16(BM, D) | kIdescBMajorMN;
   const uint32_t va = smem_u32(s.v[st]);
 #pragma unroll
-  for (int kk = 0; kk < BN / 16; kk++)
+  for (int k = 0; k < BN / 32; k++) {
+    const int kk = half * (BN / 32) + k;
     mma_f16_ts(tO, tP + kk * 8, desc_mn16(va + kk * 2048, 128 * 128), id, !first || kk > 0);
+  }
 }
 
 template <int D>
@@ -267,10 +280,13 @@ __device__ __forceinline__ void issue(PreSmem<D>& s, uint32_t tmem, int nk, int 
     const bool more = it + 1 < nk;
     ok = mbar_wait(&s.v_full[st], (it / NS) & 1, w, kSitePreV);
     for (int t = 0; ok && t < tiles; t++) {
-      ok = mbar_wait(&s.p_full[t], it & 1, w, kSitePreP);
+      for (int half = 0; ok && half < 2; half++) {
+        ok = mbar_wait(&s.p_full[t][half], it & 1, w, kSitePreP);
+        if (!ok) break;
+        tc_fence_after();
+        issue_pv<D>(s, tmem + t * BN, tmem + 2 * BN + t * D, st, half, it == 0);
+      }
       if (!ok) break;
-      tc_fence_after();
-      issue_pv<D>(s, tmem + t * BN, tmem + 2 * BN + t * D, st, it == 0);
       if (t == tiles - 1) mma_commit(&s.v_empty[st]);
       if (more) {
         if (t == 0) {
@@ -320,11 +336,11 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
     if (!ok) break;
     tc_fence_after();
     const TileMeta md = s.meta[it & 3];
-    uint32_t sv[128];
-    tmem_ld128(tS, sv);
     // a zero scale must not meet -inf as 0 * inf
     const float c[2] = {fmaxf(f * md.ks[0], FLT_MIN), fmaxf(f * md.ks[1], FLT_MIN)};
-    float tm[2];
+    const float ve[2] = {static_cast<float>(md.ve[0]), static_cast<float>(md.ve[1])};
+    uint32_t sv[128];
+    tmem_ld128(tS, sv);
 #pragma unroll
     for (int i = 0; i < 2; i++) {
       const int j0 = md.j0[i];
@@ -338,21 +354,36 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
         for (int j = 0; j < kPage; j++)
           sv[i * 64 + j] = (j < na || static_cast<uint32_t>(j - nb) < nbc) ? sv[i * 64 + j] : kNegInf;
       }
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 8; e++) {
-        const int j = i * 64 + e * 8;
-        x[e] = fmax3(__uint_as_float(sv[j]), __uint_as_float(sv[j + 1]), __uint_as_float(sv[j + 2]));
-        x[e] = fmax3(x[e], __uint_as_float(sv[j + 3]), __uint_as_float(sv[j + 4]));
-        x[e] = fmax3(x[e], __uint_as_float(sv[j + 5]), __uint_as_float(sv[j + 6]));
-        x[e] = fmaxf(x[e], __uint_as_float(sv[j + 7]));
-      }
-      tm[i] = fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
-      tm[i] = fmaf(tm[i], c[i], static_cast<float>(md.ve[i]));
     }
-    const float mx = fmaxf(tm[0], tm[1]);
-    if (__any_sync(kFull, mx > m + kLazy)) {
-      const float mn = fmaxf(m, mx);
+    // The exponentials of the first half start at once, against the reference
+    // maximum in hand, and the tile's maximum is taken beside them (its
+    // instructions fit between those of the MUFU).  Only if that has grown by
+    // more than 2^8, or is the row's first, is the half done again.
+    float mx[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
+    float sum;
+    {
+      const float nm = (m == -INFINITY ? 0.0f : kBoost - m) + ve[0];
+      float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+      const float2 cc = make_float2(c[0], c[0]), nn = make_float2(nm, nm);
+#pragma unroll
+      for (int j = 0; j < 32; j++) {
+        const float s0 = __uint_as_float(sv[2 * j]), s1 = __uint_as_float(sv[2 * j + 1]);
+        float2 x = __ffma2_rn(make_float2(s0, s1), cc, nn);
+        x.x = ex2_approx(x.x);
+        x.y = ex2_approx(x.y);
+        mx[0][j & 1] = fmax3(mx[0][j & 1], s0, s1);
+        mx[1][j & 1] = fmax3(mx[1][j & 1], __uint_as_float(sv[64 + 2 * j]), __uint_as_float(sv[65 + 2 * j]));
+        acc[j & 1] = __fadd2_rn(acc[j & 1], x);
+        const __half2 y = __floats2half2_rn(x.x, x.y);
+        sv[j] = *reinterpret_cast<const uint32_t*>(&y);
+      }
+      const float2 a2 = __fadd2_rn(acc[0], acc[1]);
+      sum = a2.x + a2.y;
+    }
+    const float top = fmaxf(fmaf(fmaxf(mx[0][0], mx[0][1]), c[0], ve[0]),
+                            fmaf(fmaxf(mx[1][0], mx[1][1]), c[1], ve[1]));
+    if (__any_sync(kFull, top > m + kLazy)) {
+      const float mn = fmaxf(m, top);
       const float al = mn == m ? 1.0f : ex2_approx(m - mn);  // 0 from -inf
       // O holds the sum of the tiles before: its last product completed
       // before s_full did
@@ -368,34 +399,59 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
       }
       l *= al;
       m = mn;
-    }
-    const float base = m == -INFINITY ? 0.0f : kBoost - m;
+      const float nm = (m == -INFINITY ? 0.0f : kBoost - m) + ve[0];
+      sum = 0.0f;
+      // S is still in TMEM; P of 32 keys takes the columns of the 16 before
+#pragma unroll 1
+      for (int k = 0; k < kPage; k += 32) {
+        uint32_t x[32], y[16];
+        tmem_ld32(tS + k, x);
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-      const float nm = base + static_cast<float>(md.ve[i]);
-      const float2 cc = make_float2(c[i], c[i]), nn = make_float2(nm, nm);
+        for (int e = 0; e < 32; e++) {
+          const int j = md.j0[0] + k + e;
+          const bool see = md.j0[0] >= 0 && (j < kr.sink || (j >= kr.lo && j < kr.hi));
+          const float v = see ? ex2_approx(fmaf(__uint_as_float(x[e]), c[0], nm)) : 0.0f;
+          sum += v;
+          x[e] = __float_as_uint(v);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; e++) {
+          const __half2 h2 = __floats2half2_rn(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+          y[e] = *reinterpret_cast<const uint32_t*>(&h2);
+        }
+        tmem_st16(tS + k / 2, y);
+      }
+    } else {
+      uint32_t pk[32];
+#pragma unroll
+      for (int j = 0; j < 32; j++) pk[j] = sv[j];
+      tmem_st32(tS, pk);
+    }
+    l = fmaf(sum, pow2i(min(-md.ve[0], 127)), l);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.p_full[t][0]);
+    {
+      const float base = m == -INFINITY ? 0.0f : kBoost - m;
       float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+      const float2 cc = make_float2(c[1], c[1]), nn = make_float2(base + ve[1], base + ve[1]);
+      uint32_t pk[32];
 #pragma unroll
       for (int j = 0; j < 32; j++) {
-        const int at = i * 64 + j * 2;
-        float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1])), cc, nn);
+        float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[64 + 2 * j]), __uint_as_float(sv[65 + 2 * j])), cc, nn);
         x.x = ex2_approx(x.x);
         x.y = ex2_approx(x.y);
         acc[j & 1] = __fadd2_rn(acc[j & 1], x);
         const __half2 y = __floats2half2_rn(x.x, x.y);
-        sv[i * 32 + j] = *reinterpret_cast<const uint32_t*>(&y);
+        pk[j] = *reinterpret_cast<const uint32_t*>(&y);
       }
-      const float2 sum = __fadd2_rn(acc[0], acc[1]);
-      l = fmaf(sum.x + sum.y, pow2i(min(-md.ve[i], 127)), l);
+      tmem_st32(tS + 32, pk);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.p_full[t][1]);
+      const float2 a2 = __fadd2_rn(acc[0], acc[1]);
+      l = fmaf(a2.x + a2.y, pow2i(min(-md.ve[1], 127)), l);
     }
-    uint32_t pk[64];
-#pragma unroll
-    for (int j = 0; j < 64; j++) pk[j] = sv[j];
-    tmem_st64_nowait(tS, pk);
-    tmem_wait_st();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&s.p_full[t]);
   }
   if (!ok) return;
   if (nk > 0) {
@@ -499,7 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_prefill(const CacheAttnAr
     }
     for (int j = 0; j < 2; j++) {
       mbar_init(&s.s_full[j], 1);
-      mbar_init(&s.p_full[j], 4);
+      mbar_init(&s.p_full[j][0], 4);
+      mbar_init(&s.p_full[j][1], 4);
     }
     mbar_init(&s.drain, 1);
     s.abort = 0;
