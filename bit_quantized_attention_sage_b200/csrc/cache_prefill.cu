@@ -2,21 +2,26 @@
 // rows (prompts, latent frames): the arithmetic of cache_attn.cu on tcgen05.
 //
 // A block owns 256 query rows of one (sequence, key head), two tiles of 128,
-// and walks KV tiles of 128 keys (two pages).  16 warps:
-//   0-3, 4-7   softmax of tile 0 and 1, a thread a row: S from TMEM, running
-//              maximum, y = 2^(t + e - M + 7), fp16(y) back into the TMEM
-//              columns of S, where the second product reads it as operand A,
-//              64 keys at a time.  M moves, and O is rescaled, only when a
-//              row's maximum grew by more than 2^8 (y <= 2^15 then still fits
-//              fp16), so a tile's maximum is off the path to its exponentials.
+// and walks KV tiles of 128 keys (two pages), the scores page by page.  16
+// warps:
+//   0-3, 4-7   softmax of tile 0 and 1, a thread a row: a page's 64 scores
+//              from TMEM, y = 2^(t + e - M + 7), fp16(y) back into the TMEM
+//              columns of the scores, where the second product reads it as
+//              operand A.  M moves, and O is rescaled, only when a row's
+//              maximum grew by more than 2^8 (y <= 2^15 then still fits
+//              fp16), so a page's maximum is off the path to its exponentials.
 //   8-11       codes from global memory to fp16 operands in shared memory, in
 //              the 128-byte swizzle the tensor core reads; K exactly, V
 //              exactly, the next tile's codes already in flight in registers.
-//   12         issues every tcgen05.mma: for each tile in turn O += P V of
-//              one KV tile and S = Q K^T of the next, so one tile's products
-//              run under the other's softmax.
+//   12         issues every tcgen05.mma: O += P V of page u, then S = Q K^T of
+//              page u + 2 into the columns that P has left.  A tile has two
+//              score buffers (2 x 64 columns, and 128 of O: two tiles fill the
+//              512), so the products of one page run under the softmax of the
+//              next; with one buffer of 128 keys the chain S, softmax, P V was
+//              serial and a KV tile took 5200 clocks.
 // What bounds it: 4 D flops a (row, key) on the fp16 tensor pipe and one exp2
-// on the MUFU take the same 2048 clocks a KV tile at D = 128.  fp16 operands
+// on the MUFU take the same 2048 clocks a KV tile at D = 128, and shared
+// memory (64-key score tiles read Q twice as often) 2560.  fp16 operands
 // rather than the codes' own 8-bit kinds: Q is not quantized, and an int8 or
 // e4m3 product would need it (and P) in two limbs or more, the same tensor
 // time without the exactness.  256 rows a block halve the conversions per
@@ -34,15 +39,12 @@ namespace sage {
 namespace {
 
 constexpr int BM = 128, BN = 128;
+constexpr int kTileCols = 256;   // TMEM columns of a row tile: S 0-63, S 64-127, O from 128
 constexpr int kThreads = 512;
 constexpr int kConvert = 128;  // of these
 constexpr int NS = 2;
 constexpr float kBoost = 7.0f;   // y = 2^7 at the reference maximum
 constexpr float kLazy = 8.0f;    // growth of the maximum that forces a rescale
-constexpr int kRegsSoftmax = 184, kRegsConvert = 104, kRegsIssue = 40;
-static_assert(kRegsSoftmax * 256 + kRegsConvert * 128 + kRegsIssue * 128 <= 65536,
-              "register split within the launch's share");
-
 enum : int { kSitePreKEmpty = 0x20201, kSitePreVEmpty, kSitePreK, kSitePreV, kSitePreP, kSitePreS,
              kSitePreDrain };
 
@@ -61,17 +63,29 @@ struct alignas(1024) PreSmem {
   float rowf[2 * BM];
   TileMeta meta[4];  // of KV tile it in slot it % 4
   uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
-  uint64_t s_full[2], p_full[2][2], drain;  // p_full[tile][half]: P of 64 keys
+  // s_full[tile][u & 1]: S of page u (and P V of page u - 2); p_full[tile][u & 1]:
+  // P of page u.  A warp may be a page ahead of the others of its tile, never
+  // two, so each buffer counts its own arrivals.
+  uint64_t s_full[2][2], p_full[2][2], drain;
   uint32_t tmem_base;
   int abort;
 };
 
-// MN-major operand of 16-bit elements, 128-byte swizzle: N in runs of 64
-// (128 bytes), `lbo` bytes from run to run; groups of 8 K rows 1024 bytes
-// apart.
-__device__ __forceinline__ uint64_t desc_mn16(uint32_t saddr, uint32_t lbo) {
-  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(lbo >> 4) << 16) |
-         (64ull << 32) | (1ull << 46) | (2ull << 61);
+// The fixed upper words of the operand descriptors (128-byte swizzle, 8-row
+// groups 1024 bytes apart); the lower word holds the address / 16 and the
+// leading offset: unused (1) for K-major tiles, from run to run of 64 channels
+// (16 KB) for the MN-major V.
+constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29);
+constexpr uint32_t kDescLoK = 1u << 16, kDescLoV = (16384u >> 4) << 16;
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(kDescHi));
+  return d;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 // D[tmem] (+)= A[tmem] B[smem], f16 operands, fp32 accumulator.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
@@ -91,15 +105,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
-}
-
-template <int N>
-__device__ __forceinline__ void set_regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void set_regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // ---------------------------------------------------------------- converters
@@ -214,8 +219,8 @@ __device__ __forceinline__ void convert(PreSmem<D>& s, const CacheAttnArgs& a, c
     if (it >= NS && !__all_sync(kFull, mbar_wait(&s.k_empty[st], ph, w, kSitePreKEmpty))) return;
     store_codes<D, false>(s.k[st], kr, ch, j0, len);
     // the tile's page data for the softmax.  Slot it % 4 was last read by the
-    // softmax of tile it - 4, whose P went into a product issued before the
-    // S of tile it - 2 that k_empty has just reported.
+    // softmax of tile it - 4: k_empty has just reported the S of tile it - 2,
+    // which was issued after the P of tile it - 3's first page.
     if (tid < 32 && (lane & ~1) == at) {
       TileMeta& m = s.meta[it & 3];
       m.j0[lane & 1] = cur.j0;
@@ -249,66 +254,86 @@ __device__ __forceinline__ void convert(PreSmem<D>& s, const CacheAttnArgs& a, c
 
 // ---------------------------------------------------------------- tensor core
 
+// S = Q K^T of one page (64 keys): q and k are the operands' lower words.
 template <int D>
-__device__ __forceinline__ void issue_qk(PreSmem<D>& s, int w, uint32_t tS, int st) {
-  mma_rows<D>(tS, smem_u32(s.q[w]), smem_u32(s.k[st]), idesc_f16(BM, BN));
-}
-template <int D>
-__device__ __forceinline__ void issue_pv(PreSmem<D>& s, uint32_t tP, uint32_t tO, int st, int half, bool first) {
-  constexpr uint32_t id = idesc_f16(BM, D) | kIdescBMajorMN;
-  const uint32_t va = smem_u32(s.v[st]);
+__device__ __forceinline__ void issue_qk(uint32_t tS, uint32_t q, uint32_t k) {
+  constexpr uint32_t id = idesc_f16(BM, kPage);
 #pragma unroll
-  for (int k = 0; k < BN / 32; k++) {
-    const int kk = half * (BN / 32) + k;
-    mma_f16_ts(tO, tP + kk * 8, desc_mn16(va + kk * 2048, 128 * 128), id, !first || kk > 0);
+  for (int kk = 0; kk < D / 16; kk++) {
+    const uint32_t off = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
+    mma_f16_ss(tS, desc_of(q + off), desc_of(k + off), id, kk > 0);
   }
+}
+// O (+)= P V of one page.
+template <int D>
+__device__ __forceinline__ void issue_pv(uint32_t tP, uint32_t tO, uint32_t v, bool first) {
+  constexpr uint32_t id = idesc_f16(BM, D) | kIdescBMajorMN;
+#pragma unroll
+  for (int kk = 0; kk < kPage / 16; kk++)
+    mma_f16_ts(tO, tP + kk * 8, desc_of(v + kk * (2048 >> 4)), id, kk > 0 ? 1u : (first ? 0u : 1u));
 }
 
+// By a whole warp, one elected lane of which issues: the waits and the
+// operands' addresses then stay uniform (a single-lane branch around all of it
+// took 90 clocks a product, most of them moves to uniform registers).
 template <int D>
 __device__ __forceinline__ void issue(PreSmem<D>& s, uint32_t tmem, int nk, int tiles, const WaitCtx& w) {
-  bool ok = mbar_wait(&s.k_full[0], 0, w, kSitePreK);
+  constexpr uint32_t kFull = 0xffffffffu;
+  auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
+    return __all_sync(kFull, mbar_wait(bar, parity, w, site));
+  };
+  const uint32_t q0 = kDescLoK | (smem_u32(s.q[0]) >> 4), k0 = kDescLoK | (smem_u32(s.k[0]) >> 4);
+  const uint32_t v0 = kDescLoV | (smem_u32(s.v[0]) >> 4);
+  constexpr uint32_t kTile = (BN * D * 2) >> 4, kHalf = (kPage * 128) >> 4;
+  bool ok = wait(&s.k_full[0], 0, kSitePreK);
   if (ok) {
     tc_fence_after();
-    for (int t = 0; t < tiles; t++) {
-      issue_qk<D>(s, t, tmem + t * BN, 0);
-      mma_commit(&s.s_full[t]);
-    }
-    mma_commit(&s.k_empty[0]);
-  }
-  for (int it = 0; ok && it < nk; it++) {
-    const int st = it % NS, sn = (it + 1) % NS;
-    const bool more = it + 1 < nk;
-    ok = mbar_wait(&s.v_full[st], (it / NS) & 1, w, kSitePreV);
-    for (int t = 0; ok && t < tiles; t++) {
-      for (int half = 0; ok && half < 2; half++) {
-        ok = mbar_wait(&s.p_full[t][half], it & 1, w, kSitePreP);
-        if (!ok) break;
-        tc_fence_after();
-        issue_pv<D>(s, tmem + t * BN, tmem + 2 * BN + t * D, st, half, it == 0);
-      }
-      if (!ok) break;
-      if (t == tiles - 1) mma_commit(&s.v_empty[st]);
-      if (more) {
-        if (t == 0) {
-          ok = mbar_wait(&s.k_full[sn], ((it + 1) / NS) & 1, w, kSitePreK);
-          if (!ok) break;
-          tc_fence_after();
+    if (elect_one()) {
+      for (int u = 0; u < 2; u++)
+        for (int t = 0; t < tiles; t++) {
+          issue_qk<D>(tmem + t * kTileCols + u * kPage, q0 + t * kTile, k0 + u * kHalf);
+          mma_commit(&s.s_full[t][u]);
         }
-        issue_qk<D>(s, t, tmem + t * BN, sn);
-        if (t == tiles - 1) mma_commit(&s.k_empty[sn]);
+      mma_commit(&s.k_empty[0]);
+    }
+    __syncwarp();
+  }
+  for (int u = 0; ok && u < 2 * nk; u++) {
+    const int it = u >> 1, st = it % NS, sn = (it + 1) % NS, half = u & 1;
+    const bool more = it + 1 < nk;
+    if (half == 0) {
+      ok = wait(&s.v_full[st], (it / NS) & 1, kSitePreV);
+      if (ok && more) ok = wait(&s.k_full[sn], ((it + 1) / NS) & 1, kSitePreK);
+    }
+    for (int t = 0; ok && t < tiles; t++) {
+      ok = wait(&s.p_full[t][half], it & 1, kSitePreP);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t tT = tmem + t * kTileCols, tS = tT + half * kPage;
+      if (elect_one()) {
+        issue_pv<D>(tS, tT + 128, v0 + st * kTile + half * kHalf, u == 0);
+        if (half == 1 && t == tiles - 1) mma_commit(&s.v_empty[st]);
+        if (more) {
+          issue_qk<D>(tS, q0 + t * kTile, k0 + sn * kTile + half * kHalf);
+          if (half == 1 && t == tiles - 1) mma_commit(&s.k_empty[sn]);
+        }
+        mma_commit(&s.s_full[t][half]);  // S of page u + 2, and O through page u
       }
-      mma_commit(&s.s_full[t]);  // the next S, or the finished O
+      __syncwarp();
     }
   }
   // everything issued completes before TMEM is freed
-  mma_commit(&s.drain);
-  const long long t0 = clock64();
-  while (!mbar_try_wait(&s.drain, 0)) {
-    if (clock64() - t0 > w.budget) {
-      record_timeout(w.status, kSitePreDrain);
-      break;
+  if (elect_one()) {
+    mma_commit(&s.drain);
+    const long long t0 = clock64();
+    while (!mbar_try_wait(&s.drain, 0)) {
+      if (clock64() - t0 > w.budget) {
+        record_timeout(w.status, kSitePreDrain);
+        break;
+      }
     }
   }
+  __syncwarp();
 }
 
 // ---------------------------------------------------------------- softmax
@@ -323,71 +348,69 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
   const int r = t * BM + quad * 32 + lane, row = r0 + r;
   const bool valid = row < r1;
   const uint32_t lo = static_cast<uint32_t>(quad * 32) << 16;
-  const uint32_t tS = tmem + t * BN + lo, tO = tmem + 2 * BN + t * D + lo;
+  const uint32_t tT = tmem + t * kTileCols + lo, tO = tT + 128;
   const float f = s.rowf[r] * (a.scale * kLog2e);
   // a row that is not there sees every key (its scores are 0) and is never
   // stored: masked, it would send its whole warp through the masking code
   KeyRange kr{0, 0, 0x7FFFFFFF};
   if (valid) kr = key_range(a.mask, off + row / a.G, len);
   float m = -INFINITY, l = 0.0f;
-  bool ok = true;
-  for (int it = 0; it < nk; it++) {
-    ok = __all_sync(kFull, mbar_wait(&s.s_full[t], it & 1, w, kSitePreS));
-    if (!ok) break;
+  // page u's scores are there, and O holds the pages through u - 2
+  auto wait_s = [&](int u) {
+    return __all_sync(kFull, mbar_wait(&s.s_full[t][u & 1], (u >> 1) & 1, w, kSitePreS));
+  };
+  for (int u = 0; u < 2 * nk; u++) {
+    if (!wait_s(u)) return;
     tc_fence_after();
-    const TileMeta md = s.meta[it & 3];
+    const TileMeta& md = s.meta[(u >> 1) & 3];
+    const int j0 = md.j0[u & 1], vexp = md.ve[u & 1];
     // a zero scale must not meet -inf as 0 * inf
-    const float c[2] = {fmaxf(f * md.ks[0], FLT_MIN), fmaxf(f * md.ks[1], FLT_MIN)};
-    const float ve[2] = {static_cast<float>(md.ve[0]), static_cast<float>(md.ve[1])};
-    uint32_t sv[128];
-    tmem_ld128(tS, sv);
+    const float c = fmaxf(f * md.ks[u & 1], FLT_MIN), ve = static_cast<float>(vexp);
+    const uint32_t tS = tT + (u & 1) * kPage;
+    uint32_t sv[64];
+    tmem_ld64(tS, sv);
+    const bool all = j0 >= 0 && (kr.sink >= j0 + kPage || (kr.lo <= j0 && kr.hi >= j0 + kPage));
+    if (!__all_sync(kFull, all)) {
+      const int na = j0 < 0 ? 0 : min(max(kr.sink - j0, 0), kPage);
+      const int nb = min(max(kr.lo - j0, 0), kPage);
+      const int nc = j0 < 0 ? nb : min(max(kr.hi - j0, nb), kPage);
+      const uint32_t nbc = static_cast<uint32_t>(nc - nb);
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-      const int j0 = md.j0[i];
-      const bool all = j0 >= 0 && (kr.sink >= j0 + kPage || (kr.lo <= j0 && kr.hi >= j0 + kPage));
-      if (!__all_sync(kFull, all)) {
-        const int na = j0 < 0 ? 0 : min(max(kr.sink - j0, 0), kPage);
-        const int nb = min(max(kr.lo - j0, 0), kPage);
-        const int nc = j0 < 0 ? nb : min(max(kr.hi - j0, nb), kPage);
-        const uint32_t nbc = static_cast<uint32_t>(nc - nb);
-#pragma unroll
-        for (int j = 0; j < kPage; j++)
-          sv[i * 64 + j] = (j < na || static_cast<uint32_t>(j - nb) < nbc) ? sv[i * 64 + j] : kNegInf;
-      }
+      for (int j = 0; j < kPage; j++)
+        sv[j] = (j < na || static_cast<uint32_t>(j - nb) < nbc) ? sv[j] : kNegInf;
     }
-    // The exponentials of the first half start at once, against the reference
-    // maximum in hand, and the tile's maximum is taken beside them (its
-    // instructions fit between those of the MUFU).  Only if that has grown by
-    // more than 2^8, or is the row's first, is the half done again.
-    float mx[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
-    float sum;
+    // The exponentials start at once, against the reference maximum in hand,
+    // and the page's maximum is taken beside them (its instructions fit
+    // between those of the MUFU).  Only if that has grown by more than 2^8,
+    // or is the row's first, are they done again.
+    float mx[2] = {-INFINITY, -INFINITY};
+    float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
     {
-      const float nm = (m == -INFINITY ? 0.0f : kBoost - m) + ve[0];
-      float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-      const float2 cc = make_float2(c[0], c[0]), nn = make_float2(nm, nm);
+      const float nm = (m == -INFINITY ? 0.0f : kBoost - m) + ve;
+      const float2 cc = make_float2(c, c), nn = make_float2(nm, nm);
 #pragma unroll
       for (int j = 0; j < 32; j++) {
         const float s0 = __uint_as_float(sv[2 * j]), s1 = __uint_as_float(sv[2 * j + 1]);
         float2 x = __ffma2_rn(make_float2(s0, s1), cc, nn);
         x.x = ex2_approx(x.x);
         x.y = ex2_approx(x.y);
-        mx[0][j & 1] = fmax3(mx[0][j & 1], s0, s1);
-        mx[1][j & 1] = fmax3(mx[1][j & 1], __uint_as_float(sv[64 + 2 * j]), __uint_as_float(sv[65 + 2 * j]));
+        mx[j & 1] = fmax3(mx[j & 1], s0, s1);
         acc[j & 1] = __fadd2_rn(acc[j & 1], x);
         const __half2 y = __floats2half2_rn(x.x, x.y);
         sv[j] = *reinterpret_cast<const uint32_t*>(&y);
       }
-      const float2 a2 = __fadd2_rn(acc[0], acc[1]);
-      sum = a2.x + a2.y;
     }
-    const float top = fmaxf(fmaf(fmaxf(mx[0][0], mx[0][1]), c[0], ve[0]),
-                            fmaf(fmaxf(mx[1][0], mx[1][1]), c[1], ve[1]));
+    const float2 a2 = __fadd2_rn(acc[0], acc[1]);
+    float sum = a2.x + a2.y;
+    const float top = fmaf(fmaxf(mx[0], mx[1]), c, ve);
     if (__any_sync(kFull, top > m + kLazy)) {
       const float mn = fmaxf(m, top);
       const float al = mn == m ? 1.0f : ex2_approx(m - mn);  // 0 from -inf
-      // O holds the sum of the tiles before: its last product completed
-      // before s_full did
-      if (it > 0) {
+      if (u > 0) {
+        // O through page u - 1: its product was issued before the S of page
+        // u + 1 (or, at the end, before the commit in that one's place)
+        if (!wait_s(u + 1)) return;
+        tc_fence_after();
 #pragma unroll 1
         for (int d = 0; d < D; d += 32) {
           uint32_t o[32];
@@ -399,7 +422,7 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
       }
       l *= al;
       m = mn;
-      const float nm = (m == -INFINITY ? 0.0f : kBoost - m) + ve[0];
+      const float nm = (m == -INFINITY ? 0.0f : kBoost - m) + ve;
       sum = 0.0f;
       // S is still in TMEM; P of 32 keys takes the columns of the 16 before
 #pragma unroll 1
@@ -408,9 +431,9 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
         tmem_ld32(tS + k, x);
 #pragma unroll
         for (int e = 0; e < 32; e++) {
-          const int j = md.j0[0] + k + e;
-          const bool see = md.j0[0] >= 0 && (j < kr.sink || (j >= kr.lo && j < kr.hi));
-          const float v = see ? ex2_approx(fmaf(__uint_as_float(x[e]), c[0], nm)) : 0.0f;
+          const int j = j0 + k + e;
+          const bool see = j0 >= 0 && (j < kr.sink || (j >= kr.lo && j < kr.hi));
+          const float v = see ? ex2_approx(fmaf(__uint_as_float(x[e]), c, nm)) : 0.0f;
           sum += v;
           x[e] = __float_as_uint(v);
         }
@@ -427,35 +450,13 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
       for (int j = 0; j < 32; j++) pk[j] = sv[j];
       tmem_st32(tS, pk);
     }
-    l = fmaf(sum, pow2i(min(-md.ve[0], 127)), l);
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&s.p_full[t][0]);
-    {
-      const float base = m == -INFINITY ? 0.0f : kBoost - m;
-      float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-      const float2 cc = make_float2(c[1], c[1]), nn = make_float2(base + ve[1], base + ve[1]);
-      uint32_t pk[32];
-#pragma unroll
-      for (int j = 0; j < 32; j++) {
-        float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[64 + 2 * j]), __uint_as_float(sv[65 + 2 * j])), cc, nn);
-        x.x = ex2_approx(x.x);
-        x.y = ex2_approx(x.y);
-        acc[j & 1] = __fadd2_rn(acc[j & 1], x);
-        const __half2 y = __floats2half2_rn(x.x, x.y);
-        pk[j] = *reinterpret_cast<const uint32_t*>(&y);
-      }
-      tmem_st32(tS + 32, pk);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.p_full[t][1]);
-      const float2 a2 = __fadd2_rn(acc[0], acc[1]);
-      l = fmaf(a2.x + a2.y, pow2i(min(-md.ve[1], 127)), l);
-    }
+    if (lane == 0) mbar_arrive(&s.p_full[t][u & 1]);
+    l = fmaf(sum, pow2i(min(-vexp, 127)), l);
   }
-  if (!ok) return;
   if (nk > 0) {
-    if (!__all_sync(kFull, mbar_wait(&s.s_full[t], nk & 1, w, kSitePreS))) return;
+    if (!wait_s(2 * nk + 1)) return;  // O through the last page
     tc_fence_after();
   }
   if (__all_sync(kFull, !valid)) return;
@@ -554,7 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_prefill(const CacheAttnAr
       mbar_init(&s.v_empty[j], 1);
     }
     for (int j = 0; j < 2; j++) {
-      mbar_init(&s.s_full[j], 1);
+      mbar_init(&s.s_full[j][0], 1);
+      mbar_init(&s.s_full[j][1], 1);
       mbar_init(&s.p_full[j][0], 4);
       mbar_init(&s.p_full[j][1], 4);
     }
@@ -578,16 +580,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_prefill(const CacheAttnAr
   const uint32_t tmem = s.tmem_base;
   const WaitCtx w{a.budget, a.c.status, &s.abort};
   if (warp < 8) {
-    set_regs_up<kRegsSoftmax>();
     const int t = warp >> 2;
     if (t < tiles)
       softmax<D>(s, a, tmem, b, h, t, r0, r1, runs, p0, p1, nk, len, off, chunk, nch, row_tiles, w);
   } else if (warp < 12) {
-    set_regs_down<kRegsConvert>();
     convert<D>(s, a, runs, b, h, p0, p1, nk, len, w);
   } else {
-    set_regs_down<kRegsIssue>();
-    if (warp == 12 && lane == 0 && nk > 0) issue<D>(s, tmem, nk, tiles, w);
+    if (warp == 12 && nk > 0) issue<D>(s, tmem, nk, tiles, w);
   }
   __syncwarp();
   tc_fence_before();
