@@ -2,26 +2,21 @@
 // rows (prompts, latent frames): the arithmetic of cache_attn.cu on tcgen05.
 //
 // A block owns 256 query rows of one (sequence, key head), two tiles of 128,
-// and walks KV tiles of 128 keys (two pages), the scores page by page.  16
-// warps:
-//   0-3, 4-7   softmax of tile 0 and 1, a thread a row: a page's 64 scores
-//              from TMEM, y = 2^(t + e - M + 7), fp16(y) back into the TMEM
-//              columns of the scores, where the second product reads it as
-//              operand A.  M moves, and O is rescaled, only when a row's
-//              maximum grew by more than 2^8 (y <= 2^15 then still fits
-//              fp16), so a page's maximum is off the path to its exponentials.
+// and walks KV tiles of 128 keys (two pages).  16 warps:
+//   0-3, 4-7   softmax of tile 0 and 1, a thread a row: S from TMEM, running
+//              maximum, y = 2^(t + e - M + 7), fp16(y) back into the TMEM
+//              columns of S, where the second product reads it as operand A,
+//              64 keys at a time.  M moves, and O is rescaled, only when a
+//              row's maximum grew by more than 2^8 (y <= 2^15 then still fits
+//              fp16), so a tile's maximum is off the path to its exponentials.
 //   8-11       codes from global memory to fp16 operands in shared memory, in
 //              the 128-byte swizzle the tensor core reads; K exactly, V
 //              exactly, the next tile's codes already in flight in registers.
-//   12         issues every tcgen05.mma: O += P V of page u, then S = Q K^T of
-//              page u + 2 into the columns that P has left.  A tile has two
-//              score buffers (2 x 64 columns, and 128 of O: two tiles fill the
-//              512), so the products of one page run under the softmax of the
-//              next; with one buffer of 128 keys the chain S, softmax, P V was
-//              serial and a KV tile took 5200 clocks.
+//   12         issues every tcgen05.mma: for each tile in turn O += P V of
+//              one KV tile and S = Q K^T of the next, so one tile's products
+//              run under the other's softmax.
 // What bounds it: 4 D flops a (row, key) on the fp16 tensor pipe and one exp2
-// on the MUFU take the same 2048 clocks a KV tile at D = 128, and shared
-// memory (64-key score tiles read Q twice as often) 2560.  fp16 operands
+// on the MUFU take the same 2048 clocks a KV tile at D = 128.  fp16 operands
 // rather than the codes' own 8-bit kinds: Q is not quantized, and an int8 or
 // e4m3 product would need it (and P) in two limbs or more, the same tensor
 // time without the exactness.  256 rows a block halve the conversions per
@@ -39,12 +34,15 @@ namespace sage {
 namespace {
 
 constexpr int BM = 128, BN = 128;
-constexpr int kTileCols = 256;   // TMEM columns of a row tile: S 0-63, S 64-127, O from 128
 constexpr int kThreads = 512;
 constexpr int kConvert = 128;  // of these
 constexpr int NS = 2;
 constexpr float kBoost = 7.0f;   // y = 2^7 at the reference maximum
 constexpr float kLazy = 8.0f;    // growth of the maximum that forces a rescale
+constexpr int kRegsSoftmax = 184, kRegsConvert = 104, kRegsIssue = 40;
+static_assert(kRegsSoftmax * 256 + kRegsConvert * 128 + kRegsIssue * 128 <= 65536,
+              "register split within the launch's share");
+
 enum : int { kSitePreKEmpty = 0x20201, kSitePreVEmpty, kSitePreK, kSitePreV, kSitePreP, kSitePreS,
              kSitePreDrain };
 
@@ -63,10 +61,7 @@ struct alignas(1024) PreSmem {
   float rowf[2 * BM];
   TileMeta meta[4];  // of KV tile it in slot it % 4
   uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
-  // s_full[tile][u & 1]: S of page u (and P V of page u - 2); p_full[tile][u & 1]:
-  // P of page u.  A warp may be a page ahead of the others of its tile, never
-  // two, so each buffer counts its own arrivals.
-  uint64_t s_full[2][2], p_full[2][2], drain;
+  uint64_t s_full[2], p_full[2][2], drain;  // p_full[tile][half]: P of 64 keys
   uint32_t tmem_base;
   int abort;
 };
@@ -105,6 +100,15 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void set_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // ---------------------------------------------------------------- converters
@@ -219,8 +223,8 @@ __device__ __forceinline__ void convert(PreSmem<D>& s, const CacheAttnArgs& a, c
     if (it >= NS && !__all_sync(kFull, mbar_wait(&s.k_empty[st], ph, w, kSitePreKEmpty))) return;
     store_codes<D, false>(s.k[st], kr, ch, j0, len);
     // the tile's page data for the softmax.  Slot it % 4 was last read by the
-    // softmax of tile it - 4: k_empty has just reported the S of tile it - 2,
-    // which was issued after the P of tile it - 3's first page.
+    // softmax of tile it - 4, whose P went into a product issued before the
+    // S of tile it - 2 that k_empty has just reported.
     if (tid < 32 && (lane & ~1) == at) {
       TileMeta& m = s.meta[it & 3];
       m.j0[lane & 1] = cur.j0;
@@ -254,17 +258,17 @@ __device__ __forceinline__ void convert(PreSmem<D>& s, const CacheAttnArgs& a, c
 
 // ---------------------------------------------------------------- tensor core
 
-// S = Q K^T of one page (64 keys): q and k are the operands' lower words.
+// S = Q K^T: q and k are the operands' lower descriptor words.
 template <int D>
 __device__ __forceinline__ void issue_qk(uint32_t tS, uint32_t q, uint32_t k) {
-  constexpr uint32_t id = idesc_f16(BM, kPage);
+  constexpr uint32_t id = idesc_f16(BM, BN);
 #pragma unroll
   for (int kk = 0; kk < D / 16; kk++) {
     const uint32_t off = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
     mma_f16_ss(tS, desc_of(q + off), desc_of(k + off), id, kk > 0);
   }
 }
-// O (+)= P V of one page.
+// O (+)= P V of 64 keys.
 template <int D>
 __device__ __forceinline__ void issue_pv(uint32_t tP, uint32_t tO, uint32_t v, bool first) {
   constexpr uint32_t id = idesc_f16(BM, D) | kIdescBMajorMN;
@@ -289,35 +293,37 @@ __device__ __forceinline__ void issue(PreSmem<D>& s, uint32_t tmem, int nk, int 
   if (ok) {
     tc_fence_after();
     if (elect_one()) {
-      for (int u = 0; u < 2; u++)
-        for (int t = 0; t < tiles; t++) {
-          issue_qk<D>(tmem + t * kTileCols + u * kPage, q0 + t * kTile, k0 + u * kHalf);
-          mma_commit(&s.s_full[t][u]);
-        }
+      for (int t = 0; t < tiles; t++) {
+        issue_qk<D>(tmem + t * BN, q0 + t * kTile, k0);
+        mma_commit(&s.s_full[t]);
+      }
       mma_commit(&s.k_empty[0]);
     }
     __syncwarp();
   }
-  for (int u = 0; ok && u < 2 * nk; u++) {
-    const int it = u >> 1, st = it % NS, sn = (it + 1) % NS, half = u & 1;
+  for (int it = 0; ok && it < nk; it++) {
+    const int st = it % NS, sn = (it + 1) % NS;
     const bool more = it + 1 < nk;
-    if (half == 0) {
-      ok = wait(&s.v_full[st], (it / NS) & 1, kSitePreV);
-      if (ok && more) ok = wait(&s.k_full[sn], ((it + 1) / NS) & 1, kSitePreK);
-    }
+    ok = wait(&s.v_full[st], (it / NS) & 1, kSitePreV);
     for (int t = 0; ok && t < tiles; t++) {
-      ok = wait(&s.p_full[t][half], it & 1, kSitePreP);
+      const uint32_t tS = tmem + t * BN, tO = tmem + 2 * BN + t * D;
+      ok = wait(&s.p_full[t][0], it & 1, kSitePreP);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t tT = tmem + t * kTileCols, tS = tT + half * kPage;
+      if (elect_one()) issue_pv<D>(tS, tO, v0 + st * kTile, it == 0);
+      __syncwarp();
+      ok = wait(&s.p_full[t][1], it & 1, kSitePreP);
+      if (ok && more && t == 0) ok = wait(&s.k_full[sn], ((it + 1) / NS) & 1, kSitePreK);
+      if (!ok) break;
+      tc_fence_after();
       if (elect_one()) {
-        issue_pv<D>(tS, tT + 128, v0 + st * kTile + half * kHalf, u == 0);
-        if (half == 1 && t == tiles - 1) mma_commit(&s.v_empty[st]);
+        issue_pv<D>(tS + 32, tO, v0 + st * kTile + kHalf, false);
+        if (t == tiles - 1) mma_commit(&s.v_empty[st]);
         if (more) {
-          issue_qk<D>(tS, q0 + t * kTile, k0 + sn * kTile + half * kHalf);
-          if (half == 1 && t == tiles - 1) mma_commit(&s.k_empty[sn]);
+          issue_qk<D>(tS, q0 + t * kTile, k0 + sn * kTile);
+          if (t == tiles - 1) mma_commit(&s.k_empty[sn]);
         }
-        mma_commit(&s.s_full[t][half]);  // S of page u + 2, and O through page u
+        mma_commit(&s.s_full[t]);  // the next S, or the finished O
       }
       __syncwarp();
     }
@@ -348,69 +354,71 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
   const int r = t * BM + quad * 32 + lane, row = r0 + r;
   const bool valid = row < r1;
   const uint32_t lo = static_cast<uint32_t>(quad * 32) << 16;
-  const uint32_t tT = tmem + t * kTileCols + lo, tO = tT + 128;
+  const uint32_t tS = tmem + t * BN + lo, tO = tmem + 2 * BN + t * D + lo;
   const float f = s.rowf[r] * (a.scale * kLog2e);
   // a row that is not there sees every key (its scores are 0) and is never
   // stored: masked, it would send its whole warp through the masking code
   KeyRange kr{0, 0, 0x7FFFFFFF};
   if (valid) kr = key_range(a.mask, off + row / a.G, len);
   float m = -INFINITY, l = 0.0f;
-  // page u's scores are there, and O holds the pages through u - 2
-  auto wait_s = [&](int u) {
-    return __all_sync(kFull, mbar_wait(&s.s_full[t][u & 1], (u >> 1) & 1, w, kSitePreS));
-  };
-  for (int u = 0; u < 2 * nk; u++) {
-    if (!wait_s(u)) return;
+  bool ok = true;
+  for (int it = 0; it < nk; it++) {
+    ok = __all_sync(kFull, mbar_wait(&s.s_full[t], it & 1, w, kSitePreS));
+    if (!ok) break;
     tc_fence_after();
-    const TileMeta& md = s.meta[(u >> 1) & 3];
-    const int j0 = md.j0[u & 1], vexp = md.ve[u & 1];
+    const TileMeta md = s.meta[it & 3];
     // a zero scale must not meet -inf as 0 * inf
-    const float c = fmaxf(f * md.ks[u & 1], FLT_MIN), ve = static_cast<float>(vexp);
-    const uint32_t tS = tT + (u & 1) * kPage;
-    uint32_t sv[64];
-    tmem_ld64(tS, sv);
-    const bool all = j0 >= 0 && (kr.sink >= j0 + kPage || (kr.lo <= j0 && kr.hi >= j0 + kPage));
-    if (!__all_sync(kFull, all)) {
-      const int na = j0 < 0 ? 0 : min(max(kr.sink - j0, 0), kPage);
-      const int nb = min(max(kr.lo - j0, 0), kPage);
-      const int nc = j0 < 0 ? nb : min(max(kr.hi - j0, nb), kPage);
-      const uint32_t nbc = static_cast<uint32_t>(nc - nb);
+    const float c[2] = {fmaxf(f * md.ks[0], FLT_MIN), fmaxf(f * md.ks[1], FLT_MIN)};
+    const float ve[2] = {static_cast<float>(md.ve[0]), static_cast<float>(md.ve[1])};
+    uint32_t sv[128];
+    tmem_ld128(tS, sv);
 #pragma unroll
-      for (int j = 0; j < kPage; j++)
-        sv[j] = (j < na || static_cast<uint32_t>(j - nb) < nbc) ? sv[j] : kNegInf;
+    for (int i = 0; i < 2; i++) {
+      const int j0 = md.j0[i];
+      const bool all = j0 >= 0 && (kr.sink >= j0 + kPage || (kr.lo <= j0 && kr.hi >= j0 + kPage));
+      if (!__all_sync(kFull, all)) {
+        const int na = j0 < 0 ? 0 : min(max(kr.sink - j0, 0), kPage);
+        const int nb = min(max(kr.lo - j0, 0), kPage);
+        const int nc = j0 < 0 ? nb : min(max(kr.hi - j0, nb), kPage);
+        const uint32_t nbc = static_cast<uint32_t>(nc - nb);
+#pragma unroll
+        for (int j = 0; j < kPage; j++)
+          sv[i * 64 + j] = (j < na || static_cast<uint32_t>(j - nb) < nbc) ? sv[i * 64 + j] : kNegInf;
+      }
     }
-    // The exponentials start at once, against the reference maximum in hand,
-    // and the page's maximum is taken beside them (its instructions fit
-    // between those of the MUFU).  Only if that has grown by more than 2^8,
-    // or is the row's first, are they done again.
-    float mx[2] = {-INFINITY, -INFINITY};
-    float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+    // The exponentials of the first half start at once, against the reference
+    // maximum in hand, and the tile's maximum is taken beside them (its
+    // instructions fit between those of the MUFU).  Only if that has grown by
+    // more than 2^8, or is the row's first, is the half done again.
+    float mx[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
+    float sum;
     {
-      const float nm = (m == -INFINITY ? 0.0f : kBoost - m) + ve;
-      const float2 cc = make_float2(c, c), nn = make_float2(nm, nm);
+      const float nm = (m == -INFINITY ? 0.0f : kBoost - m) + ve[0];
+      float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+      const float2 cc = make_float2(c[0], c[0]), nn = make_float2(nm, nm);
 #pragma unroll
       for (int j = 0; j < 32; j++) {
         const float s0 = __uint_as_float(sv[2 * j]), s1 = __uint_as_float(sv[2 * j + 1]);
         float2 x = __ffma2_rn(make_float2(s0, s1), cc, nn);
         x.x = ex2_approx(x.x);
         x.y = ex2_approx(x.y);
-        mx[j & 1] = fmax3(mx[j & 1], s0, s1);
+        mx[0][j & 1] = fmax3(mx[0][j & 1], s0, s1);
+        mx[1][j & 1] = fmax3(mx[1][j & 1], __uint_as_float(sv[64 + 2 * j]), __uint_as_float(sv[65 + 2 * j]));
         acc[j & 1] = __fadd2_rn(acc[j & 1], x);
         const __half2 y = __floats2half2_rn(x.x, x.y);
         sv[j] = *reinterpret_cast<const uint32_t*>(&y);
       }
+      const float2 a2 = __fadd2_rn(acc[0], acc[1]);
+      sum = a2.x + a2.y;
     }
-    const float2 a2 = __fadd2_rn(acc[0], acc[1]);
-    float sum = a2.x + a2.y;
-    const float top = fmaf(fmaxf(mx[0], mx[1]), c, ve);
+    const float top = fmaxf(fmaf(fmaxf(mx[0][0], mx[0][1]), c[0], ve[0]),
+                            fmaf(fmaxf(mx[1][0], mx[1][1]), c[1], ve[1]));
     if (__any_sync(kFull, top > m + kLazy)) {
       const float mn = fmaxf(m, top);
       const float al = mn == m ? 1.0f : ex2_approx(m - mn);  // 0 from -inf
-      if (u > 0) {
-        // O through page u - 1: its product was issued before the S of page
-        // u + 1 (or, at the end, before the commit in that one's place)
-        if (!wait_s(u + 1)) return;
-        tc_fence_after();
+      // O holds the sum of the tiles before: its last product completed
+      // before s_full did
+      if (it > 0) {
 #pragma unroll 1
         for (int d = 0; d < D; d += 32) {
           uint32_t o[32];
@@ -422,7 +430,7 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
       }
       l *= al;
       m = mn;
-      const float nm = (m == -INFINITY ? 0.0f : kBoost - m) + ve;
+      const float nm = (m == -INFINITY ? 0.0f : kBoost - m) + ve[0];
       sum = 0.0f;
       // S is still in TMEM; P of 32 keys takes the columns of the 16 before
 #pragma unroll 1
@@ -431,9 +439,9 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
         tmem_ld32(tS + k, x);
 #pragma unroll
         for (int e = 0; e < 32; e++) {
-          const int j = j0 + k + e;
-          const bool see = j0 >= 0 && (j < kr.sink || (j >= kr.lo && j < kr.hi));
-          const float v = see ? ex2_approx(fmaf(__uint_as_float(x[e]), c, nm)) : 0.0f;
+          const int j = md.j0[0] + k + e;
+          const bool see = md.j0[0] >= 0 && (j < kr.sink || (j >= kr.lo && j < kr.hi));
+          const float v = see ? ex2_approx(fmaf(__uint_as_float(x[e]), c[0], nm)) : 0.0f;
           sum += v;
           x[e] = __float_as_uint(v);
         }
@@ -450,13 +458,35 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
       for (int j = 0; j < 32; j++) pk[j] = sv[j];
       tmem_st32(tS, pk);
     }
+    l = fmaf(sum, pow2i(min(-md.ve[0], 127)), l);
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&s.p_full[t][u & 1]);
-    l = fmaf(sum, pow2i(min(-vexp, 127)), l);
+    if (lane == 0) mbar_arrive(&s.p_full[t][0]);
+    {
+      const float base = m == -INFINITY ? 0.0f : kBoost - m;
+      float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+      const float2 cc = make_float2(c[1], c[1]), nn = make_float2(base + ve[1], base + ve[1]);
+      uint32_t pk[32];
+#pragma unroll
+      for (int j = 0; j < 32; j++) {
+        float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[64 + 2 * j]), __uint_as_float(sv[65 + 2 * j])), cc, nn);
+        x.x = ex2_approx(x.x);
+        x.y = ex2_approx(x.y);
+        acc[j & 1] = __fadd2_rn(acc[j & 1], x);
+        const __half2 y = __floats2half2_rn(x.x, x.y);
+        pk[j] = *reinterpret_cast<const uint32_t*>(&y);
+      }
+      tmem_st32(tS + 32, pk);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.p_full[t][1]);
+      const float2 a2 = __fadd2_rn(acc[0], acc[1]);
+      l = fmaf(a2.x + a2.y, pow2i(min(-md.ve[1], 127)), l);
+    }
   }
+  if (!ok) return;
   if (nk > 0) {
-    if (!wait_s(2 * nk + 1)) return;  // O through the last page
+    if (!__all_sync(kFull, mbar_wait(&s.s_full[t], nk & 1, w, kSitePreS))) return;
     tc_fence_after();
   }
   if (__all_sync(kFull, !valid)) return;
@@ -555,8 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_prefill(const CacheAttnAr
       mbar_init(&s.v_empty[j], 1);
     }
     for (int j = 0; j < 2; j++) {
-      mbar_init(&s.s_full[j][0], 1);
-      mbar_init(&s.s_full[j][1], 1);
+      mbar_init(&s.s_full[j], 1);
       mbar_init(&s.p_full[j][0], 4);
       mbar_init(&s.p_full[j][1], 4);
     }
@@ -580,12 +609,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_prefill(const CacheAttnAr
   const uint32_t tmem = s.tmem_base;
   const WaitCtx w{a.budget, a.c.status, &s.abort};
   if (warp < 8) {
+    set_regs_up<kRegsSoftmax>();
     const int t = warp >> 2;
     if (t < tiles)
       softmax<D>(s, a, tmem, b, h, t, r0, r1, runs, p0, p1, nk, len, off, chunk, nch, row_tiles, w);
   } else if (warp < 12) {
+    set_regs_down<kRegsConvert>();
     convert<D>(s, a, runs, b, h, p0, p1, nk, len, w);
   } else {
+    set_regs_down<kRegsIssue>();
     if (warp == 12 && nk > 0) issue<D>(s, tmem, nk, tiles, w);
   }
   __syncwarp();
