@@ -374,7 +374,8 @@ SAGE_EXPORT sage_status sage_cache_evict(const sage_kv_cache* cache, const sage_
              workspace_bytes < cache_evict_ws_bytes(seqs->B, cache->heads, cache->D, keep)) {
     return SAGE_ERR_INVALID_ARG;
   }
-  if (!cache_fits(cache)) return SAGE_ERR_UNSUPPORTED;
+  if (!cache_fits(cache) || static_cast<long long>(seqs->B) * cache->heads > (1 << 28))
+    return SAGE_ERR_UNSUPPORTED;
   int* status = api_status_word();
   if (!status) return SAGE_ERR_CUDA;
   EvictArgs a{};

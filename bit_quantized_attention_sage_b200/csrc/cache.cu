@@ -8,6 +8,7 @@
 // are rescaled by the ratio.  All of it is one pass over the data: what bounds
 // it is HBM (a prompt, a prune) or the launch (one token).
 #include <cuda_bf16.h>
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
 #include "cache.cuh"
@@ -18,6 +19,15 @@ namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kThreads = 256;
+
+constexpr float kRound = 12582912.0f;       // 1.5 * 2^23
+constexpr float kNearTie = 6.1035156e-5f;   // 2^-14: four times the error of x * (1 / s) at 127
+
+// The low bytes of four words as one.
+__device__ __forceinline__ uint32_t low_bytes(float a, float b, float c, float d) {
+  return __byte_perm(__byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040),
+                     __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040), 0x5410);
+}
 
 __device__ __forceinline__ float e4m3_value(uint32_t code) {
   const __half_raw h = [&] {
@@ -30,25 +40,51 @@ __device__ __forceinline__ float e4m3_value(uint32_t code) {
   return __half2float(__half(h));
 }
 
-// round-half-even(x / s) for |x / s| <= 127.01, exactly.  x * inv (inv =
-// fp32(1 / s)) is off by at most 2^-23 of 127; where that leaves the side of
-// a tie open, the remainder x - (k + 1/2) s decides, which one fma gives
-// without rounding (it is a small multiple of the last place of s or x).
-__device__ __forceinline__ int key_code(float x, float s, float inv) {
-  const float q = x * inv;
-  float c = rintf(q);
-  if (fabsf(fabsf(q - c) - 0.5f) < 6.1035156e-5f) {
-    const float lo = floorf(q), r = fmaf(-(lo + 0.5f), s, x);
-    c = r > 0.0f ? lo + 1.0f : r < 0.0f ? lo : 2.0f * rintf(0.5f * lo + 0.25f);
-    // tie: the even one of lo and lo + 1 (0.5 lo + 0.25 is lo/2 + 1/4, whose
-    // nearest integer is lo/2 for even lo and (lo + 1)/2 for odd lo)
+// round-half-even(x / s) for |x / s| <= 127.01, exactly, by the slow way:
+// x * inv (inv = fp32(1 / s)) is off by at most 2^-23 of 127; where that leaves
+// the side of a tie open, the remainder x - (k + 1/2) s decides, which one fma
+// gives without rounding (it is a small multiple of the last place of s or
+// x).  `tiny`: 1 / s is no normal fp32 number (keys below 1e-36), fp64 decides.
+__device__ __noinline__ int key_code_slow(float x, float s, float inv, bool tiny) {
+  float c;
+  if (tiny) {
+    c = s > 0.0f ? static_cast<float>(rint(static_cast<double>(x) / static_cast<double>(s))) : 0.0f;
+  } else {
+    const float q = x * inv;
+    c = rintf(q);
+    if (fabsf(fabsf(q - c) - 0.5f) < kNearTie) {
+      const float lo = floorf(q), r = fmaf(-(lo + 0.5f), s, x);
+      c = r > 0.0f ? lo + 1.0f : r < 0.0f ? lo : 2.0f * rintf(0.5f * lo + 0.25f);
+      // tie: the even one of lo and lo + 1 (0.5 lo + 0.25 is lo/2 + 1/4, whose
+      // nearest integer is lo/2 for even lo and (lo + 1)/2 for odd lo)
+    }
   }
   return max(-127, min(127, static_cast<int>(c)));
 }
-// The same where 1 / s is no normal fp32 number (keys below 1e-36).
-__device__ __forceinline__ int key_code_tiny(float x, float s) {
-  const double q = s > 0.0f ? rint(static_cast<double>(x) / static_cast<double>(s)) : 0.0;
-  return max(-127, min(127, static_cast<int>(q)));
+// Eight codes as two words.  Adding 1.5 * 2^23 leaves the rounded quotient in
+// the sum's low byte; only where one of the eight is next to a tie, or 1 / s
+// is no normal number, does the slow way run.
+__device__ __forceinline__ void key_codes(const float (&x)[8], float s, float inv, bool tiny, uint32_t (&w)[2]) {
+  float y[8], worst = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; e++) {
+    const float q = fmaxf(fminf(x[e] * inv, 127.0f), -127.0f);
+    y[e] = __fadd_rn(q, kRound);
+    worst = fmaxf(worst, fabsf(__fsub_rn(q, __fsub_rn(y[e], kRound))));
+  }
+#pragma unroll
+  for (int i = 0; i < 2; i++) w[i] = low_bytes(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+  if (tiny || worst > 0.5f - kNearTie) {
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      uint32_t u = 0;
+      for (int e = 0; e < 4; e++) {
+        const float v = e == 0 ? x[4 * i] : e == 1 ? x[4 * i + 1] : e == 2 ? x[4 * i + 2] : x[4 * i + 3];
+        u |= static_cast<uint32_t>(key_code_slow(v, s, inv, tiny) & 0xFF) << (8 * e);
+      }
+      w[i] = u;
+    }
+  }
 }
 // round-half-even(code * s_old / s_new): the product is exact in fp64, and a
 // quotient of 24-bit numbers that is not a tie is farther from one than fp64
@@ -58,10 +94,34 @@ __device__ __forceinline__ int rescale_key(int code, float s_old, float s_new) {
   const double q = rint(static_cast<double>(code) * s_old / static_cast<double>(s_new));
   return max(-127, min(127, static_cast<int>(q)));
 }
-// e4m3 code times 2^diff (diff <= 0), rounded to nearest even.
+__device__ __noinline__ uint32_t rescale_keys(uint32_t w, float s_old, float s_new) {
+  uint32_t o = 0;
+  for (int e = 0; e < 4; e++)
+    o |= static_cast<uint32_t>(rescale_key(static_cast<int8_t>(w >> (8 * e)), s_old, s_new) & 0xFF) << (8 * e);
+  return o;
+}
+// e4m3 code times 2^diff, rounded to nearest even.
 __device__ __forceinline__ uint32_t rescale_value(uint32_t code, int diff) {
-  const float v = diff < -60 ? 0.0f * e4m3_value(code) : e4m3_value(code) * pow2i(diff);
+  const float v = diff < -60 ? 0.0f * e4m3_value(code) : e4m3_value(code) * pow2i(min(diff, 126));
   return cvt_e4m3x2(v, 0.0f) & 0xFFu;
+}
+__device__ __noinline__ uint32_t rescale_values(uint32_t w, int diff) {
+  uint32_t o = 0;
+  for (int e = 0; e < 4; e++) o |= rescale_value((w >> (8 * e)) & 0xFF, diff) << (8 * e);
+  return o;
+}
+// Four e4m3 codes times a power of two that is exact in fp16.
+__device__ __forceinline__ uint32_t scale_values(uint32_t w, __half2 f) {
+  uint32_t a, b, r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(a), "=r"(b) : "r"(w));
+  const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&a), f);
+  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&b), f);
+  asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f16x2 l, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n\tmov.b32 %0, {l, h};\n\t}"
+      : "=r"(r) : "r"(*reinterpret_cast<const uint32_t*>(&x)), "r"(*reinterpret_cast<const uint32_t*>(&y)));
+  return r;
 }
 
 template <typename T>
@@ -71,24 +131,27 @@ __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return
 template <>
 __device__ __forceinline__ float to_f32<__half>(__half x) { return __half2float(x); }
 
-// Eight consecutive channels as fp32; VEC: one 16-byte load.
+// Eight consecutive 16-bit channels; VEC: one 16-byte load.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* p, float (&f)[8]) {
-  if constexpr (VEC) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ uint4 load8(const T* p) {
+  if constexpr (VEC) return __ldg(reinterpret_cast<const uint4*>(p));
+  uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      if constexpr (sizeof(T) == 2) {
-        T pr[2];
-        *reinterpret_cast<uint32_t*>(pr) = w[i];
-        f[2 * i] = to_f32(pr[0]);
-        f[2 * i + 1] = to_f32(pr[1]);
-      }
-    }
-  } else {
+  for (int i = 0; i < 4; i++) {
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + 2 * i;
+    w[i] = q[0] | static_cast<uint32_t>(q[1]) << 16;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename T>
+__device__ __forceinline__ void unpack8(uint4 u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 8; i++) f[i] = to_f32(p[i]);
+  for (int i = 0; i < 4; i++) {
+    T pr[2];
+    *reinterpret_cast<uint32_t*>(pr) = w[i];
+    f[2 * i] = to_f32(pr[0]);
+    f[2 * i + 1] = to_f32(pr[1]);
   }
 }
 
@@ -104,135 +167,134 @@ __device__ __forceinline__ float block_max(float v, float* red) {
   return m;
 }
 
+// Two maxima at once.
+__device__ __forceinline__ void block_max2(float& a, float& b, float (*red)[kThreads / 32]) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    a = fmaxf(a, __shfl_xor_sync(kFull, a, o));
+    b = fmaxf(b, __shfl_xor_sync(kFull, b, o));
+  }
+  if ((threadIdx.x & 31) == 0) {
+    red[0][threadIdx.x >> 5] = a;
+    red[1][threadIdx.x >> 5] = b;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; i++) {
+    a = fmaxf(a, red[0][i]);
+    b = fmaxf(b, red[1][i]);
+  }
+}
+
 // ---------------------------------------------------------------- append
 
-// Block (touched page, head, batch): the new tokens of one page, held in
-// registers between their maximum and their codes (one read).
-template <typename T, int D, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_append(const AppendArgs a) {
-  __shared__ float red[kThreads / 32];
-  constexpr int CH = D / 8;                      // 8-channel chunks of a token
-  constexpr int PER = kPage * CH / kThreads;     // chunks per thread
-  const int b = blockIdx.z, h = blockIdx.y;
+// Block (touched page and keys or values, head, batch): the new tokens of one
+// page, held in registers as they came between their maximum and their codes,
+// so they are read once.  Keys and values in blocks of their own: twice the
+// blocks at half the registers, and a block is mostly latency (the sequence's
+// length, the tokens, the page).
+template <typename T, int D, bool VEC, bool KEYS>
+__device__ __forceinline__ void append_page(const AppendArgs& a, int b, int h, int blk, int before, int lo,
+                                            int hi, float* red) {
+  constexpr int CH = D / 8;                   // 8-channel chunks of a token
+  constexpr int PER = kPage * CH / kThreads;  // chunks per thread
+  constexpr int RS = kThreads / CH;           // rows between a thread's chunks
+  static_assert(kThreads % CH == 0, "a thread's chunks are of the same channels");
   const CacheView& c = a.c;
-  const int before = seq_length(c, b);
-  int n = a.n;
-  if (a.n_new) n = max(0, min(n, __ldg(a.n_new + b)));
-  const int blk = before / kPage + static_cast<int>(blockIdx.x);
-  const long long t0 = static_cast<long long>(blk) * kPage;
-  const long long end = static_cast<long long>(before) + n;
-  const int lo = static_cast<int>(max(t0, static_cast<long long>(before)) - t0);
-  const int hi = static_cast<int>(min(static_cast<long long>(kPage), end - t0));
-  if (n == 0 || hi <= lo) return;
-  if (blk >= c.max_pages) {  // past the page table: recorded, not written
-    if (threadIdx.x == 0 && atomicCAS(c.status, 0, 1) == 0) atomicExch(c.status + 1, 0x20003);
-    return;
+  const int r0 = threadIdx.x / CH, d = threadIdx.x % CH * 8;
+  const T* src = static_cast<const T*>(KEYS ? a.k : a.v) + (KEYS ? a.kb : a.vb) * b + (KEYS ? a.kh : a.vh) * h + d;
+  const long long sn = KEYS ? a.kn : a.vn, first = static_cast<long long>(blk) * kPage - before;
+  uint4 x[PER];
+#pragma unroll
+  for (int i = 0; i < PER; i++) {
+    const int r = r0 + i * RS;
+    x[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r >= lo && r < hi) x[i] = load8<T, VEC>(src + sn * (first + r));
   }
+  float sh[8];
+#pragma unroll
+  for (int e = 0; e < 8; e++)
+    sh[e] = KEYS && a.k_shift ? __ldg(a.k_shift + static_cast<size_t>(h) * D + d + e) : 0.0f;
   const int pg = page_id(c, b, blk);
   if (pg < 0) return;
   const size_t unit = static_cast<size_t>(pg) * c.Hkv + h;
-  int8_t* kd = c.k_i8 + unit * (kPage * D);
-  uint8_t* vd = c.v_f8 + unit * (kPage * D);
-  const T* ks = static_cast<const T*>(a.k) + a.kb * b + a.kh * h;
-  const T* vs = static_cast<const T*>(a.v) + a.vb * b + a.vh * h;
-
-  float kx[PER][8], vx[PER][8];
-  float ka = 0.0f, va = 0.0f;
+  uint8_t* dst = (KEYS ? reinterpret_cast<uint8_t*>(c.k_i8) : c.v_f8) + unit * (kPage * D) + d;
+  const float s_old = KEYS && lo > 0 ? c.k_scale[unit] : 0.0f;
+  const int e_old = !KEYS && lo > 0 ? c.v_exp[unit] : kMinVExp;
+  float m = 0.0f;
 #pragma unroll
   for (int i = 0; i < PER; i++) {
-    const int it = threadIdx.x + i * kThreads, r = it / CH, d = it % CH * 8;
+    const int r = r0 + i * RS;
     if (r >= lo && r < hi) {
-      const long long t = t0 + r - before;
-      load8<T, VEC>(ks + a.kn * t + d, kx[i]);
-      load8<T, VEC>(vs + a.vn * t + d, vx[i]);
+      float f[8];
+      unpack8<T>(x[i], f);
+#pragma unroll
+      for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(__fsub_rn(f[e], sh[e])));
     }
   }
-#pragma unroll
-  for (int i = 0; i < PER; i++) {
-    const int it = threadIdx.x + i * kThreads, r = it / CH, d = it % CH * 8;
-    if (r >= lo && r < hi) {
-      if (a.k_shift) {
-#pragma unroll
-        for (int e = 0; e < 8; e++)
-          kx[i][e] = __fsub_rn(kx[i][e], __ldg(a.k_shift + static_cast<size_t>(h) * D + d + e));
-      }
-#pragma unroll
-      for (int e = 0; e < 8; e++) {
-        ka = fmaxf(ka, fabsf(kx[i][e]));
-        va = fmaxf(va, fabsf(vx[i][e]));
-      }
-    }
-  }
-  const float s_old = lo > 0 ? c.k_scale[unit] : 0.0f;
-  const int e_old = lo > 0 ? c.v_exp[unit] : kMinVExp;
-  ka = block_max(ka, red);
-  va = block_max(va, red);
-  const float s = fmaxf(s_old, __fdiv_rn(ka, 127.0f));
-  const int ve = max(e_old, value_exp(va));
-  // every thread has read the old scales (block_max's barriers)
+  m = block_max(m, red);
+  const float s = fmaxf(s_old, __fdiv_rn(m, 127.0f));
+  const int ve = max(e_old, value_exp(m));
+  // every thread has read the old scale (block_max's barriers)
   if (threadIdx.x == 0) {
-    c.k_scale[unit] = s;
-    c.v_exp[unit] = static_cast<int8_t>(ve);
+    if (KEYS) c.k_scale[unit] = s;
+    else c.v_exp[unit] = static_cast<int8_t>(ve);
   }
   const bool tiny = !(s >= 1e-36f);
   const float inv = tiny ? 0.0f : __frcp_rn(s), pv = pow2i(-ve);
 #pragma unroll
   for (int i = 0; i < PER; i++) {
-    const int it = threadIdx.x + i * kThreads, r = it / CH, d = it % CH * 8;
+    const int r = r0 + i * RS;
+    uint2* p = reinterpret_cast<uint2*>(dst + r * D);
     if (r >= lo && r < hi) {
-      uint32_t kw[2], vw[2];
+      uint32_t w[2];
+      float f[8];
+      unpack8<T>(x[i], f);
+      if constexpr (KEYS) {
 #pragma unroll
-      for (int w = 0; w < 2; w++) {
-        uint32_t u = 0;
+        for (int e = 0; e < 8; e++) f[e] = __fsub_rn(f[e], sh[e]);
+        key_codes(f, s, inv, tiny, w);
+      } else {
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-          const float x = kx[i][w * 4 + e];
-          const int q = tiny ? key_code_tiny(x, s) : key_code(x, s, inv);
-          u |= static_cast<uint32_t>(q & 0xFF) << (8 * e);
-        }
-        kw[w] = u;
-        vw[w] = cvt_e4m3x4(vx[i][w * 4] * pv, vx[i][w * 4 + 1] * pv, vx[i][w * 4 + 2] * pv,
-                           vx[i][w * 4 + 3] * pv);
+        for (int k = 0; k < 2; k++)
+          w[k] = cvt_e4m3x4(f[k * 4] * pv, f[k * 4 + 1] * pv, f[k * 4 + 2] * pv, f[k * 4 + 3] * pv);
       }
-      *reinterpret_cast<uint2*>(kd + r * D + d) = make_uint2(kw[0], kw[1]);
-      *reinterpret_cast<uint2*>(vd + r * D + d) = make_uint2(vw[0], vw[1]);
+      *p = make_uint2(w[0], w[1]);
     } else if (r < lo) {  // tokens the page held: only a grown scale moves them
-      if (s > s_old) {
-        uint2 u = *reinterpret_cast<const uint2*>(kd + r * D + d);
-        uint32_t w[2] = {u.x, u.y};
-#pragma unroll
-        for (int j = 0; j < 2; j++) {
-          uint32_t o = 0;
-#pragma unroll
-          for (int e = 0; e < 4; e++) {
-            const int code = static_cast<int8_t>(w[j] >> (8 * e));
-            o |= static_cast<uint32_t>(rescale_key(code, s_old, s) & 0xFF) << (8 * e);
-          }
-          w[j] = o;
-        }
-        *reinterpret_cast<uint2*>(kd + r * D + d) = make_uint2(w[0], w[1]);
-      }
-      if (ve > e_old) {
-        uint2 u = *reinterpret_cast<const uint2*>(vd + r * D + d);
-        uint32_t w[2] = {u.x, u.y};
-#pragma unroll
-        for (int j = 0; j < 2; j++) {
-          uint32_t o = 0;
-#pragma unroll
-          for (int e = 0; e < 4; e++) o |= rescale_value((w[j] >> (8 * e)) & 0xFF, e_old - ve) << (8 * e);
-          w[j] = o;
-        }
-        *reinterpret_cast<uint2*>(vd + r * D + d) = make_uint2(w[0], w[1]);
+      if (KEYS ? s > s_old : ve > e_old) {
+        const uint2 u = *p;
+        *p = KEYS ? make_uint2(rescale_keys(u.x, s_old, s), rescale_keys(u.y, s_old, s))
+                  : make_uint2(rescale_values(u.x, e_old - ve), rescale_values(u.y, e_old - ve));
       }
     } else if (lo == 0) {  // a fresh page: the tokens to come read as zero
-      *reinterpret_cast<uint2*>(kd + r * D + d) = make_uint2(0u, 0u);
-      *reinterpret_cast<uint2*>(vd + r * D + d) = make_uint2(0u, 0u);
+      *p = make_uint2(0u, 0u);
     }
   }
-  if (c.weight && threadIdx.x < kPage) {
+  if (KEYS && c.weight && threadIdx.x < kPage) {
     const int r = threadIdx.x;
     if (r >= lo && (r < hi || lo == 0)) c.weight[unit * kPage + r] = 0.0f;
   }
+}
+
+template <typename T, int D, bool VEC>
+__global__ void __launch_bounds__(kThreads) k_append(const AppendArgs a) {
+  __shared__ float red[kThreads / 32];
+  const int b = blockIdx.z, h = blockIdx.y;
+  const int before = seq_length(a.c, b);
+  int n = a.n;
+  if (a.n_new) n = max(0, min(n, __ldg(a.n_new + b)));
+  const int blk = before / kPage + static_cast<int>(blockIdx.x >> 1);
+  const long long t0 = static_cast<long long>(blk) * kPage;
+  const long long end = static_cast<long long>(before) + n;
+  const int lo = static_cast<int>(max(t0, static_cast<long long>(before)) - t0);
+  const int hi = static_cast<int>(min(static_cast<long long>(kPage), end - t0));
+  if (n == 0 || hi <= lo) return;
+  if (blk >= a.c.max_pages) {  // past the page table: recorded, not written
+    if (threadIdx.x == 0 && atomicCAS(a.c.status, 0, 1) == 0) atomicExch(a.c.status + 1, 0x20003);
+    return;
+  }
+  if (blockIdx.x & 1) append_page<T, D, VEC, false>(a, b, h, blk, before, lo, hi, red);
+  else append_page<T, D, VEC, true>(a, b, h, blk, before, lo, hi, red);
 }
 
 // ---------------------------------------------------------------- read back
@@ -282,7 +344,10 @@ __global__ void __launch_bounds__(kThreads) k_read(const ReadArgs a) {
 
 // ---------------------------------------------------------------- evict
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelCluster = 4;   // blocks that share a (batch, head)
+constexpr int kSelThreads = 512;
+constexpr int kSelBins = 2048;
+constexpr int kSelKeys = 16384;  // weights a block keeps in shared memory
 
 // A weight as an unsigned key that sorts the same way (-0 as +0, NaN above
 // every number).
@@ -292,77 +357,123 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// One block per (batch, head): which tokens stay.  The first `sink` and the
+// One cluster per (batch, head): which tokens stay.  The first `sink` and the
 // last `recent` do; of the others the ones of largest weight, the lowest
 // index among equal ones.  The smallest weight that stays is found by radix
-// selection (four passes over 8 bits, a 256-bin histogram each), then one
-// sweep in index order writes the survivors, every warp its own run of
-// tokens.
-__global__ void __launch_bounds__(kSelThreads) k_select(const EvictArgs a) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t sh_prefix, sh_need;
-  __shared__ int n_above[32], n_tie[32];
-  const int bh = blockIdx.x, b = bh / a.c.Hkv, h = bh % a.c.Hkv;
+// selection: three passes over 11, 11 and 10 bits (the first digit then splits
+// an octave in four, so a heavy tail spreads over many bins).  Each of the four
+// blocks takes a quarter of the sequence; then a quarter of the bins, summed
+// over the blocks' shared memories; a lone block took 45 us for 26520 tokens
+// and left most SMs idle.  One sweep in index order then writes the survivors, every warp
+// its own run of tokens.  The weights are read from memory once and kept in
+// shared memory where they fit (65536 tokens); longer sequences read them
+// again (L2) in every pass.
+__global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThreads) k_select(const EvictArgs a) {
+  namespace cg = cooperative_groups;
+  extern __shared__ uint32_t sel[];
+  constexpr int W = kSelThreads / 32;
+  static_assert(kSelThreads * kSelCluster == kSelBins, "a bin of the cluster's histogram for every thread");
+  uint32_t* hist = sel;             // [kSelBins]
+  uint32_t* keys = sel + kSelBins;  // [a.sel_keys], of this block's tokens
+  __shared__ uint32_t sh_prefix, sh_need, sh_sum[W], quarter;
+  __shared__ int n_above[W], n_tie[W], total[2];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = static_cast<int>(cluster.block_rank());
+  const int bh = blockIdx.x / kSelCluster, b = bh / a.c.Hkv, h = bh % a.c.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const CacheView& c = a.c;
   const int len = seq_length(c, b);
   const int n = min(len, a.keep);
   int* kept = a.kept + static_cast<size_t>(bh) * a.keep;
-  if (h == 0 && tid == 0) a.lengths_out[b] = n;
-  for (int i = n + tid; i < a.keep; i += kSelThreads) kept[i] = -1;
-  if (n == len) {
-    for (int i = tid; i < n; i += kSelThreads) kept[i] = i;
+  const int all_tid = rank * kSelThreads + tid, all = kSelCluster * kSelThreads;
+  if (h == 0 && all_tid == 0) a.lengths_out[b] = n;
+  for (int i = n + all_tid; i < a.keep; i += all) kept[i] = -1;
+  if (n == len) {  // (the whole cluster leaves)
+    for (int i = all_tid; i < n; i += all) kept[i] = i;
     return;
   }
   // len > keep >= sink + recent: the contested tokens [lo, hi), of which
-  // `need` stay
+  // `need` stay; this block's tokens are [t0, t1), whole pages
   const int lo = a.sink, hi = len - a.recent;
   const int need = n - a.sink - a.recent;
-  auto key = [&](int i) -> uint32_t {
+  const int share = ((len + kSelCluster - 1) / kSelCluster + kPage - 1) / kPage * kPage;
+  const int t0 = min(len, rank * share), t1 = min(len, t0 + share);
+  auto fetch = [&](int i) -> uint32_t {
     const int pg = page_id(c, b, i / kPage);
     if (pg < 0) return 0u;
     return weight_key(c.weight[(static_cast<size_t>(pg) * c.Hkv + h) * kPage + i % kPage]);
   };
+  const bool local = share <= a.sel_keys;
+  if (local && need > 0) {
+    // a half warp a page, 16 bytes a lane
+#pragma unroll 4
+    for (int i = t0 + tid * 4; i < t1; i += kSelThreads * 4) {
+      const int pg = page_id(c, b, i / kPage);
+      float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (pg >= 0)
+        w = *reinterpret_cast<const float4*>(c.weight + (static_cast<size_t>(pg) * c.Hkv + h) * kPage + i % kPage);
+      const bool ok = pg >= 0;
+      *reinterpret_cast<uint4*>(keys + i - t0) = make_uint4(ok ? weight_key(w.x) : 0u, ok ? weight_key(w.y) : 0u,
+                                                            ok ? weight_key(w.z) : 0u, ok ? weight_key(w.w) : 0u);
+    }
+    __syncthreads();
+  }
+  auto key = [&](int i) -> uint32_t { return local ? keys[i - t0] : fetch(i); };
   uint32_t prefix = 0, left = static_cast<uint32_t>(need);
   if (need > 0) {
+    const int c0 = max(t0, lo), c1 = min(t1, hi);
 #pragma unroll 1
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
+    for (int pass = 0; pass < 3; pass++) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+      const uint32_t mask = (1u << bits) - 1u;
+      for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
       __syncthreads();
-      for (int i = lo + tid; i < hi; i += kSelThreads) {
+      for (int i = c0 + tid; i < c1; i += kSelThreads) {
         const uint32_t k = key(i);
-        if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & 0xFF], 1u);
+        if (pass == 0 || (k >> (shift + bits)) == prefix) atomicAdd(&hist[(k >> shift) & mask], 1u);
       }
+      cluster.sync();
+      // this thread's bin, from the top, of the whole cluster
+      const int bin = kSelBins - 1 - all_tid;
+      uint32_t cnt = 0;
+#pragma unroll
+      for (int r = 0; r < kSelCluster; r++) cnt += cluster.map_shared_rank(hist, r)[bin];
+      uint32_t run = cnt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(kFull, run, o);
+        if (lane >= o) run += v;
+      }
+      if (lane == 31) sh_sum[warp] = run;
       __syncthreads();
-      if (warp == 0) {  // the bin in which the count from the top reaches `left`
-        uint32_t s = 0;
-        for (int e = 0; e < 8; e++) s += hist[255 - (lane * 8 + e)];
-        uint32_t run = s;
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t v = __shfl_up_sync(kFull, run, o);
-          if (lane >= o) run += v;
-        }
-        uint32_t at = run - s;  // keys in higher bins than this lane's
-        if (at < left && run >= left) {
-          for (int e = 0; e < 8; e++) {
-            const int bin = 255 - (lane * 8 + e);
-            if (at + hist[bin] >= left) {
-              sh_prefix = (prefix << 8) | static_cast<uint32_t>(bin);
-              sh_need = left - at;
-              break;
-            }
-            at += hist[bin];
-          }
+      uint32_t below = lane < W ? sh_sum[lane] : 0u, mine = lane < warp ? below : 0u;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        below += __shfl_xor_sync(kFull, below, o);
+        mine += __shfl_xor_sync(kFull, mine, o);
+      }
+      if (tid == 0) quarter = below;
+      cluster.sync();
+      uint32_t before = run - cnt + mine;
+#pragma unroll
+      for (int r = 0; r < kSelCluster; r++)
+        if (r < rank) before += *cluster.map_shared_rank(&quarter, r);
+      // the bin in which the count from the top reaches `left`, to all blocks
+      if (before < left && before + cnt >= left) {
+#pragma unroll
+        for (int r = 0; r < kSelCluster; r++) {
+          *cluster.map_shared_rank(&sh_prefix, r) = (prefix << bits) | static_cast<uint32_t>(bin);
+          *cluster.map_shared_rank(&sh_need, r) = left - before;
         }
       }
-      __syncthreads();
+      cluster.sync();
       prefix = sh_prefix;
       left = sh_need;
     }
   }
   // tokens above the threshold `prefix` stay, and the first `left` equal to it
-  const int seg = ((len + 31) / 32 + 31) / 32 * 32;
-  const int s0 = min(len, warp * seg), s1 = min(len, s0 + seg);
+  const int seg = ((t1 - t0 + W - 1) / W + 31) / 32 * 32;
+  const int s0 = min(t1, t0 + warp * seg), s1 = min(t1, s0 + seg);
   // 2: stays, 1: equal to the threshold, 0: goes
   auto judge = [&](int i) -> int {
     if (i < lo || i >= hi) return 2;
@@ -371,21 +482,45 @@ __global__ void __launch_bounds__(kSelThreads) k_select(const EvictArgs a) {
     return k > prefix ? 2 : k == prefix ? 1 : 0;
   };
   int above = 0, tie = 0;
-  for (int i = s0 + lane; i - lane < s1; i += 32) {
-    const int j = i < s1 ? judge(i) : 0;
-    above += __popc(__ballot_sync(kFull, j == 2));
-    tie += __popc(__ballot_sync(kFull, j == 1));
+#pragma unroll 4
+  for (int i = s0 + lane; i < s1; i += 32) {
+    const int j = judge(i);
+    above += j == 2;
+    tie += j == 1;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    above += __shfl_xor_sync(kFull, above, o);
+    tie += __shfl_xor_sync(kFull, tie, o);
   }
   if (lane == 0) {
     n_above[warp] = above;
     n_tie[warp] = tie;
   }
   __syncthreads();
-  int at = 0, ties = 0;
-  for (int w = 0; w < warp; w++) {
-    at += n_above[w];
-    ties += n_tie[w];
+  int a_in = lane < W ? n_above[lane] : 0, t_in = lane < W ? n_tie[lane] : 0;
+  int at = lane < warp ? a_in : 0, ties = lane < warp ? t_in : 0;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    a_in += __shfl_xor_sync(kFull, a_in, o);
+    t_in += __shfl_xor_sync(kFull, t_in, o);
+    at += __shfl_xor_sync(kFull, at, o);
+    ties += __shfl_xor_sync(kFull, ties, o);
   }
+  if (tid == 0) {
+    total[0] = a_in;
+    total[1] = t_in;
+  }
+  cluster.sync();
+#pragma unroll
+  for (int r = 0; r < kSelCluster; r++) {
+    const int* other = cluster.map_shared_rank(total, r);
+    if (r < rank) {
+      at += other[0];
+      ties += other[1];
+    }
+  }
+  cluster.sync();  // no block leaves while another reads its totals
   at += min(ties, static_cast<int>(left));  // of the ties before, the first `left` stay
   for (int i = s0 + lane; i - lane < s1; i += 32) {
     const int j = i < s1 ? judge(i) : 0;
@@ -427,14 +562,11 @@ __device__ __forceinline__ uint32_t abs_max4(uint32_t m, uint32_t w) {
 
 // Block (64 survivors, head, batch): gather their codes, take the page's new
 // scales from them and write the requantized codes to the result's page, or
-// to the staging buffer of an in-place prune.
+// to the staging buffer of an in-place prune.  Every thread finds the places
+// of its own two tokens (three dependent loads, no barrier between them).
 template <int D>
 __global__ void __launch_bounds__(kThreads) k_gather(const EvictArgs a) {
-  __shared__ float red[kThreads / 32];
-  __shared__ int src[kPage];      // token, or -1
-  __shared__ float s_src[kPage];
-  __shared__ int e_src[kPage];
-  __shared__ long long at_src[kPage];
+  __shared__ float red[2][kThreads / 32];
   constexpr int CH = D / 16, PER = kPage * CH / kThreads;
   const CacheView& c = a.c;
   const int b = blockIdx.z, h = blockIdx.y, blk = blockIdx.x, tid = threadIdx.x;
@@ -442,51 +574,40 @@ __global__ void __launch_bounds__(kThreads) k_gather(const EvictArgs a) {
   const int m = min(kPage, n - blk * kPage);
   if (m <= 0 || (!a.pages_out && n == len)) return;
   const size_t ou = (static_cast<size_t>(b) * c.Hkv + h) * gridDim.x + blk;
-  if (tid < kPage) {
-    int t = -1;
-    float s = 0.0f, w = 0.0f;
-    int e = 0;
-    long long at = 0;
-    if (tid < m) {
-      t = a.kept[(static_cast<size_t>(b) * c.Hkv + h) * a.keep + blk * kPage + tid];
-      const int pg = page_id(c, b, t / kPage);
-      if (pg < 0) {
-        t = -1;
-      } else {
-        const size_t unit = static_cast<size_t>(pg) * c.Hkv + h;
-        s = c.k_scale[unit];
-        e = c.v_exp[unit];
-        at = static_cast<long long>(unit * kPage + t % kPage);
-        w = c.weight[at];
+  const int* kept = a.kept + (static_cast<size_t>(b) * c.Hkv + h) * a.keep + blk * kPage;
+  const int d = tid % CH * 16;
+  uint4 kc[PER], vc[PER];
+  float s_src[PER], w[PER];
+  int e_src[PER];
+  bool there[PER];
+#pragma unroll
+  for (int i = 0; i < PER; i++) {
+    const int r = tid / CH + i * (kThreads / CH);
+    kc[i] = vc[i] = make_uint4(0u, 0u, 0u, 0u);
+    s_src[i] = w[i] = 0.0f;
+    e_src[i] = 0;
+    there[i] = false;
+    if (r < m) {
+      const int t = kept[r], pg = page_id(c, b, t / kPage);
+      if (pg >= 0) {
+        const size_t unit = static_cast<size_t>(pg) * c.Hkv + h, at = unit * kPage + t % kPage;
+        kc[i] = *reinterpret_cast<const uint4*>(c.k_i8 + at * D + d);
+        vc[i] = *reinterpret_cast<const uint4*>(c.v_f8 + at * D + d);
+        s_src[i] = c.k_scale[unit];
+        e_src[i] = c.v_exp[unit];
+        if (d == 0) w[i] = c.weight[at];
+        there[i] = true;
       }
     }
-    src[tid] = t;
-    s_src[tid] = s;
-    e_src[tid] = e;
-    at_src[tid] = at;
-    if (a.pages_out) {
-      const int po = page_id(c, a.pages_out, a.out_pages, b, blk);
-      if (po >= 0) c.weight[(static_cast<size_t>(po) * c.Hkv + h) * kPage + tid] = w;
-    } else {
-      stage_of(a.ws, static_cast<size_t>(gridDim.x) * c.Hkv * c.B, D).weight[ou * kPage + tid] = w;
-    }
   }
-  __syncthreads();
-  uint4 kc[PER], vc[PER];
-  float ks = 0.0f;
-  int ve = kMinVExp;
+  int po = 0;
+  if (a.pages_out) {
+    po = page_id(c, a.pages_out, a.out_pages, b, blk);
+    if (po < 0) return;
+  }
+  float ks = 0.0f, vmax = kMinVExp;
 #pragma unroll
   for (int i = 0; i < PER; i++) {
-    const int it = tid + i * kThreads, r = it / CH, d = it % CH * 16;
-    kc[i] = vc[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (src[r] >= 0) {
-      kc[i] = *reinterpret_cast<const uint4*>(c.k_i8 + at_src[r] * D + d);
-      vc[i] = *reinterpret_cast<const uint4*>(c.v_f8 + at_src[r] * D + d);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < PER; i++) {
-    const int it = tid + i * kThreads, r = it / CH;
     // largest |code| of the token: of the thread's 16 channels, then of its
     // CH lanes.  e4m3 codes without their sign order like their values.
     uint32_t mk = 0;
@@ -502,68 +623,87 @@ __global__ void __launch_bounds__(kThreads) k_gather(const EvictArgs a) {
       mk = max(mk, __shfl_xor_sync(kFull, mk, o));
       mv = max(mv, __shfl_xor_sync(kFull, mv, o));
     }
-    if (src[r] >= 0) {
-      ks = fmaxf(ks, __fmul_rn(s_src[r], __fdiv_rn(static_cast<float>(mk), 127.0f)));
+    if (there[i]) {
+      ks = fmaxf(ks, __fmul_rn(s_src[i], __fdiv_rn(static_cast<float>(mk), 127.0f)));
       // |value| = code * 2^e: its exponent is the code's, shifted
-      if (mv) ve = max(ve, value_exp(e4m3_value(mv)) + e_src[r]);
+      if (mv) vmax = fmaxf(vmax, static_cast<float>(value_exp(e4m3_value(mv)) + e_src[i]));
     }
   }
-  ks = block_max(ks, red);
-  ve = static_cast<int>(block_max(static_cast<float>(ve), red));
+  block_max2(ks, vmax, red);
+  const int ve = static_cast<int>(vmax);
 
   int8_t* kd;
   uint8_t* vd;
+  float* wd;
+  float* sd;
+  int8_t* ed;
   if (a.pages_out) {
-    const int po = page_id(c, a.pages_out, a.out_pages, b, blk);
-    if (po < 0) return;
     const size_t unit = static_cast<size_t>(po) * c.Hkv + h;
     kd = c.k_i8 + unit * (kPage * D);
     vd = c.v_f8 + unit * (kPage * D);
-    if (tid == 0) {
-      c.k_scale[unit] = ks;
-      c.v_exp[unit] = static_cast<int8_t>(ve);
-    }
+    wd = c.weight + unit * kPage;
+    sd = c.k_scale + unit;
+    ed = c.v_exp + unit;
   } else {
     const Stage st = stage_of(a.ws, static_cast<size_t>(gridDim.x) * c.Hkv * c.B, D);
     kd = st.k + ou * (kPage * D);
     vd = st.v + ou * (kPage * D);
-    if (tid == 0) {
-      st.scale[ou] = ks;
-      st.exp[ou] = static_cast<int8_t>(ve);
-    }
+    wd = st.weight + ou * kPage;
+    sd = st.scale + ou;
+    ed = st.exp + ou;
+  }
+  if (tid == 0) {
+    *sd = ks;
+    *ed = static_cast<int8_t>(ve);
   }
 #pragma unroll
   for (int i = 0; i < PER; i++) {
-    const int it = tid + i * kThreads, r = it / CH, d = it % CH * 16;
+    const int r = tid / CH + i * (kThreads / CH);
+    if (d == 0) wd[r] = w[i];
     uint32_t kw[4] = {kc[i].x, kc[i].y, kc[i].z, kc[i].w};
     uint32_t vw[4] = {vc[i].x, vc[i].y, vc[i].z, vc[i].w};
-    if (s_src[r] != ks) {
-      const float s = s_src[r], ratio = ks > 0.0f ? s / ks : 0.0f;
+    if (s_src[i] != ks) {
+      // round-half-even(code * ratio) in the low byte of the sum with 1.5 *
+      // 2^23 (one rounding); next to a tie of any of the 16, fp64 decides.
+      // |code| * s_src <= 127 ks for every survivor, so nothing clamps.
+      const float s = s_src[i], ratio = ks > 0.0f ? s / ks : 0.0f;
+      float worst = 0.0f;
+      uint32_t o[4];
 #pragma unroll
       for (int j = 0; j < 4; j++) {
-        uint32_t o = 0;
+        const uint32_t u = kw[j] ^ 0x80808080u;
+        float y[4];
 #pragma unroll
         for (int e = 0; e < 4; e++) {
-          const int code = static_cast<int8_t>(kw[j] >> (8 * e));
-          // as key_code: the quotient in fp32, in fp64 next to a tie
-          const float q = static_cast<float>(code) * ratio, f = rintf(q);
-          const int r8 = fabsf(fabsf(q - f) - 0.5f) < 6.1035156e-5f
-                             ? rescale_key(code, s, ks)
-                             : max(-127, min(127, static_cast<int>(f)));
-          o |= static_cast<uint32_t>(r8 & 0xFF) << (8 * e);
+          // 2^23 + (code + 128), less 2^23 + 128
+          const float x = __fsub_rn(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540 + e)), 8388736.0f);
+          y[e] = fmaf(x, ratio, kRound);
+          worst = fmaxf(worst, fabsf(fmaf(x, ratio, __fsub_rn(kRound, y[e]))));
         }
-        kw[j] = o;
+        o[j] = low_bytes(y[0], y[1], y[2], y[3]);
       }
-    }
-    const int diff = e_src[r] - ve;
-    if (diff != 0 && src[r] >= 0) {
-      // diff > 0 happens where a page's largest tokens went: exact, as the
-      // new exponent covers every survivor
-      const float up = diff < -60 ? 0.0f : pow2i(min(diff, 126));
+      if (worst > 0.5f - kNearTie) {
 #pragma unroll
-      for (int j = 0; j < 4; j++)
-        vw[j] = cvt_e4m3x4(e4m3_value(vw[j] & 0xFF) * up, e4m3_value((vw[j] >> 8) & 0xFF) * up,
-                           e4m3_value((vw[j] >> 16) & 0xFF) * up, e4m3_value(vw[j] >> 24) * up);
+        for (int j = 0; j < 4; j++) o[j] = rescale_keys(kw[j], s, ks);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; j++) kw[j] = o[j];
+    }
+    const int diff = e_src[i] - ve;
+    if (diff != 0 && there[i]) {
+      // e4m3 values times 2^diff: exact in fp16 for |diff| <= 15 (diff > 0
+      // happens where a page's largest tokens went; the new exponent covers
+      // every survivor), so only the step back to e4m3 rounds
+      if (diff >= -15 && diff <= 15) {
+        const __half2 up = __half2half2(__ushort_as_half(static_cast<unsigned short>((diff + 15) << 10)));
+        const __half2 lo2 = __half2half2(__float2half_rn(pow2i(diff)));
+        const __half2 f = diff == -15 ? lo2 : up;  // 2^-15 is a subnormal number
+#pragma unroll
+        for (int j = 0; j < 4; j++) vw[j] = scale_values(vw[j], f);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++) vw[j] = rescale_values(vw[j], diff);
+      }
     }
     *reinterpret_cast<uint4*>(kd + r * D + d) = make_uint4(kw[0], kw[1], kw[2], kw[3]);
     *reinterpret_cast<uint4*>(vd + r * D + d) = make_uint4(vw[0], vw[1], vw[2], vw[3]);
@@ -606,7 +746,7 @@ void append_d(const AppendArgs& a, bool vec, dim3 grid, cudaStream_t s) {
 
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t s) {
   // n tokens touch at most this many pages, wherever the first one starts
-  const dim3 grid((a.n + kPage - 2) / kPage + 1, a.c.Hkv, a.c.B);
+  const dim3 grid(2 * ((a.n + kPage - 2) / kPage + 1), a.c.Hkv, a.c.B);
   const long long st = a.kb | a.kh | a.kn | a.vb | a.vh | a.vn;
   const bool vec = ((reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) & 15u) == 0 &&
                    st % 8 == 0;
@@ -632,8 +772,17 @@ size_t cache_evict_ws_bytes(int B, int Hkv, int D, int keep) {
   return (units * (2ull * kPage * D + kPage * 4 + 4 + 1) + 15) / 16 * 16;
 }
 
-cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
-  k_select<<<a.c.B * a.c.Hkv, kSelThreads, 0, s>>>(a);
+cudaError_t cache_evict_prepare() {
+  return cudaFuncSetAttribute(k_select, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (kSelBins + kSelKeys) * 4);
+}
+
+cudaError_t launch_cache_evict(const EvictArgs& args, cudaStream_t s) {
+  EvictArgs a = args;
+  // shared memory for a block's share of as many weights as the page table holds
+  const long long share = (static_cast<long long>(a.c.max_pages) + kSelCluster - 1) / kSelCluster * kPage;
+  a.sel_keys = static_cast<int>(share < kSelKeys ? share : kSelKeys);
+  k_select<<<a.c.B * a.c.Hkv * kSelCluster, kSelThreads, (kSelBins + a.sel_keys) * 4, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const dim3 grid((a.keep + kPage - 1) / kPage, a.c.Hkv, a.c.B);

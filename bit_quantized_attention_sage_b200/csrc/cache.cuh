@@ -186,8 +186,10 @@ struct EvictArgs {
   int* lengths_out;  // [B]
   const int* pages_out;  // [B][out_pages], or null: in place through the workspace
   int out_pages;
+  int sel_keys;  // weights that k_select keeps in shared memory
   void* ws;
 };
+cudaError_t cache_evict_prepare();
 size_t cache_evict_ws_bytes(int B, int Hkv, int D, int keep);
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s);
 

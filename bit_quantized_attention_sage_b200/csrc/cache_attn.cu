@@ -839,6 +839,7 @@ cudaError_t cache_prepare() {
   if (e == cudaSuccess) e = prepare_d<64>();
   if (e == cudaSuccess) e = cache_prefill_prepare();
   if (e == cudaSuccess) e = cache_weights_prepare();
+  if (e == cudaSuccess) e = cache_evict_prepare();
   return e;
 }
 

@@ -123,32 +123,51 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const RopeArgs a, int til
     const int nr = HALF ? R2 / V : a.R / V;
     const int per = nr + (a.D - a.R) / V;
     const int items = nt * per;
-    for (int hi = 0; hi < nh; hi++) {
-      const T* xh = x + a.xh * (h0 + hi);
-      T* yh = y + a.yh * (h0 + hi);
-      for (int i = threadIdx.x; i < items; i += kRopeThreads) {
-        const int t = i / per, c = i - t * per;
-        const T* xr = xh + a.xn * (n0 + t);
-        T* yr = yh + a.yn * (n0 + t);
-        float f[V];
-        if (c >= nr) {
-          const int d = a.R + (c - nr) * V;
-          *reinterpret_cast<uint4*>(yr + d) = *reinterpret_cast<const uint4*>(xr + d);
-        } else if constexpr (HALF) {
-          const int d = c * V;
-          float g[V];
-          unpack16<T>(*reinterpret_cast<const uint4*>(xr + d), f);
-          unpack16<T>(*reinterpret_cast<const uint4*>(xr + R2 + d), g);
+    // an item's channels are the same in every head, and so are its angles;
+    // four heads' loads are in flight at once
+    constexpr int U = 4;
+    for (int i = threadIdx.x; i < items; i += kRopeThreads) {
+      const int t = i / per, c = i - t * per;
+      const bool pass = c >= nr;
+      const int d = pass ? a.R + (c - nr) * V : c * V;
+      constexpr int P = HALF ? V : V / 2;  // pairs of an item
+      float2 w[P];
+      if (!pass) {
 #pragma unroll
-          for (int e = 0; e < V; e++) rotate(f[e], g[e], cs[t * R2 + d + e]);
-          *reinterpret_cast<uint4*>(yr + d) = pack16<T>(f);
-          *reinterpret_cast<uint4*>(yr + R2 + d) = pack16<T>(g);
-        } else {
-          const int d = c * V;
-          unpack16<T>(*reinterpret_cast<const uint4*>(xr + d), f);
+        for (int e = 0; e < P; e++) w[e] = cs[t * R2 + (HALF ? d : d / 2) + e];
+      }
+      const T* xr = x + a.xh * h0 + a.xn * (n0 + t) + d;
+      T* yr = y + a.yh * h0 + a.yn * (n0 + t) + d;
+      for (int hi = 0; hi < nh; hi += U) {
+        uint4 u[U], v[U];
 #pragma unroll
-          for (int e = 0; e < V; e += 2) rotate(f[e], f[e + 1], cs[t * R2 + (d + e) / 2]);
-          *reinterpret_cast<uint4*>(yr + d) = pack16<T>(f);
+        for (int k = 0; k < U; k++) {
+          if (hi + k >= nh) break;
+          const T* p = xr + a.xh * (hi + k);
+          u[k] = *reinterpret_cast<const uint4*>(p);
+          if (HALF && !pass) v[k] = *reinterpret_cast<const uint4*>(p + R2);
+        }
+#pragma unroll
+        for (int k = 0; k < U; k++) {
+          if (hi + k >= nh) break;
+          T* p = yr + a.yh * (hi + k);
+          if (pass) {
+            *reinterpret_cast<uint4*>(p) = u[k];
+            continue;
+          }
+          float f[V];
+          unpack16<T>(u[k], f);
+          if constexpr (HALF) {
+            float g[V];
+            unpack16<T>(v[k], g);
+#pragma unroll
+            for (int e = 0; e < V; e++) rotate(f[e], g[e], w[e]);
+            *reinterpret_cast<uint4*>(p + R2) = pack16<T>(g);
+          } else {
+#pragma unroll
+            for (int e = 0; e < V; e += 2) rotate(f[e], f[e + 1], w[e / 2]);
+          }
+          *reinterpret_cast<uint4*>(p) = pack16<T>(f);
         }
       }
     }
