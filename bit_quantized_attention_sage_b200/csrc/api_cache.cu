@@ -351,11 +351,11 @@ SAGE_EXPORT sage_status sage_cache_weights(const sage_kv_cache* cache, const sag
   return status_of(launch_cache_weights_few(maps, a, static_cast<cudaStream_t>(stream)));
 }
 
-SAGE_EXPORT size_t sage_cache_evict_workspace_bytes(int B, int heads, int D, int keep) {
+SAGE_EXPORT size_t sage_cache_evict_workspace_bytes(int B, int heads, int D, int keep, int in_place) {
   if (B < 1 || B > 65535 || heads < 1 || heads > 65535 || (D != 64 && D != 128) || keep < 1 ||
       keep > (1 << 30))
     return 0;
-  return cache_evict_ws_bytes(B, heads, D, keep);
+  return cache_evict_ws_bytes(B, heads, D, keep, in_place != 0);
 }
 
 SAGE_EXPORT sage_status sage_cache_evict(const sage_kv_cache* cache, const sage_kv_seqs* seqs, int keep,
@@ -368,12 +368,10 @@ SAGE_EXPORT sage_status sage_cache_evict(const sage_kv_cache* cache, const sage_
     return SAGE_ERR_INVALID_ARG;
   if (!al(kept, 4) || !al(lengths_out, 4)) return SAGE_ERR_INVALID_ARG;
   const int need = (keep + kPage - 1) / kPage;
-  if (pages_out) {
-    if (!al(pages_out, 4) || out_pages < need) return SAGE_ERR_INVALID_ARG;
-  } else if (!al(workspace, 16) ||
-             workspace_bytes < cache_evict_ws_bytes(seqs->B, cache->heads, cache->D, keep)) {
+  if (pages_out && (!al(pages_out, 4) || out_pages < need)) return SAGE_ERR_INVALID_ARG;
+  if (!al(workspace, 16) ||
+      workspace_bytes < cache_evict_ws_bytes(seqs->B, cache->heads, cache->D, keep, !pages_out))
     return SAGE_ERR_INVALID_ARG;
-  }
   if (!cache_fits(cache) || static_cast<long long>(seqs->B) * cache->heads > (1 << 28))
     return SAGE_ERR_UNSUPPORTED;
   int* status = api_status_word();

@@ -12,6 +12,7 @@
 #include <cuda_fp16.h>
 
 #include "cache.cuh"
+#include "cache_dev.cuh"
 #include "sm100.cuh"
 
 namespace sage {
@@ -21,7 +22,8 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kThreads = 256;
 
 constexpr float kRound = 12582912.0f;       // 1.5 * 2^23
-constexpr float kNearTie = 6.1035156e-5f;   // 2^-14: four times the error of x * (1 / s) at 127
+constexpr float kNearTie = 3.0517578e-5f;   // 2^-15: twice the error of x * fp32(1 / s) at 127
+constexpr float kNearTieScaled = 1.5258789e-5f;  // 2^-16: twice that of code * fp32(s / s')
 
 // The low bytes of four words as one.
 __device__ __forceinline__ uint32_t low_bytes(float a, float b, float c, float d) {
@@ -165,25 +167,6 @@ __device__ __forceinline__ float block_max(float v, float* red) {
 #pragma unroll
   for (int i = 1; i < kThreads / 32; i++) m = fmaxf(m, red[i]);
   return m;
-}
-
-// Two maxima at once.
-__device__ __forceinline__ void block_max2(float& a, float& b, float (*red)[kThreads / 32]) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    a = fmaxf(a, __shfl_xor_sync(kFull, a, o));
-    b = fmaxf(b, __shfl_xor_sync(kFull, b, o));
-  }
-  if ((threadIdx.x & 31) == 0) {
-    red[0][threadIdx.x >> 5] = a;
-    red[1][threadIdx.x >> 5] = b;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; i++) {
-    a = fmaxf(a, red[0][i]);
-    b = fmaxf(b, red[1][i]);
-  }
 }
 
 // ---------------------------------------------------------------- append
@@ -375,6 +358,7 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
   static_assert(kSelThreads * kSelCluster == kSelBins, "a bin of the cluster's histogram for every thread");
   uint32_t* hist = sel;             // [kSelBins]
   uint32_t* keys = sel + kSelBins;  // [a.sel_keys], of this block's tokens
+  int* unit = reinterpret_cast<int*>(keys + a.sel_keys);  // [a.sel_keys / 64]: (page, head) of its pages, or -1
   __shared__ uint32_t sh_prefix, sh_need, sh_sum[W], quarter;
   __shared__ int n_above[W], n_tie[W], total[2];
   cg::cluster_group cluster = cg::this_cluster();
@@ -385,11 +369,19 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
   const int len = seq_length(c, b);
   const int n = min(len, a.keep);
   int* kept = a.kept + static_cast<size_t>(bh) * a.keep;
+  int* from = a.from + static_cast<size_t>(bh) * a.keep;
+  auto unit_of = [&](int i) {
+    const int pg = page_id(c, b, i / kPage);
+    return pg < 0 ? -1 : pg * c.Hkv + h;
+  };
   const int all_tid = rank * kSelThreads + tid, all = kSelCluster * kSelThreads;
   if (h == 0 && all_tid == 0) a.lengths_out[b] = n;
-  for (int i = n + all_tid; i < a.keep; i += all) kept[i] = -1;
+  for (int i = n + all_tid; i < a.keep; i += all) kept[i] = from[i] = -1;
   if (n == len) {  // (the whole cluster leaves)
-    for (int i = all_tid; i < n; i += all) kept[i] = i;
+    for (int i = all_tid; i < n; i += all) {
+      kept[i] = i;
+      from[i] = unit_of(i);
+    }
     return;
   }
   // len > keep >= sink + recent: the contested tokens [lo, hi), of which
@@ -399,20 +391,19 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
   const int share = ((len + kSelCluster - 1) / kSelCluster + kPage - 1) / kPage * kPage;
   const int t0 = min(len, rank * share), t1 = min(len, t0 + share);
   auto fetch = [&](int i) -> uint32_t {
-    const int pg = page_id(c, b, i / kPage);
-    if (pg < 0) return 0u;
-    return weight_key(c.weight[(static_cast<size_t>(pg) * c.Hkv + h) * kPage + i % kPage]);
+    const int u = unit_of(i);
+    return u < 0 ? 0u : weight_key(c.weight[static_cast<size_t>(u) * kPage + i % kPage]);
   };
   const bool local = share <= a.sel_keys;
-  if (local && need > 0) {
+  if (local) {
     // a half warp a page, 16 bytes a lane
 #pragma unroll 4
     for (int i = t0 + tid * 4; i < t1; i += kSelThreads * 4) {
-      const int pg = page_id(c, b, i / kPage);
+      const int u = unit_of(i);
       float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (pg >= 0)
-        w = *reinterpret_cast<const float4*>(c.weight + (static_cast<size_t>(pg) * c.Hkv + h) * kPage + i % kPage);
-      const bool ok = pg >= 0;
+      if (u >= 0) w = *reinterpret_cast<const float4*>(c.weight + static_cast<size_t>(u) * kPage + i % kPage);
+      const bool ok = u >= 0;
+      if (i % kPage == 0) unit[(i - t0) / kPage] = u;
       *reinterpret_cast<uint4*>(keys + i - t0) = make_uint4(ok ? weight_key(w.x) : 0u, ok ? weight_key(w.y) : 0u,
                                                             ok ? weight_key(w.z) : 0u, ok ? weight_key(w.w) : 0u);
     }
@@ -528,7 +519,10 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
     const uint32_t mt = __ballot_sync(kFull, j == 1);
     const bool stay = j == 2 || (j == 1 && ties + __popc(mt & lower) < static_cast<int>(left));
     const uint32_t ms = __ballot_sync(kFull, stay);
-    if (stay) kept[at + __popc(ms & lower)] = i;
+    if (stay) {
+      kept[at + __popc(ms & lower)] = i;
+      from[at + __popc(ms & lower)] = local ? unit[(i - t0) / kPage] : unit_of(i);
+    }
     at += __popc(ms);
     ties += __popc(mt);
   }
@@ -556,158 +550,173 @@ __host__ __device__ inline Stage stage_of(void* ws, size_t units, int D) {
   return s;
 }
 
-__device__ __forceinline__ uint32_t abs_max4(uint32_t m, uint32_t w) {
-  return __vmaxu4(m, __vabsss4(w));  // per byte; -128 (never written) reads as 127
+// The page's new scale from its survivors, and their requantized codes to the
+// result's page, or to the staging buffer of an in-place prune.
+template <int D, bool KEYS, int PER>
+__device__ __forceinline__ void requantize(const EvictArgs& a, int h, int po, size_t units, size_t ou,
+                                           const uint4 (&x)[PER], const float (&s_src)[PER],
+                                           const int (&e_src)[PER], const float (&w)[PER],
+                                           const bool (&there)[PER], float* red) {
+  constexpr int CH = D / 16;
+  const CacheView& c = a.c;
+  const int tid = threadIdx.x, d = tid % CH * 16;
+  float top = KEYS ? 0.0f : static_cast<float>(kMinVExp);  // scale, or exponent
+#pragma unroll
+  for (int i = 0; i < PER; i++) {
+    // largest |code| or |value| of the token, in fp16 (exact): of the
+    // thread's 16 channels, then of its CH lanes
+    const uint32_t q[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    __half2 m2 = __half2half2(__ushort_as_half(0));
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      uint32_t p0, p1;
+      if (KEYS)
+        i8x4_to_f16(q[j], p0, p1);
+      else
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(p0), "=r"(p1) : "r"(q[j]));
+      m2 = __hmax2(m2, __hmax2(__habs2(*reinterpret_cast<const __half2*>(&p0)), __habs2(*reinterpret_cast<const __half2*>(&p1))));
+    }
+#pragma unroll
+    for (int o = CH / 2; o; o >>= 1) m2 = __hmax2(m2, __shfl_xor_sync(kFull, m2, o));
+    const float big = fmaxf(__low2float(m2), __high2float(m2));
+    if (there[i]) {
+      if (KEYS)
+        top = fmaxf(top, __fmul_rn(s_src[i], __fdiv_rn(fminf(big, 127.0f), 127.0f)));  // -128 is never written
+      else if (big > 0.0f)  // |value| = code * 2^e: its exponent is the code's, shifted
+        top = fmaxf(top, static_cast<float>(value_exp(big) + e_src[i]));
+    }
+  }
+  top = block_max(top, red);
+  const int ve = static_cast<int>(top);
+
+  uint8_t* dst;
+  if (a.pages_out) {
+    const size_t unit = static_cast<size_t>(po) * c.Hkv + h;
+    dst = (KEYS ? reinterpret_cast<uint8_t*>(c.k_i8) : c.v_f8) + unit * (kPage * D);
+    if (KEYS) {
+      if (tid == 0) c.k_scale[unit] = top;
+#pragma unroll
+      for (int i = 0; i < PER; i++)
+        if (d == 0) c.weight[unit * kPage + tid / CH + i * (kThreads / CH)] = w[i];
+    } else if (tid == 0) {
+      c.v_exp[unit] = static_cast<int8_t>(ve);
+    }
+  } else {
+    const Stage st = stage_of(a.ws, units, D);
+    dst = (KEYS ? reinterpret_cast<uint8_t*>(st.k) : st.v) + ou * (kPage * D);
+    if (KEYS) {
+      if (tid == 0) st.scale[ou] = top;
+#pragma unroll
+      for (int i = 0; i < PER; i++)
+        if (d == 0) st.weight[ou * kPage + tid / CH + i * (kThreads / CH)] = w[i];
+    } else if (tid == 0) {
+      st.exp[ou] = static_cast<int8_t>(ve);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < PER; i++) {
+    const int r = tid / CH + i * (kThreads / CH);
+    uint32_t q[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    if constexpr (KEYS) {
+      if (s_src[i] != top) {
+        // round-half-even(code * ratio) in the low byte of the sum with 1.5 *
+        // 2^23 (one rounding); next to a tie of any of the 16 fp64 decides.
+        // |code| * s_src <= 127 top for every survivor, so nothing clamps.
+        const float s = s_src[i], ratio = top > 0.0f ? s / top : 0.0f;
+        float worst = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          uint32_t p0, p1;
+          i8x4_to_f16(q[j], p0, p1);
+          const float2 a2 = __half22float2(*reinterpret_cast<const __half2*>(&p0));
+          const float2 b2 = __half22float2(*reinterpret_cast<const __half2*>(&p1));
+          const float f[4] = {a2.x, a2.y, b2.x, b2.y};
+          float y[4], rem[4];
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            y[e] = fmaf(f[e], ratio, kRound);
+            rem[e] = fabsf(fmaf(f[e], ratio, __fsub_rn(kRound, y[e])));
+          }
+          worst = fmax3(worst, fmax3(rem[0], rem[1], rem[2]), rem[3]);
+          q[j] = low_bytes(y[0], y[1], y[2], y[3]);
+        }
+        if (worst > 0.5f - kNearTieScaled) {
+          q[0] = rescale_keys(x[i].x, s, top);
+          q[1] = rescale_keys(x[i].y, s, top);
+          q[2] = rescale_keys(x[i].z, s, top);
+          q[3] = rescale_keys(x[i].w, s, top);
+        }
+      }
+    } else {
+      const int diff = e_src[i] - ve;
+      if (diff != 0 && there[i]) {
+        // e4m3 values times 2^diff: exact in fp16 for |diff| <= 15 (diff > 0
+        // happens where a page's largest tokens went; the new exponent covers
+        // every survivor), so only the step back to e4m3 rounds
+        if (diff >= -15 && diff <= 15) {
+          const __half2 f = __half2half2(__float2half_rn(pow2i(diff)));
+#pragma unroll
+          for (int j = 0; j < 4; j++) q[j] = scale_values(q[j], f);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; j++) q[j] = rescale_values(q[j], diff);
+        }
+      }
+    }
+    *reinterpret_cast<uint4*>(dst + r * D + d) = make_uint4(q[0], q[1], q[2], q[3]);
+  }
 }
 
-// Block (64 survivors, head, batch): gather their codes, take the page's new
-// scales from them and write the requantized codes to the result's page, or
-// to the staging buffer of an in-place prune.  Every thread finds the places
-// of its own two tokens (three dependent loads, no barrier between them).
+// Block (64 survivors, head, batch).  A block is mostly the latency of its
+// dependent loads, so there are two steps of them: the places of the thread's
+// tokens (which the selection left with their page already looked up), the
+// result's page and the lengths; then keys, values, scales and weights.
 template <int D>
-__global__ void __launch_bounds__(kThreads) k_gather(const EvictArgs a) {
-  __shared__ float red[2][kThreads / 32];
+__global__ void __launch_bounds__(kThreads, 4) k_gather(const EvictArgs a) {
+  __shared__ float red[kThreads / 32];
   constexpr int CH = D / 16, PER = kPage * CH / kThreads;
   const CacheView& c = a.c;
-  const int b = blockIdx.z, h = blockIdx.y, blk = blockIdx.x, tid = threadIdx.x;
-  const int len = seq_length(c, b), n = min(len, a.keep);
-  const int m = min(kPage, n - blk * kPage);
-  if (m <= 0 || (!a.pages_out && n == len)) return;
-  const size_t ou = (static_cast<size_t>(b) * c.Hkv + h) * gridDim.x + blk;
-  const int* kept = a.kept + (static_cast<size_t>(b) * c.Hkv + h) * a.keep + blk * kPage;
-  const int d = tid % CH * 16;
-  uint4 kc[PER], vc[PER];
+  const int b = blockIdx.z, h = blockIdx.y, blk = blockIdx.x, blocks = gridDim.x;
+  const int tid = threadIdx.x, d = tid % CH * 16;
+  const int n = __ldg(a.lengths_out + b), len = a.pages_out ? 0 : seq_length(c, b);
+  const size_t list = (static_cast<size_t>(b) * c.Hkv + h) * a.keep + blk * kPage;
+  int t[PER], unit[PER];
+#pragma unroll
+  for (int i = 0; i < PER; i++) {
+    const int r = tid / CH + i * (kThreads / CH);
+    t[i] = unit[i] = -1;
+    if (blk * kPage + r < a.keep) {
+      t[i] = a.kept[list + r];
+      unit[i] = a.from[list + r];
+    }
+  }
+  const int po = a.pages_out ? page_id(c, a.pages_out, a.out_pages, b, blk, n > blk * kPage) : 0;
+  if (n <= blk * kPage || po < 0 || (!a.pages_out && n == len)) return;
+  uint4 k[PER], v[PER];
   float s_src[PER], w[PER];
   int e_src[PER];
   bool there[PER];
 #pragma unroll
   for (int i = 0; i < PER; i++) {
-    const int r = tid / CH + i * (kThreads / CH);
-    kc[i] = vc[i] = make_uint4(0u, 0u, 0u, 0u);
+    k[i] = v[i] = make_uint4(0u, 0u, 0u, 0u);
     s_src[i] = w[i] = 0.0f;
     e_src[i] = 0;
-    there[i] = false;
-    if (r < m) {
-      const int t = kept[r], pg = page_id(c, b, t / kPage);
-      if (pg >= 0) {
-        const size_t unit = static_cast<size_t>(pg) * c.Hkv + h, at = unit * kPage + t % kPage;
-        kc[i] = *reinterpret_cast<const uint4*>(c.k_i8 + at * D + d);
-        vc[i] = *reinterpret_cast<const uint4*>(c.v_f8 + at * D + d);
-        s_src[i] = c.k_scale[unit];
-        e_src[i] = c.v_exp[unit];
-        if (d == 0) w[i] = c.weight[at];
-        there[i] = true;
-      }
-    }
-  }
-  int po = 0;
-  if (a.pages_out) {
-    po = page_id(c, a.pages_out, a.out_pages, b, blk);
-    if (po < 0) return;
-  }
-  float ks = 0.0f, vmax = kMinVExp;
-#pragma unroll
-  for (int i = 0; i < PER; i++) {
-    // largest |code| of the token: of the thread's 16 channels, then of its
-    // CH lanes.  e4m3 codes without their sign order like their values.
-    uint32_t mk = 0;
-    mk = abs_max4(abs_max4(abs_max4(abs_max4(mk, kc[i].x), kc[i].y), kc[i].z), kc[i].w);
-    uint32_t mv = __vmaxu4(__vmaxu4(vc[i].x & 0x7F7F7F7Fu, vc[i].y & 0x7F7F7F7Fu),
-                           __vmaxu4(vc[i].z & 0x7F7F7F7Fu, vc[i].w & 0x7F7F7F7Fu));
-    mk = __vmaxu4(mk, mk >> 16);
-    mk = max(mk & 0xFF, (mk >> 8) & 0xFF);
-    mv = __vmaxu4(mv, mv >> 16);
-    mv = max(mv & 0xFF, (mv >> 8) & 0xFF);
-#pragma unroll
-    for (int o = CH / 2; o; o >>= 1) {
-      mk = max(mk, __shfl_xor_sync(kFull, mk, o));
-      mv = max(mv, __shfl_xor_sync(kFull, mv, o));
-    }
+    there[i] = unit[i] >= 0;
     if (there[i]) {
-      ks = fmaxf(ks, __fmul_rn(s_src[i], __fdiv_rn(static_cast<float>(mk), 127.0f)));
-      // |value| = code * 2^e: its exponent is the code's, shifted
-      if (mv) vmax = fmaxf(vmax, static_cast<float>(value_exp(e4m3_value(mv)) + e_src[i]));
+      const size_t at = static_cast<size_t>(unit[i]) * kPage + t[i] % kPage;
+      k[i] = *reinterpret_cast<const uint4*>(c.k_i8 + at * D + d);
+      v[i] = *reinterpret_cast<const uint4*>(c.v_f8 + at * D + d);
+      s_src[i] = c.k_scale[unit[i]];
+      e_src[i] = c.v_exp[unit[i]];
+      if (d == 0) w[i] = c.weight[at];
     }
   }
-  block_max2(ks, vmax, red);
-  const int ve = static_cast<int>(vmax);
-
-  int8_t* kd;
-  uint8_t* vd;
-  float* wd;
-  float* sd;
-  int8_t* ed;
-  if (a.pages_out) {
-    const size_t unit = static_cast<size_t>(po) * c.Hkv + h;
-    kd = c.k_i8 + unit * (kPage * D);
-    vd = c.v_f8 + unit * (kPage * D);
-    wd = c.weight + unit * kPage;
-    sd = c.k_scale + unit;
-    ed = c.v_exp + unit;
-  } else {
-    const Stage st = stage_of(a.ws, static_cast<size_t>(gridDim.x) * c.Hkv * c.B, D);
-    kd = st.k + ou * (kPage * D);
-    vd = st.v + ou * (kPage * D);
-    wd = st.weight + ou * kPage;
-    sd = st.scale + ou;
-    ed = st.exp + ou;
-  }
-  if (tid == 0) {
-    *sd = ks;
-    *ed = static_cast<int8_t>(ve);
-  }
-#pragma unroll
-  for (int i = 0; i < PER; i++) {
-    const int r = tid / CH + i * (kThreads / CH);
-    if (d == 0) wd[r] = w[i];
-    uint32_t kw[4] = {kc[i].x, kc[i].y, kc[i].z, kc[i].w};
-    uint32_t vw[4] = {vc[i].x, vc[i].y, vc[i].z, vc[i].w};
-    if (s_src[i] != ks) {
-      // round-half-even(code * ratio) in the low byte of the sum with 1.5 *
-      // 2^23 (one rounding); next to a tie of any of the 16, fp64 decides.
-      // |code| * s_src <= 127 ks for every survivor, so nothing clamps.
-      const float s = s_src[i], ratio = ks > 0.0f ? s / ks : 0.0f;
-      float worst = 0.0f;
-      uint32_t o[4];
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const uint32_t u = kw[j] ^ 0x80808080u;
-        float y[4];
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-          // 2^23 + (code + 128), less 2^23 + 128
-          const float x = __fsub_rn(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540 + e)), 8388736.0f);
-          y[e] = fmaf(x, ratio, kRound);
-          worst = fmaxf(worst, fabsf(fmaf(x, ratio, __fsub_rn(kRound, y[e]))));
-        }
-        o[j] = low_bytes(y[0], y[1], y[2], y[3]);
-      }
-      if (worst > 0.5f - kNearTie) {
-#pragma unroll
-        for (int j = 0; j < 4; j++) o[j] = rescale_keys(kw[j], s, ks);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; j++) kw[j] = o[j];
-    }
-    const int diff = e_src[i] - ve;
-    if (diff != 0 && there[i]) {
-      // e4m3 values times 2^diff: exact in fp16 for |diff| <= 15 (diff > 0
-      // happens where a page's largest tokens went; the new exponent covers
-      // every survivor), so only the step back to e4m3 rounds
-      if (diff >= -15 && diff <= 15) {
-        const __half2 up = __half2half2(__ushort_as_half(static_cast<unsigned short>((diff + 15) << 10)));
-        const __half2 lo2 = __half2half2(__float2half_rn(pow2i(diff)));
-        const __half2 f = diff == -15 ? lo2 : up;  // 2^-15 is a subnormal number
-#pragma unroll
-        for (int j = 0; j < 4; j++) vw[j] = scale_values(vw[j], f);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; j++) vw[j] = rescale_values(vw[j], diff);
-      }
-    }
-    *reinterpret_cast<uint4*>(kd + r * D + d) = make_uint4(kw[0], kw[1], kw[2], kw[3]);
-    *reinterpret_cast<uint4*>(vd + r * D + d) = make_uint4(vw[0], vw[1], vw[2], vw[3]);
-  }
+  const size_t units = static_cast<size_t>(blocks) * c.Hkv * c.B;
+  const size_t ou = (static_cast<size_t>(b) * c.Hkv + h) * blocks + blk;
+  requantize<D, true>(a, h, po, units, ou, k, s_src, e_src, w, there, red);
+  requantize<D, false>(a, h, po, units, ou, v, s_src, e_src, w, there, red);
 }
 
 // In place: the staged blocks into the sequence's own first pages.
@@ -767,14 +776,19 @@ cudaError_t launch_cache_read(const ReadArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-size_t cache_evict_ws_bytes(int B, int Hkv, int D, int keep) {
+// The survivors' (page, head), then, in place, the staged blocks.
+size_t cache_evict_list_bytes(int B, int Hkv, int keep) {
+  return (static_cast<size_t>(B) * Hkv * keep * 4 + 15) / 16 * 16;
+}
+size_t cache_evict_ws_bytes(int B, int Hkv, int D, int keep, bool in_place) {
   const size_t units = static_cast<size_t>(B) * Hkv * ((keep + kPage - 1) / kPage);
-  return (units * (2ull * kPage * D + kPage * 4 + 4 + 1) + 15) / 16 * 16;
+  return cache_evict_list_bytes(B, Hkv, keep) +
+         (in_place ? (units * (2ull * kPage * D + kPage * 4 + 4 + 1) + 15) / 16 * 16 : 0);
 }
 
 cudaError_t cache_evict_prepare() {
   return cudaFuncSetAttribute(k_select, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (kSelBins + kSelKeys) * 4);
+                              (kSelBins + kSelKeys + kSelKeys / kPage) * 4);
 }
 
 cudaError_t launch_cache_evict(const EvictArgs& args, cudaStream_t s) {
@@ -782,7 +796,9 @@ cudaError_t launch_cache_evict(const EvictArgs& args, cudaStream_t s) {
   // shared memory for a block's share of as many weights as the page table holds
   const long long share = (static_cast<long long>(a.c.max_pages) + kSelCluster - 1) / kSelCluster * kPage;
   a.sel_keys = static_cast<int>(share < kSelKeys ? share : kSelKeys);
-  k_select<<<a.c.B * a.c.Hkv * kSelCluster, kSelThreads, (kSelBins + a.sel_keys) * 4, s>>>(a);
+  a.from = static_cast<int*>(args.ws);
+  a.ws = static_cast<char*>(args.ws) + cache_evict_list_bytes(a.c.B, a.c.Hkv, a.keep);
+  k_select<<<a.c.B * a.c.Hkv * kSelCluster, kSelThreads, (kSelBins + a.sel_keys + a.sel_keys / kPage) * 4, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const dim3 grid((a.keep + kPage - 1) / kPage, a.c.Hkv, a.c.B);

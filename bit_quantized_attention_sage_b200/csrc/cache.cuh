@@ -54,11 +54,12 @@ __device__ __forceinline__ int seq_length(const CacheView& c, int b) {
 }
 
 // Page id of block blk of sequence b in a table of `width` columns, or -1
-// (recorded) if it is no page.
-__device__ __forceinline__ int page_id(const CacheView& c, const int* table, int width, int b, int blk) {
+// (recorded, if `record`) if it is no page.
+__device__ __forceinline__ int page_id(const CacheView& c, const int* table, int width, int b, int blk,
+                                       bool record = true) {
   const int pg = __ldg(table + static_cast<size_t>(b) * width + blk);
   if (static_cast<unsigned>(pg) >= static_cast<unsigned>(c.n_pages)) {
-    if (atomicCAS(c.status, 0, 1 /* SAGE_ERR_INVALID_ARG */) == 0) atomicExch(c.status + 1, 0x20002);
+    if (record && atomicCAS(c.status, 0, 1 /* SAGE_ERR_INVALID_ARG */) == 0) atomicExch(c.status + 1, 0x20002);
     return -1;
   }
   return pg;
@@ -187,10 +188,11 @@ struct EvictArgs {
   const int* pages_out;  // [B][out_pages], or null: in place through the workspace
   int out_pages;
   int sel_keys;  // weights that k_select keeps in shared memory
+  int* from;     // [B][Hkv][keep]: the survivors' (page, head)
   void* ws;
 };
 cudaError_t cache_evict_prepare();
-size_t cache_evict_ws_bytes(int B, int Hkv, int D, int keep);
+size_t cache_evict_ws_bytes(int B, int Hkv, int D, int keep, bool in_place);
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s);
 
 struct CacheAttnMaps {

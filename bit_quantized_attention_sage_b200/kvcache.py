@@ -73,7 +73,7 @@ def declare(L):
     L.sage_cache_weights.restype = I
     L.sage_cache_weights.argtypes = [P, P, P, I, I, I, I, P, I, P]
     L.sage_cache_evict_workspace_bytes.restype = SZ
-    L.sage_cache_evict_workspace_bytes.argtypes = [I] * 4
+    L.sage_cache_evict_workspace_bytes.argtypes = [I] * 5
     L.sage_cache_evict.restype = I
     L.sage_cache_evict.argtypes = [P, P, I, I, I, P, I, P, P, P, SZ, P]
 
@@ -545,15 +545,14 @@ def cache_evict(cache, pages, lengths, keep, sink=0, recent=0, pages_out=None, w
     out = torch.empty_like(lengths)
     if sq.B == 0:
         return kept, out
-    if po is None and workspace is None:
-        n = _lib().sage_cache_evict_workspace_bytes(sq.B, cache.kv_heads, cache.head_dim, keep)
-        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=cache.device)
-    if workspace is not None and (workspace.device != cache.device or
-                                  not workspace.is_contiguous()):
+    if workspace is None:
+        n = _lib().sage_cache_evict_workspace_bytes(sq.B, cache.kv_heads, cache.head_dim, keep,
+                                                    po is None)
+        workspace = lengths.new_empty((max(n, 16),), dtype=torch.uint8)
+    elif workspace.device != cache.device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on %s" % cache.device)
     _check(_lib().sage_cache_evict(
         ctypes.byref(cache.struct()), ctypes.byref(sq), keep, sink, recent, po, width,
-        kept.data_ptr(), out.data_ptr(), None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), st),
-        "sage_cache_evict")
+        kept.data_ptr(), out.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), st), "sage_cache_evict")
     return kept, out

@@ -696,8 +696,9 @@ sage_status sage_cache_weights(const sage_kv_cache *cache, const sage_kv_seqs *s
                                const sage_kv_query *query, int mask, int mask_block, int win,
                                int sink, const float *lse, int accumulate, void *stream);
 
-/* Workspace of sage_cache_evict in place, bytes (0: invalid arguments). */
-size_t sage_cache_evict_workspace_bytes(int B, int heads, int D, int keep);
+/* Workspace of sage_cache_evict, bytes (0: invalid arguments): the survivors'
+ * pages and, in place (pages_out = NULL), the result before it is copied. */
+size_t sage_cache_evict_workspace_bytes(int B, int heads, int D, int keep, int in_place);
 
 /* Cut every sequence and head to at most `keep` tokens: the first `sink`, the
  * last `recent` and, of the others, those of largest weight (the lowest index
@@ -710,8 +711,8 @@ size_t sage_cache_evict_workspace_bytes(int B, int heads, int D, int keep);
  * its codes and scales).  Their weights move along.
  *   pages_out   device int32 [B, out_pages], out_pages >= ceil(keep / 64):
  *               where they go; these pages must not be among the pages read
- *               or appear twice.  NULL: the sequence's own first pages,
- *               through the workspace; sequences of at most `keep` tokens then
+ *               or appear twice.  NULL: the sequence's own first pages;
+ *               sequences of at most `keep` tokens then
  *               stay as they are.
  *   kept        int32 [B, heads, keep]: the survivors' old places, then -1
  *   lengths_out int32 [B]: min(length, keep); must not be seqs->lengths */

@@ -105,18 +105,20 @@ def test_attention_arguments(L):
 
 
 def test_evict_arguments_and_workspace(L):
-    need = L.sage_cache_evict_workspace_bytes(2, 2, 128, 100)
-    # two staged pages a sequence and head: codes, weights, scale, exponent
-    assert need == -(-(2 * 2 * 2 * (2 * 64 * 128 + 64 * 4 + 4 + 1)) // 16) * 16
+    need = L.sage_cache_evict_workspace_bytes(2, 2, 128, 100, 1)
+    # a place for every survivor; in place two staged pages a sequence and
+    # head: codes, weights, scale, exponent
+    assert L.sage_cache_evict_workspace_bytes(2, 2, 128, 100, 0) == 2 * 2 * 100 * 4
+    assert need == 1600 + -(-(2 * 2 * 2 * (2 * 64 * 128 + 64 * 4 + 4 + 1)) // 16) * 16
     for a in ((0, 2, 128, 100), (2, 0, 128, 100), (2, 2, 96, 100), (2, 2, 128, 0)):
-        assert L.sage_cache_evict_workspace_bytes(*a) == 0
+        assert L.sage_cache_evict_workspace_bytes(*a, 1) == 0
 
     def call(keep=100, sink=0, recent=0, po=None, width=0, kept=P, lo=P, ws=P, nb=need, c=None):
         return L.sage_cache_evict(c or cache(), seqs(), keep, sink, recent, po, width, kept, lo, ws, nb,
                                   None)
 
     for kw in (dict(keep=0), dict(sink=-1), dict(recent=-1), dict(sink=60, recent=41), dict(po=P, width=1),
-               dict(po=ODD, width=2), dict(kept=None), dict(lo=None), dict(ws=None), dict(nb=need - 1),
+               dict(po=ODD, width=2), dict(po=P, width=2, nb=1599), dict(kept=None), dict(lo=None), dict(ws=None), dict(nb=need - 1),
                dict(ws=ctypes.c_void_p(4100)), dict(c=cache(weight=None))):
         assert call(**kw) == 1, kw
 
