@@ -69,13 +69,31 @@ __device__ __forceinline__ uint32_t op_off(int r, int ch) {
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-// D[tmem] = A B^T over D channels of two K-major operand tiles.
+// The fixed upper words of the operand descriptors (128-byte swizzle, 8-row
+// groups 1024 bytes apart); the lower word holds the address / 16 and the
+// leading offset: unused (1) for K-major tiles, from run to run of 64 channels
+// (16 KB) for the MN-major V.
+constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29);
+constexpr uint32_t kDescLoK = 1u << 16, kDescLoV = (16384u >> 4) << 16;
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(kDescHi));
+  return d;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// D[tmem] = A B^T over D channels of two K-major operand tiles, given by the
+// lower words of their descriptors.
 template <int D>
 __device__ __forceinline__ void mma_rows(uint32_t tmem, uint32_t a, uint32_t b, uint32_t idesc) {
 #pragma unroll
   for (int kk = 0; kk < D / 16; kk++) {
-    const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-    mma_f16_ss(tmem, smem_desc_kmajor(a + off, 128), smem_desc_kmajor(b + off, 128), idesc, kk > 0);
+    const uint32_t off = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
+    mma_f16_ss(tmem, desc_of(a + off), desc_of(b + off), idesc, kk > 0);
   }
 }
 
@@ -142,17 +160,6 @@ __device__ __forceinline__ void stage_rows(const CacheAttnArgs& a, int b, int h,
       if (i % CH == 0) factor[i / CH] = pow2i(p);
     }
   }
-}
-
-// 16 codes of a row's chunk pair 2 c, 2 c + 1.  Lanes of the upper half of a
-// 128-channel row store their chunks in the other order, so that eight lanes
-// always hit eight different banks.
-template <int D>
-__device__ __forceinline__ void store_pair(uint8_t* tile, int row, int c, const uint32_t (&o)[8]) {
-  const int sw = D == 128 ? c >> 2 : 0;
-  const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-  *reinterpret_cast<uint4*>(tile + op_off(row, 2 * c + sw)) = sw ? hi : lo;
-  *reinterpret_cast<uint4*>(tile + op_off(row, 2 * c + (sw ^ 1))) = sw ? lo : hi;
 }
 
 __device__ __forceinline__ int query_len(const CacheAttnArgs& a, int b) {

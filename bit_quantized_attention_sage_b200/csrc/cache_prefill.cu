@@ -66,22 +66,6 @@ struct alignas(1024) PreSmem {
   int abort;
 };
 
-// The fixed upper words of the operand descriptors (128-byte swizzle, 8-row
-// groups 1024 bytes apart); the lower word holds the address / 16 and the
-// leading offset: unused (1) for K-major tiles, from run to run of 64 channels
-// (16 KB) for the MN-major V.
-constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29);
-constexpr uint32_t kDescLoK = 1u << 16, kDescLoV = (16384u >> 4) << 16;
-__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(kDescHi));
-  return d;
-}
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
 // D[tmem] (+)= A[tmem] B[smem], f16 operands, fp32 accumulator.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
                                            uint32_t accumulate) {
@@ -258,16 +242,6 @@ __device__ __forceinline__ void convert(PreSmem<D>& s, const CacheAttnArgs& a, c
 
 // ---------------------------------------------------------------- tensor core
 
-// S = Q K^T: q and k are the operands' lower descriptor words.
-template <int D>
-__device__ __forceinline__ void issue_qk(uint32_t tS, uint32_t q, uint32_t k) {
-  constexpr uint32_t id = idesc_f16(BM, BN);
-#pragma unroll
-  for (int kk = 0; kk < D / 16; kk++) {
-    const uint32_t off = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
-    mma_f16_ss(tS, desc_of(q + off), desc_of(k + off), id, kk > 0);
-  }
-}
 // O (+)= P V of 64 keys.
 template <int D>
 __device__ __forceinline__ void issue_pv(uint32_t tP, uint32_t tO, uint32_t v, bool first) {
@@ -294,7 +268,7 @@ __device__ __forceinline__ void issue(PreSmem<D>& s, uint32_t tmem, int nk, int 
     tc_fence_after();
     if (elect_one()) {
       for (int t = 0; t < tiles; t++) {
-        issue_qk<D>(tmem + t * BN, q0 + t * kTile, k0);
+        mma_rows<D>(tmem + t * BN, q0 + t * kTile, k0, idesc_f16(BM, BN));
         mma_commit(&s.s_full[t]);
       }
       mma_commit(&s.k_empty[0]);
@@ -320,7 +294,7 @@ __device__ __forceinline__ void issue(PreSmem<D>& s, uint32_t tmem, int nk, int 
         issue_pv<D>(tS + 32, tO, v0 + st * kTile + kHalf, false);
         if (t == tiles - 1) mma_commit(&s.v_empty[st]);
         if (more) {
-          issue_qk<D>(tS, q0 + t * kTile, k0 + sn * kTile);
+          mma_rows<D>(tS, q0 + t * kTile, k0 + sn * kTile, idesc_f16(BM, BN));
           if (t == tiles - 1) mma_commit(&s.k_empty[sn]);
         }
         mma_commit(&s.s_full[t]);  // the next S, or the finished O

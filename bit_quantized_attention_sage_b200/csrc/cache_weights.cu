@@ -36,10 +36,9 @@ template <int D>
 struct alignas(1024) WgtSmem {
   uint8_t k[2][128 * D * 2];  // fp16 operand tiles of 128 keys
   uint8_t q[kRows * D * 2];   // and of the query rows
-  float factor[kRows];
-  float c[kRows], nl[kRows];  // factor * scale * log2(e); -lse * log2(e)
+  float c[kRows], nl[kRows];  // power of two * scale * log2(e); -lse * log2(e)
   KeyRange kr[kRows];
-  uint64_t done;
+  uint64_t done[2];           // scores of the two key tiles
   uint32_t tmem_base;
   int abort;
 };
@@ -56,20 +55,66 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "memory");
 }
 
-// Codes of 256 keys, 16 bytes a chunk: page p of the pass holds chunks
-// [p * 64 * CH, ...), so a chunk's page is known from its index.
+// A thread's chunks (16 codes) of 256 keys: chunk column c, rows row0 + i *
+// STEP.  Eight neighbouring lanes take four chunks of two rows, so that their
+// 16-byte stores hit eight different banks; a warp still reads whole rows.
+template <int D>
+struct KeyChunks {
+  static constexpr int CH = D / 16, N = kKeys * CH / kThreads, STEP = kKeys / N;
+  int c, row0;
+  uint32_t off0, off1;
+  __device__ __forceinline__ explicit KeyChunks(int tid) {
+    const int lane = tid & 31, w = tid >> 5;
+    if (D == 128) {
+      c = (lane & 3) | ((lane >> 1) & 4);
+      row0 = w * 4 + ((lane >> 2) & 1) + ((lane >> 3) & 2);
+    } else {
+      c = lane & 3;
+      row0 = w * 8 + (lane >> 2);
+    }
+    off0 = op_off(row0, 2 * c);
+    off1 = op_off(row0, 2 * c + 1);
+  }
+};
 template <int D>
 __device__ __forceinline__ void load_keys(uint4 (&r)[D / 16], const CacheAttnArgs& a, const int (&unit)[4],
-                                          int tid) {
-  constexpr int CH = D / 16;
+                                          const KeyChunks<D>& ch) {
+  using K = KeyChunks<D>;
 #pragma unroll
-  for (int i = 0; i < CH; i++) {
-    const int row = tid / CH + i * (kThreads / CH), c = tid % CH;
-    // kThreads / CH rows a step: 32 (D = 128) or 64 (D = 64), within one page
-    const int u = unit[i * (kThreads / CH) / kPage];
-    r[i] = u < 0 ? make_uint4(0u, 0u, 0u, 0u)
-                 : __ldg(reinterpret_cast<const uint4*>(
-                       a.c.k_i8 + (static_cast<size_t>(u) * kPage + (row & (kPage - 1))) * D + c * 16));
+  for (int p = 0; p < 4; p++) {
+    const int8_t* src = a.c.k_i8 + static_cast<size_t>(max(unit[p], 0)) * (kPage * D) + ch.row0 * D + ch.c * 16;
+#pragma unroll
+    for (int i = 0; i < K::N / 4; i++)
+      r[p * (K::N / 4) + i] = unit[p] < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                                          : __ldg(reinterpret_cast<const uint4*>(src + i * K::STEP * D));
+  }
+}
+
+// acc += exp2(S ks c - lse) over N query rows (columns n0 on); rows that do not
+// see key j add nothing.
+template <int D, int N>
+__device__ __forceinline__ void add_columns(const WgtSmem<D>& s, const uint32_t (&r)[N], int n0, float2 k2,
+                                            bool all, long long j, float2 (&acc)[2]) {
+#pragma unroll
+  for (int e = 0; e < N; e += 4) {
+    const float4 c = *reinterpret_cast<const float4*>(s.c + n0 + e);
+    const float4 nl = *reinterpret_cast<const float4*>(s.nl + n0 + e);
+    float2 x = __fmul2_rn(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), k2);
+    float2 y = __fmul2_rn(make_float2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), k2);
+    x = __ffma2_rn(x, make_float2(c.x, c.y), make_float2(nl.x, nl.y));
+    y = __ffma2_rn(y, make_float2(c.z, c.w), make_float2(nl.z, nl.w));
+    x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+    y = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+    if (!all) {
+      float* f[4] = {&x.x, &x.y, &y.x, &y.y};
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        const KeyRange k = s.kr[n0 + e + q];
+        if (!(j < k.sink || (j >= k.lo && j < k.hi))) *f[q] = 0.0f;
+      }
+    }
+    acc[0] = __fadd2_rn(acc[0], x);
+    acc[1] = __fadd2_rn(acc[1], y);
   }
 }
 
@@ -78,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_cache_weights(const CacheAttnAr
   extern __shared__ __align__(1024) uint8_t raw[];
   if (smem_misaligned(raw, a.c.status)) return;
   WgtSmem<D>& s = *reinterpret_cast<WgtSmem<D>*>(raw);
-  constexpr int CH = D / 16;
+  constexpr int CH = D / 16;  // chunks of a thread
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int chunk = static_cast<int>(blockIdx.x % a.chunks), bh = static_cast<int>(blockIdx.x / a.chunks);
   const int b = bh / a.c.Hkv, h = bh % a.c.Hkv;
@@ -90,7 +135,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_cache_weights(const CacheAttnAr
   if (p0 >= p1) return;
   const long long off = static_cast<long long>(len) - qn;
   if (tid == 0) {
-    mbar_init(&s.done, 1);
+    mbar_init(&s.done[0], 1);
+    mbar_init(&s.done[1], 1);
     s.abort = 0;
     fence_mbar_init();
   }
@@ -106,36 +152,47 @@ __global__ void __launch_bounds__(kThreads, 2) k_cache_weights(const CacheAttnAr
       u[i] = pg < 0 ? -1 : pg * a.c.Hkv + h;
     }
   };
-  int unit[4];
+  // the pass's pages, and the next one's: a pass ahead of their codes, which
+  // are a pass ahead of their conversion
+  int unit[4], next[4];
   units(p0, unit);
   uint4 kr[CH];
-  load_keys<D>(kr, a, unit, tid);
+  const KeyChunks<D> ch(tid);
+  load_keys<D>(kr, a, unit, ch);
+  units(p0 + 4, next);
 
   const int tile = warp >> 2, quad = warp & 3;
   const int key = tile * 128 + quad * 32 + lane;  // of the pass
   int staged = -1;                                // row block in s.q
   uint32_t phase = 0;
-  bool ok = true;
-  for (int p = p0; p < p1 && ok; p += 4) {
+  bool ok = true;    // of this warp: a wait that ran out makes it false for good
+  bool live = true;  // of the block, as of its last barrier
+  bool pending = false;
+  for (int p = p0; p < p1 && live; p += 4) {
 #pragma unroll
-    for (int i = 0; i < CH; i++) {
-      const int row = tid / CH + i * (kThreads / CH), c = tid % CH;
+    for (int i = 0; i < KeyChunks<D>::N; i++) {
       const uint32_t w[4] = {kr[i].x, kr[i].y, kr[i].z, kr[i].w};
       uint32_t o[8];
 #pragma unroll
       for (int j = 0; j < 4; j++) i8x4_to_f16(w[j], o[2 * j], o[2 * j + 1]);
-      store_pair<D>(s.k[row >> 7], row & 127, c, o);
+      // rows 128 on are the second tile, which follows the first
+      const uint32_t at = i * KeyChunks<D>::STEP < 128 ? i * KeyChunks<D>::STEP * 128
+                                                      : 128 * D * 2 + (i * KeyChunks<D>::STEP - 128) * 128;
+      *reinterpret_cast<uint4*>(s.k[0] + ch.off0 + at) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(s.k[0] + ch.off1 + at) = make_uint4(o[4], o[5], o[6], o[7]);
     }
     // this thread's key
     const int mu = quad < 2 ? (tile ? unit[2] : unit[0]) : (tile ? unit[3] : unit[1]);
     const float ks = mu < 0 ? 0.0f : __ldg(a.c.k_scale + mu);
     const long long j = static_cast<long long>(p) * kPage + key;
     const int mine = mu;
-    units(p + 4, unit);
-    load_keys<D>(kr, a, unit, tid);
+    load_keys<D>(kr, a, next, ch);
+#pragma unroll
+    for (int i = 0; i < 4; i++) unit[i] = next[i];
+    units(p + 8, next);
     float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
     const int first = p * kPage, last = min(len, first + kKeys);
-    for (int rb = 0; rb < rows && ok; rb += kRows) {
+    for (int rb = 0; rb < rows; rb += kRows) {
       const int nr = min(kRows, rows - rb), n = (nr + 15) / 16 * 16;
       // does any row of the block see any of these keys, and all see all?
       const KeyRange ra = key_range(a.mask, off + rb / a.G, len);
@@ -144,9 +201,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_cache_weights(const CacheAttnAr
       if (none) continue;
       const bool all = min(ra.sink, rz.sink) >= last || (rz.lo <= first && ra.hi >= last);
       if (staged != rb) {
+        if (staged >= 0) __syncthreads();  // the last block's products and constants are done with
         staged = rb;
-        stage_rows<D, kThreads>(a, b, h, rb, rows, n, s.q, s.factor, tid);
-        __syncthreads();
         if (tid < n) {
           float nl = -INFINITY;  // a row that saw nothing, or is not there: weight 0
           KeyRange k{0, 0, 0};
@@ -156,54 +212,50 @@ __global__ void __launch_bounds__(kThreads, 2) k_cache_weights(const CacheAttnAr
             if (v != -INFINITY) nl = -v * kLog2e;
             k = key_range(a.mask, off + tok, len);
           }
-          s.c[tid] = s.factor[tid] * (a.scale * kLog2e);
           s.nl[tid] = nl;
           s.kr[tid] = k;
         }
+        stage_rows<D, kThreads>(a, b, h, rb, rows, n, s.q, s.c, tid);
+        __syncthreads();
+        if (tid < n) s.c[tid] *= a.scale * kLog2e;
       }
       fence_proxy_async_smem();
       tc_fence_before();
-      __syncthreads();
+      live = !__syncthreads_or(!ok);
+      if (!live) break;
       tc_fence_after();
       const uint32_t tmem = s.tmem_base;
-      if (tid == 0) {
-        mma_rows<D>(tmem, smem_u32(s.k[0]), smem_u32(s.q), idesc_f16(128, n));
-        if (last - first > 128) mma_rows<D>(tmem + 128, smem_u32(s.k[1]), smem_u32(s.q), idesc_f16(128, n));
-        mma_commit(&s.done);
+      if (warp == 0) {
+        const uint32_t q0 = kDescLoK | (smem_u32(s.q) >> 4), k0 = kDescLoK | (smem_u32(s.k[0]) >> 4);
+        if (elect_one()) {
+          mma_rows<D>(tmem, k0, q0, idesc_f16(128, n));
+          mma_commit(&s.done[0]);
+          if (last - first > 128) mma_rows<D>(tmem + 128, k0 + ((128 * D * 2) >> 4), q0, idesc_f16(128, n));
+          mma_commit(&s.done[1]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
-      ok = __syncthreads_and(mbar_wait(&s.done, phase, wc, kSiteWgtMma));
+      ok = ok && __all_sync(kFull, mbar_wait(&s.done[tile], phase, wc, kSiteWgtMma));
       phase ^= 1;
-      if (!ok) break;
+      pending = true;
       tc_fence_after();
-      if (tile * 128 < last - first) {
+      if (ok && tile * 128 < last - first) {
         const uint32_t tS = tmem + tile * 128 + (static_cast<uint32_t>(quad * 32) << 16);
         const float2 k2 = make_float2(ks, ks);
+        // 64 columns at a time (the load's latency is paid once for them),
+        // the rest in steps of 16
+        int n0 = 0;
 #pragma unroll 1
-        for (int n0 = 0; n0 < n; n0 += 16) {
+        for (; n0 + 64 <= n; n0 += 64) {
+          uint32_t r[64];
+          tmem_ld64(tS + n0, r);
+          add_columns<D, 64>(s, r, n0, k2, all, j, acc);
+        }
+#pragma unroll 1
+        for (; n0 < n; n0 += 16) {
           uint32_t r[16];
           tmem_ld16(tS + n0, r);
-#pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            const float4 c = *reinterpret_cast<const float4*>(s.c + n0 + e);
-            const float4 nl = *reinterpret_cast<const float4*>(s.nl + n0 + e);
-            float2 x = __fmul2_rn(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), k2);
-            float2 y = __fmul2_rn(make_float2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), k2);
-            x = __ffma2_rn(x, make_float2(c.x, c.y), make_float2(nl.x, nl.y));
-            y = __ffma2_rn(y, make_float2(c.z, c.w), make_float2(nl.z, nl.w));
-            x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-            y = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-            if (!all) {
-              float* f[4] = {&x.x, &x.y, &y.x, &y.y};
-#pragma unroll
-              for (int q = 0; q < 4; q++) {
-                const KeyRange k = s.kr[n0 + e + q];
-                if (!(j < k.sink || (j >= k.lo && j < k.hi))) *f[q] = 0.0f;
-              }
-            }
-            acc[0] = __fadd2_rn(acc[0], x);
-            acc[1] = __fadd2_rn(acc[1], y);
-          }
+          add_columns<D, 16>(s, r, n0, k2, all, j, acc);
         }
       }
     }
@@ -215,18 +267,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_cache_weights(const CacheAttnAr
     }
     // the operand tiles and TMEM are free again
     tc_fence_before();
-    __syncthreads();
+    live = !__syncthreads_or(!ok);
     tc_fence_after();
   }
-  if (!ok) {
-    // a wait ran out (recorded): give the products in flight their time
-    if (tid == 0) {
-      const long long t0 = clock64();
-      while (!mbar_try_wait(&s.done, phase ^ 1) && clock64() - t0 < wc.budget) {
-      }
+  // Both tiles' last products are done before their shared memory and TMEM
+  // go (after a wait that ran out, recorded, that takes its time once more).
+  if (pending && tid == 0) {
+    const long long t0 = clock64();
+    while (!mbar_try_wait(&s.done[1], phase ^ 1) && clock64() - t0 < wc.budget) {
     }
-    __syncthreads();
   }
+  __syncthreads();
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(s.tmem_base, 256);
