@@ -335,12 +335,8 @@ SAGE_EXPORT sage_status sage_cache_weights(const sage_kv_cache* cache, const sag
   const int pages = std::max(1, (query->max_len + kPage - 1) / kPage);
   const long long units = static_cast<long long>(seqs->B) * cache->heads;
   if (static_cast<long long>(a.Nq) * a.G > kDecRows) {
-    // Two blocks an SM, each with query rows to stage before its first key:
-    // ranges that leave one round of blocks.
-    const long long want = std::max(1ll, 2ll * sms / units);
-    a.chunk_pages = static_cast<int>(((pages + want - 1) / want + 3) / 4 * 4);
-    a.chunks = (pages + a.chunk_pages - 1) / a.chunk_pages;
-    if (units * a.chunks > (1ll << 31) - 1) return SAGE_ERR_UNSUPPORTED;
+    // a block an SM, with eight pages each at least
+    a.chunks = static_cast<int>(std::min<long long>(sms, (units * pages + 7) / 8));
     return status_of(launch_cache_weights(a, static_cast<cudaStream_t>(stream)));
   }
   // up to 16 query rows the keys stream past one mma.sync tile

@@ -121,11 +121,6 @@ struct TileMeta {
   int unit;  // (page, head)
 };
 
-struct PlaceSmem {
-  long long sum[kWarps];
-  long long before;
-  int b;
-};
 template <int D>
 struct alignas(1024) DecSmem {
   uint8_t kv[kWarps][kStages][2][kHalf * D];  // TMA tiles: K, V
@@ -133,7 +128,7 @@ struct alignas(1024) DecSmem {
   float rowf[kDecRows];                       // power of two * scale * log2(e) of each row
   float ml[kWarps][kDecRows][2];
   TileMeta meta[kWarps][kStages];
-  PlaceSmem place;
+  PlaceSmem<kWarps> place;
   uint64_t full[kWarps][kStages];
   int abort;
 };
@@ -145,13 +140,11 @@ __device__ __forceinline__ void stage_limbs(DecSmem<D>& s, const CacheAttnArgs& 
   constexpr int CH = D / 8;
   for (int i = threadIdx.x; i < n * CH; i += kWarps * 32) {
     const int r = i / CH, c = i % CH;
+    const long long at[1] = {r < rows ? q8_at(a, b, h, r, c) : -1};
+    uint4 raw[1];
+    load_q8(a, at, raw);
     float f[8];
-    if (r < rows) {
-      load_q8(a, a.qb * b + a.qh * (static_cast<size_t>(h) * a.G + r % a.G) + a.qn * (r / a.G) + c * 8, f);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; e++) f[e] = 0.0f;
-    }
+    q8_floats(a, raw[0], f);
     float m = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(f[e]));
@@ -176,99 +169,6 @@ __device__ __forceinline__ void stage_limbs(DecSmem<D>& s, const CacheAttnArgs& 
     if (c == 0) s.rowf[r] = pow2i(p) * (a.scale * kLog2e);
   }
 }
-
-// ---------------------------------------------------------------- shares of the work
-//
-// The work of a call is a line of pages: sequences in order, in each the key
-// heads, in each head the pages its rows visit.  Block c of C takes the c-th
-// of C equal stretches of it, so uneven sequences cost no tail and a block's
-// start (its first dependent loads and tile, some 4 us) is paid once, not
-// once for every range of a fixed length.  A stretch cuts at most two heads:
-// the partial result of a head begun by an earlier block goes to slot 2 c,
-// that of one a later block finishes to slot 2 c + 1.
-
-// Pages of sequence b that count (0: nothing to do; at least 1 where rows
-// have to be written).
-template <bool WEIGHTS>
-__device__ __forceinline__ PageRuns seq_runs(const CacheAttnArgs& a, int b, int len, int qn) {
-  PageRuns r;
-  if constexpr (WEIGHTS) {  // every page: those that no row sees get 0
-    r.n = r.ns = (len + kPage - 1) / kPage;
-    r.gap = 0;
-  } else {
-    const long long off = static_cast<long long>(len) - qn;
-    r = page_runs(a.mask, off, off + max(qn - 1, 0), len);
-  }
-  return r;
-}
-template <bool WEIGHTS>
-__device__ __forceinline__ int seq_work(const CacheAttnArgs& a, int b) {
-  const int len = seq_length(a.c, b), qn = query_len(a, b);
-  if (WEIGHTS) return seq_runs<WEIGHTS>(a, b, len, qn).n;
-  return qn == 0 ? 0 : max(1, seq_runs<WEIGHTS>(a, b, len, qn).n);
-}
-
-__device__ __forceinline__ long long share_start(long long work, int c, int n) { return work * c / n; }
-// The block whose stretch holds position x.
-__device__ __forceinline__ int share_of(long long work, long long x, int n) {
-  return static_cast<int>(((x + 1) * n - 1) / work);
-}
-
-struct Place {
-  long long work;    // of the whole call, pages
-  long long before;  // pages of one head before sequence b
-  int b;
-};
-// By a block of kWarps * 32 threads: the whole work, and the sequence that
-// position x (a function of the work) lies in.
-template <bool WEIGHTS, typename X>
-__device__ __forceinline__ Place locate(PlaceSmem& s, const CacheAttnArgs& a, X x) {
-  constexpr int NT = kWarps * 32;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int first = tid < a.c.B ? seq_work<WEIGHTS>(a, tid) : 0;
-  long long mine = first;
-  for (int b = tid + NT; b < a.c.B; b += NT) mine += seq_work<WEIGHTS>(a, b);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(kFull, mine, o);
-  if (lane == 0) s.sum[warp] = mine;
-  if (tid == 0) s.b = a.c.B;
-  __syncthreads();
-  Place p{0, 0, 0};
-#pragma unroll
-  for (int w = 0; w < kWarps; w++) p.work += s.sum[w];
-  p.work *= a.c.Hkv;
-  const long long at = x(p.work);
-  long long base = 0;  // of the 128 sequences from b0 on
-  for (int b0 = 0; b0 < a.c.B; b0 += NT) {
-    const int n = b0 == 0 ? first : b0 + tid < a.c.B ? seq_work<WEIGHTS>(a, b0 + tid) : 0;
-    long long run = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(kFull, run, o);
-      if (lane >= o) run += v;
-    }
-    __syncthreads();
-    if (lane == 31) s.sum[warp] = run;
-    __syncthreads();
-    long long all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; w++) {
-      if (w < warp) run += s.sum[w];
-      all += s.sum[w];
-    }
-    if ((base + run - n) * a.c.Hkv <= at && at < (base + run) * a.c.Hkv) {
-      s.b = b0 + tid;
-      s.before = base + run - n;
-    }
-    base += all;
-    if (base * a.c.Hkv > at) break;
-  }
-  __syncthreads();
-  p.b = s.b;
-  p.before = s.before;
-  return p;
-}
-
 
 // One head's pages [p0, p1) (of the runs its rows visit): attention, or the
 // weights.  `seen` counts the warp's tiles so far (the ring's phase).
@@ -661,7 +561,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     return;
   }
   // (locate's barriers also publish the ring's)
-  const Place pl = locate<WEIGHTS>(s.place, a, [&](long long w) { return share_start(w, c, n); });
+  const Place pl = locate<kWarps, WEIGHTS>(s.place, a, [&](long long w) { return share_start(w, c, n); });
   if (!WEIGHTS) cudaTriggerProgrammaticLaunchCompletion();
   long long x = share_start(pl.work, c, n);
   const long long end = share_start(pl.work, c + 1, n);

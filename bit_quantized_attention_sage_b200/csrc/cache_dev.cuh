@@ -40,11 +40,6 @@ __device__ __forceinline__ int row_power(float amax) {
   return max(-126, min(static_cast<int>(u >> 23) - 127 - 14, 126));
 }
 
-__device__ __forceinline__ float load_q(const void* q, int type, size_t i) {
-  return type == kTypeBf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(q)[i])
-                           : __half2float(static_cast<const __half*>(q)[i]);
-}
-
 // Two neighbouring channels of one output row.
 __device__ __forceinline__ void store_o2(const CacheAttnArgs& a, size_t i, float x, float y) {
   if (a.type == kTypeBf16) {
@@ -97,26 +92,69 @@ __device__ __forceinline__ void mma_rows(uint32_t tmem, uint32_t a, uint32_t b, 
   }
 }
 
-// Eight channels of the query as fp32.
-__device__ __forceinline__ void load_q8(const CacheAttnArgs& a, size_t i, float (&f)[8]) {
+// UN chunks of eight channels of the query, as they lie (at[u] < 0: zeros);
+// all loads are on their way before the first is waited for.
+template <int UN>
+__device__ __forceinline__ void load_q8(const CacheAttnArgs& a, const long long (&at)[UN], uint4 (&r)[UN]) {
+  const uint16_t* q = static_cast<const uint16_t*>(a.q);
   if (a.q_vec) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + i));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      if (a.type == kTypeBf16) {
-        f[2 * j] = __uint_as_float(w[j] << 16);
-        f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-      } else {
-        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-        f[2 * j] = x.x;
-        f[2 * j + 1] = x.y;
-      }
-    }
+    for (int u = 0; u < UN; u++)
+      r[u] = at[u] < 0 ? make_uint4(0u, 0u, 0u, 0u) : __ldg(reinterpret_cast<const uint4*>(q + at[u]));
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; j++) f[j] = load_q(a.q, a.type, i + j);
+    for (int u = 0; u < UN; u++) {
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+      if (at[u] >= 0) {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+          w[j] = __ldg(q + at[u] + 2 * j) | static_cast<uint32_t>(__ldg(q + at[u] + 2 * j + 1)) << 16;
+      }
+      r[u] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
+}
+__device__ __forceinline__ void q8_floats(const CacheAttnArgs& a, const uint4& u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    if (a.type == kTypeBf16) {
+      f[2 * j] = __uint_as_float(w[j] << 16);
+      f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    } else {
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+      f[2 * j] = x.x;
+      f[2 * j + 1] = x.y;
+    }
+  }
+}
+// Of head h of key heads, chunk c of query row r (token r / G, head r % G of the group).
+__device__ __forceinline__ long long q8_at(const CacheAttnArgs& a, int b, int h, int r, int c) {
+  const int tok = r / a.G;
+  return static_cast<long long>(a.qb * b + a.qh * (static_cast<size_t>(h) * a.G + (r - tok * a.G)) + a.qn * tok +
+                                c * 8);
+}
+
+// The largest magnitude of a row whose CH chunks lie in as many lanes.
+template <int CH>
+__device__ __forceinline__ float row_max(const float (&f)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(f[e]));
+#pragma unroll
+  for (int o = CH / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+// Chunk c of operand row r: f 2^-p as fp16.
+__device__ __forceinline__ void store_q8(uint8_t* tile, int r, int c, const float (&f)[8], int p) {
+  const float inv = pow2i(-p);
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    const __half2 x = __floats2half2_rn(f[2 * j] * inv, f[2 * j + 1] * inv);
+    w[j] = *reinterpret_cast<const uint32_t*>(&x);
+  }
+  *reinterpret_cast<uint4*>(tile + op_off(r, c)) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Query rows r0 .. r0 + n - 1 (n <= 128; those from `rows` on become zero) to
@@ -127,36 +165,22 @@ __device__ __forceinline__ void stage_rows(const CacheAttnArgs& a, int b, int h,
                                            uint8_t* tile, float* factor, int tid) {
   constexpr int CH = D / 8, UN = 4;
   for (int i0 = tid; i0 < n * CH; i0 += NT * UN) {
-    float f[UN][8];
+    long long at[UN];
+    uint4 raw[UN];
 #pragma unroll
     for (int u = 0; u < UN; u++) {
       const int i = i0 + u * NT, r = r0 + i / CH;
-      if (i < n * CH && r < rows) {
-        load_q8(a, a.qb * b + a.qh * (static_cast<size_t>(h) * a.G + r % a.G) + a.qn * (r / a.G) + i % CH * 8,
-                f[u]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; e++) f[u][e] = 0.0f;
-      }
+      at[u] = i < n * CH && r < rows ? q8_at(a, b, h, r, i % CH) : -1;
     }
+    load_q8(a, at, raw);
 #pragma unroll
     for (int u = 0; u < UN; u++) {
       const int i = i0 + u * NT;
       if (i - (tid & 31) >= n * CH) break;  // whole warps
-      float m = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(f[u][e]));
-#pragma unroll
-      for (int o = CH / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const int p = row_power(m);
-      const float inv = pow2i(-p);
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const __half2 x = __floats2half2_rn(f[u][2 * j] * inv, f[u][2 * j + 1] * inv);
-        w[j] = *reinterpret_cast<const uint32_t*>(&x);
-      }
-      *reinterpret_cast<uint4*>(tile + op_off(i / CH, i % CH)) = make_uint4(w[0], w[1], w[2], w[3]);
+      float f[8];
+      q8_floats(a, raw[u], f);
+      const int p = row_power(row_max<CH>(f));
+      store_q8(tile, i / CH, i % CH, f, p);
       if (i % CH == 0) factor[i / CH] = pow2i(p);
     }
   }
@@ -170,6 +194,104 @@ __device__ __forceinline__ int query_len(const CacheAttnArgs& a, int b) {
     return n < 0 ? 0 : a.Nq;
   }
   return n;
+}
+
+// ---------------------------------------------------------------- shares of the work
+//
+// The work of a call is a line of pages: sequences in order, in each the key
+// heads, in each head the pages its rows visit.  Block c of C takes the c-th
+// of C equal stretches of it, so uneven sequences cost no tail and a block's
+// start (its first dependent loads and tile, some 4 us) is paid once, not
+// once for every range of a fixed length.  A stretch cuts at most two heads:
+// the partial result of a head begun by an earlier block goes to slot 2 c,
+// that of one a later block finishes to slot 2 c + 1.
+
+// Pages of sequence b that count (0: nothing to do; at least 1 where rows
+// have to be written).
+template <bool WEIGHTS>
+__device__ __forceinline__ PageRuns seq_runs(const CacheAttnArgs& a, int b, int len, int qn) {
+  PageRuns r;
+  if constexpr (WEIGHTS) {  // every page: those that no row sees get 0
+    r.n = r.ns = (len + kPage - 1) / kPage;
+    r.gap = 0;
+  } else {
+    const long long off = static_cast<long long>(len) - qn;
+    r = page_runs(a.mask, off, off + max(qn - 1, 0), len);
+  }
+  return r;
+}
+template <bool WEIGHTS>
+__device__ __forceinline__ int seq_work(const CacheAttnArgs& a, int b) {
+  const int len = seq_length(a.c, b), qn = query_len(a, b);
+  if (WEIGHTS) return seq_runs<WEIGHTS>(a, b, len, qn).n;
+  return qn == 0 ? 0 : max(1, seq_runs<WEIGHTS>(a, b, len, qn).n);
+}
+
+__device__ __forceinline__ long long share_start(long long work, int c, int n) { return work * c / n; }
+// The block whose stretch holds position x.
+__device__ __forceinline__ int share_of(long long work, long long x, int n) {
+  return static_cast<int>(((x + 1) * n - 1) / work);
+}
+
+struct Place {
+  long long work;    // of the whole call, pages
+  long long before;  // pages of one head before sequence b
+  int b;
+};
+template <int W>
+struct PlaceSmem {
+  long long sum[W];
+  long long before;
+  int b;
+};
+// By a block of W warps: the whole work, and the sequence that position x (a
+// function of the work) lies in.
+template <int W, bool WEIGHTS, typename X>
+__device__ __forceinline__ Place locate(PlaceSmem<W>& s, const CacheAttnArgs& a, X x) {
+  constexpr int NT = W * 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int first = tid < a.c.B ? seq_work<WEIGHTS>(a, tid) : 0;
+  long long mine = first;
+  for (int b = tid + NT; b < a.c.B; b += NT) mine += seq_work<WEIGHTS>(a, b);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) s.sum[warp] = mine;
+  if (tid == 0) s.b = a.c.B;
+  __syncthreads();
+  Place p{0, 0, 0};
+#pragma unroll
+  for (int w = 0; w < W; w++) p.work += s.sum[w];
+  p.work *= a.c.Hkv;
+  const long long at = x(p.work);
+  long long base = 0;  // pages before the sequences from b0 on
+  for (int b0 = 0; b0 < a.c.B; b0 += NT) {
+    const int n = b0 == 0 ? first : b0 + tid < a.c.B ? seq_work<WEIGHTS>(a, b0 + tid) : 0;
+    long long run = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += v;
+    }
+    __syncthreads();
+    if (lane == 31) s.sum[warp] = run;
+    __syncthreads();
+    long long all = 0;
+#pragma unroll
+    for (int w = 0; w < W; w++) {
+      if (w < warp) run += s.sum[w];
+      all += s.sum[w];
+    }
+    if ((base + run - n) * a.c.Hkv <= at && at < (base + run) * a.c.Hkv) {
+      s.b = b0 + tid;
+      s.before = base + run - n;
+    }
+    base += all;
+    if (base * a.c.Hkv > at) break;
+  }
+  __syncthreads();
+  p.b = s.b;
+  p.before = s.before;
+  return p;
 }
 
 }  // namespace sage
