@@ -44,8 +44,13 @@ namespace sage {
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kWarps = 6;
-constexpr int kStages = 2;
+// Warps of a block (two an SM) and half pages on their way to each: a warp that
+// holds 16 rows needs some 200 registers.
+template <int NT>
+struct Shape {
+  static constexpr int kWarps = NT == 1 ? 6 : 4, kStages = NT == 1 ? 2 : 3;
+};
+constexpr int kJoinWarps = 6;
 constexpr int kHalf = 32;      // keys a tile
 constexpr float kBoost = 7.0f;  // y = 2^7 at the reference maximum
 constexpr float kLazy = 8.0f;   // growth of the maximum that moves the reference
@@ -121,8 +126,9 @@ struct TileMeta {
   int unit;  // (page, head)
 };
 
-template <int D>
+template <int D, int NT>
 struct alignas(1024) DecSmem {
+  static constexpr int kWarps = Shape<NT>::kWarps, kStages = Shape<NT>::kStages;
   uint8_t kv[kWarps][kStages][2][kHalf * D];  // TMA tiles: K, V
   int8_t q[3][kDecRows][D];                   // limbs of the query rows, low to high
   float rowf[kDecRows];                       // power of two * scale * log2(e) of each row
@@ -134,10 +140,9 @@ struct alignas(1024) DecSmem {
 };
 
 // The first n query rows (from `rows` on: zero) as limbs.
-template <int D>
-__device__ __forceinline__ void stage_limbs(DecSmem<D>& s, const CacheAttnArgs& a, int b, int h, int rows,
-                                            int n) {
-  constexpr int CH = D / 8;
+template <int D, int NT>
+__device__ __forceinline__ void stage_limbs(DecSmem<D, NT>& s, const CacheAttnArgs& a, int b, int h, int rows) {
+  constexpr int CH = D / 8, n = 8 * NT, kWarps = Shape<NT>::kWarps;
   for (int i = threadIdx.x; i < n * CH; i += kWarps * 32) {
     const int r = i / CH, c = i % CH;
     const long long at[1] = {r < rows ? q8_at(a, b, h, r, c) : -1};
@@ -173,10 +178,10 @@ __device__ __forceinline__ void stage_limbs(DecSmem<D>& s, const CacheAttnArgs& 
 // One head's pages [p0, p1) (of the runs its rows visit): attention, or the
 // weights.  `seen` counts the warp's tiles so far (the ring's phase).
 template <int D, int NT, bool WEIGHTS>
-__device__ __forceinline__ void decode_head(DecSmem<D>& s, const CacheAttnMaps& maps, const CacheAttnArgs& a,
+__device__ __forceinline__ void decode_head(DecSmem<D, NT>& s, const CacheAttnMaps& maps, const CacheAttnArgs& a,
                                             int b, int h, int len, int qn, const PageRuns& runs, int p0,
                                             int p1, int np, int& seen, const WaitCtx& wc) {
-  constexpr int ROWS = 8 * NT;
+  constexpr int ROWS = 8 * NT, kWarps = Shape<NT>::kWarps, kStages = Shape<NT>::kStages;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int rows = qn * a.G;
@@ -218,7 +223,7 @@ __device__ __forceinline__ void decode_head(DecSmem<D>& s, const CacheAttnMaps& 
     issued++;
   };
   while (issued < min(mine, kStages)) issue();
-  stage_limbs<D>(s, a, b, h, rows, ROWS);
+  stage_limbs(s, a, b, h, rows);
   __syncthreads();
   // B fragments of Q^T: channels 32 kk + 4 t .. + 3 and 16 on, of row g.  For
   // 16 rows they stay in shared memory: 48 registers would spill.
@@ -536,11 +541,12 @@ __device__ __forceinline__ void decode_head(DecSmem<D>& s, const CacheAttnMaps& 
 // NT: query rows in eighths (8 NT rows).  WEIGHTS: instead of attending,
 // w[key] (+)= sum over the rows of exp(s - lse), the rows' lse given.
 template <int D, int NT, bool WEIGHTS>
-__global__ void __launch_bounds__(kWarps * 32, 2)
+__global__ void __launch_bounds__(Shape<NT>::kWarps * 32, 2)
     k_cache_decode(const __grid_constant__ CacheAttnMaps maps, const CacheAttnArgs a) {
   extern __shared__ __align__(1024) uint8_t raw[];
   if (smem_misaligned(raw, a.c.status)) return;
-  DecSmem<D>& s = *reinterpret_cast<DecSmem<D>*>(raw);
+  constexpr int kWarps = Shape<NT>::kWarps, kStages = Shape<NT>::kStages;
+  DecSmem<D, NT>& s = *reinterpret_cast<DecSmem<D, NT>*>(raw);
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&maps.k);
     if (!WEIGHTS) tma_prefetch_desc(&maps.v);
@@ -583,14 +589,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   }
 }
 
-// Join of the heads that stretches cut, one block a head: first the factor of
-// every partial result (2^(its maximum - the largest)), a warp a row; then
-// threads (group, row, 4 channels), each group every so many-th partial, the
-// groups summed in order.
+// Join of the heads that stretches cut, a block a head and slice of its
+// channels (gridDim.y slices): first the factor of every partial result (2^(its
+// maximum - the largest)), a warp a row; then threads (group, row, 4 channels),
+// each group every so many-th partial, the groups summed in order.
 template <int D, int ROWS>
-__global__ void __launch_bounds__(kWarps * 32) k_cache_join(const CacheAttnArgs a, int n) {
-  constexpr int NT = kWarps * 32, Q = D / 4;
-  __shared__ long long sum[2][kWarps];
+__global__ void __launch_bounds__(kJoinWarps * 32) k_cache_join(const CacheAttnArgs a, int n) {
+  constexpr int NT = kJoinWarps * 32;
+  const int Q = D / 4 / gridDim.y, d0 = blockIdx.y * (D / gridDim.y);
+  __shared__ long long sum[2][kJoinWarps];
   __shared__ float fac[kMaxShares][ROWS];  // maximum, then factor
   __shared__ float lsum[kMaxShares][ROWS];
   __shared__ float tot[2][ROWS];           // largest maximum, joined sum
@@ -617,7 +624,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_cache_join(const CacheAttnArgs 
   __syncthreads();
   long long before = 0, work = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; w++) {
+  for (int w = 0; w < kJoinWarps; w++) {
     before += sum[0][w];
     work += sum[1][w];
   }
@@ -639,7 +646,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_cache_join(const CacheAttnArgs 
     lsum[p][r] = ml.y;
   }
   __syncthreads();
-  for (int r = warp; r < rows; r += kWarps) {
+  for (int r = warp; r < rows; r += kJoinWarps) {
     float mx = -INFINITY, ls = 0.0f;
     for (int p = lane; p < k; p += 32) mx = fmaxf(mx, fac[p][r]);
 #pragma unroll
@@ -662,7 +669,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_cache_join(const CacheAttnArgs 
   for (int it0 = 0; it0 < items; it0 += NT) {
     const int grp = groups > 1 ? tid / items : 0, it = groups > 1 ? tid % items : it0 + tid;
     const bool live = grp < groups && it < items;
-    const int r = live ? it / Q : 0, d = it % Q * 4;
+    const int r = live ? it / Q : 0, d = d0 + it % Q * 4;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (live) {
 #pragma unroll 8
@@ -701,7 +708,7 @@ namespace {
 template <int D, int NT, bool WEIGHTS>
 cudaError_t prepare_one() {
   return cudaFuncSetAttribute(k_cache_decode<D, NT, WEIGHTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(sizeof(DecSmem<D>)));
+                              static_cast<int>(sizeof(DecSmem<D, NT>)));
 }
 template <int D>
 cudaError_t prepare_d() {
@@ -714,8 +721,8 @@ cudaError_t prepare_d() {
 template <int D, bool WEIGHTS>
 cudaError_t launch_d(const CacheAttnMaps& m, const CacheAttnArgs& a, cudaStream_t s) {
   const bool one = decode_tile_rows(a.Nq, a.G) == 8;
-  if (one) k_cache_decode<D, 1, WEIGHTS><<<a.chunks, kWarps * 32, sizeof(DecSmem<D>), s>>>(m, a);
-  else k_cache_decode<D, 2, WEIGHTS><<<a.chunks, kWarps * 32, sizeof(DecSmem<D>), s>>>(m, a);
+  if (one) k_cache_decode<D, 1, WEIGHTS><<<a.chunks, Shape<1>::kWarps * 32, sizeof(DecSmem<D, 1>), s>>>(m, a);
+  else k_cache_decode<D, 2, WEIGHTS><<<a.chunks, Shape<2>::kWarps * 32, sizeof(DecSmem<D, 2>), s>>>(m, a);
   cudaError_t e = cudaGetLastError();
   if (WEIGHTS || e != cudaSuccess || a.whole) return e;
   // the join starts while the last attention blocks still run and waits for
@@ -724,8 +731,12 @@ cudaError_t launch_d(const CacheAttnMaps& m, const CacheAttnArgs& a, cudaStream_
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.c.B) * a.c.Hkv);
-  cfg.blockDim = dim3(kWarps * 32);
+  const unsigned heads = static_cast<unsigned>(a.c.B) * a.c.Hkv;
+  // few heads, each cut into many stretches: slices of their channels
+  unsigned slices = 1;
+  while (slices < 8 && 2 * slices * heads <= static_cast<unsigned>(a.chunks)) slices *= 2;
+  cfg.gridDim = dim3(heads, slices);
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;

@@ -464,7 +464,7 @@ def cache_attn(q, cache, pages, lengths, mask=None, q_lens=None, max_len=None, s
         os = _out_strides(out)
     if lse is None:
         if return_lse:
-            lse = q.new_empty(q.shape[:3], dtype=torch.float32)
+            lse = cache.k_scale.new_empty(q.shape[:3])
     elif lse.shape != q.shape[:3] or lse.dtype != torch.float32 or lse.device != q.device or \
             not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 tensor [B, H, Nq]")
