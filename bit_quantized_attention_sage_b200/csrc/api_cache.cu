@@ -21,7 +21,7 @@ sage_status status_of(cudaError_t e) { return e == cudaSuccess ? SAGE_OK : SAGE_
 
 bool cache_ok(const sage_kv_cache* c) {
   return c && al(c->k_i8, 16) && al(c->v_f8, 16) && al(c->k_scale, 4) && c->v_exp &&
-         (!c->weight || al(c->weight, 4)) && c->n_pages >= 1 && c->heads >= 1 && c->heads <= 65535 &&
+         (!c->weight || al(c->weight, 16)) && c->n_pages >= 1 && c->heads >= 1 && c->heads <= 65535 &&
          (c->D == 64 || c->D == 128);
 }
 bool seqs_ok(const sage_kv_seqs* s) {
@@ -146,7 +146,8 @@ sage_status attn_common(const sage_kv_cache* c, const sage_kv_seqs* s, const sag
   if (!std::isfinite(q->scale) || q->scale < 0.0f) return SAGE_ERR_INVALID_ARG;
   const sage_status st = mask_of(mask, mask_block, win, sink, &a->mask);
   if (st != SAGE_OK) return st;
-  if (!cache_fits(c)) return SAGE_ERR_UNSUPPORTED;
+  // (the join of a decode call has a block for every head)
+  if (!cache_fits(c) || static_cast<long long>(s->B) * c->heads > (1ll << 31) - 1) return SAGE_ERR_UNSUPPORTED;
   int* status = api_status_word();
   if (!status) return SAGE_ERR_CUDA;
   a->c = view_of(c, s, status);
@@ -340,7 +341,6 @@ SAGE_EXPORT sage_status sage_cache_weights(const sage_kv_cache* cache, const sag
     return status_of(launch_cache_weights(a, static_cast<cudaStream_t>(stream)));
   }
   // up to 16 query rows the keys stream past one mma.sync tile
-  if (units > (1ll << 31) - 1) return SAGE_ERR_UNSUPPORTED;
   plan_decode(units, pages, sms, &a.chunks, &a.whole);
   CacheAttnMaps maps;
   if (!maps_of(cache, &maps)) return SAGE_ERR_CUDA;
@@ -370,6 +370,7 @@ SAGE_EXPORT sage_status sage_cache_evict(const sage_kv_cache* cache, const sage_
     return SAGE_ERR_INVALID_ARG;
   if (!cache_fits(cache) || static_cast<long long>(seqs->B) * cache->heads > (1 << 28))
     return SAGE_ERR_UNSUPPORTED;
+  if (lengths_out == seqs->lengths) return SAGE_ERR_INVALID_ARG;
   int* status = api_status_word();
   if (!status) return SAGE_ERR_CUDA;
   EvictArgs a{};

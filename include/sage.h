@@ -587,7 +587,7 @@ sage_status sage_rope_tables(int N, int R, const void *positions, int positions_
  *   v_exp    int8 [n_pages, heads]
  *   weight   f32  [n_pages, heads, 64]     summed attention weight of each
  *            token (sage_cache_weights, sage_cache_evict), or NULL
- * All device, caller-allocated; codes 16-byte aligned.  D is 64 or 128,
+ * All device, caller-allocated; codes and weights 16-byte aligned.  D is 64 or 128,
  * heads <= 65535, n_pages * heads <= 2^30 (else SAGE_ERR_UNSUPPORTED). */
 typedef struct {
     int8_t *k_i8;
@@ -602,7 +602,8 @@ typedef struct {
  * pages[b * max_pages + t / 64], t < lengths[b].  Both arrays are device
  * int32 and read when the kernels run, so a captured step follows them.
  * Pages may be shared by sequences that only read them; a page that a call
- * writes must belong to one sequence of that call.  Entries past a sequence's
+ * writes must belong to one sequence of that call and stand in it once.
+ * Entries past a sequence's
  * last page are not read.  A page id outside [0, n_pages) or a length outside
  * [0, 64 * max_pages] is recorded in the device status word
  * (SAGE_ERR_INVALID_ARG from sage_sync_status); its tokens count as absent
@@ -661,7 +662,9 @@ typedef struct {
     float scale;
 } sage_kv_query;
 
-/* Workspace of sage_cache_attn on the current device, bytes (0: invalid). */
+/* Workspace of sage_cache_attn on the current device, bytes (0: invalid),
+ * 16-byte aligned.  It holds partial results: calls that may run at the same
+ * time, captured ones among them, need one each. */
 size_t sage_cache_attn_workspace_bytes(int B, int heads, int H, int Nq, int D, int max_len,
                                        int mask, int mask_block, int win, int sink);
 
@@ -679,7 +682,7 @@ size_t sage_cache_attn_workspace_bytes(int B, int heads, int H, int Nq, int D, i
  * gets 0 and lse = -inf.  Q is not quantized; probabilities enter the second
  * product as fp16 relative to the row's largest term, sums are fp32.
  * Errors: SAGE_ERR_INVALID_ARG / SAGE_ERR_UNSUPPORTED (more than 2^31 - 1
- * blocks) before anything is enqueued; SAGE_ERR_CUDA if a launch fails. */
+ * blocks or B * heads) before anything is enqueued; SAGE_ERR_CUDA if a launch fails. */
 sage_status sage_cache_attn(const sage_kv_cache *cache, const sage_kv_seqs *seqs,
                             const sage_kv_query *query, int mask, int mask_block, int win,
                             int sink, void *out, const long long o_strides[3], float *lse,
@@ -697,7 +700,8 @@ sage_status sage_cache_weights(const sage_kv_cache *cache, const sage_kv_seqs *s
                                int sink, const float *lse, int accumulate, void *stream);
 
 /* Workspace of sage_cache_evict, bytes (0: invalid arguments): the survivors'
- * pages and, in place (pages_out = NULL), the result before it is copied. */
+ * pages and, in place (pages_out = NULL), the result before it is copied.
+ * 16-byte aligned, one for each call that may run at the same time. */
 size_t sage_cache_evict_workspace_bytes(int B, int heads, int D, int keep, int in_place);
 
 /* Cut every sequence and head to at most `keep` tokens: the first `sink`, the

@@ -171,3 +171,23 @@ def test_cpu_tensors_are_refused():
         sage.KVCache8(4, 2, 64, device="cpu")
     with pytest.raises(ValueError):
         kvcache._mask(("window", 1, 2))
+
+
+def test_weights_that_vector_loads_cannot_read(L):
+    # the prune reads four weights at a time
+    for f in calls(L):
+        assert f(cache(weight=(1 << 16) + 4), seqs()) == 1
+        assert f(cache(weight=(1 << 16) + 8), seqs()) == 1
+
+
+def test_evict_must_not_write_the_lengths_it_reads(L):
+    s = ctypes.c_void_p(1 << 16)
+    assert L.sage_cache_evict(cache(), seqs(lengths=1 << 16), 64, 0, 0, None, 0, P, s, P, 1 << 40,
+                              None) == 1
+
+
+def test_more_heads_than_blocks(L):
+    # a decode call's join has a block for each of B * heads
+    c = cache(n_pages=1, heads=65535)
+    assert L.sage_cache_attn(c, seqs(B=65535, max_pages=100), query(H=65535, max_len=6400), 0, 0, 0, 0,
+                             P, S3, None, P, 1 << 60, None) == 2
