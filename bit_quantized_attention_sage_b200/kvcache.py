@@ -15,6 +15,7 @@ Every call takes the tensors' device (not the current one) and, without
 stream.
 """
 import ctypes
+import functools
 import math
 
 PAGE = 64          # tokens per page
@@ -23,13 +24,20 @@ _MASKS = "mask must be None, 'causal', ('block_causal', n) or " \
          "('window', frame_len, window_frames, sink_tokens)"
 
 
-_TYPES = {}  # torch dtype -> type code
+torch = None  # the module, once a call has brought a tensor (the package imports without it)
+_TYPES = {}   # torch dtype -> type code
+
+
+def _load():
+    global torch
+    import torch as t
+    torch = t
+    _TYPES.update({t.bfloat16: 0, t.float16: 1, t.float32: 2})
 
 
 def _type(t):
-    if not _TYPES:
-        import torch
-        _TYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    if torch is None:
+        _load()
     return _TYPES.get(t.dtype, -1)
 
 
@@ -97,7 +105,8 @@ def _check(code, what):
 def _here(t, stream):
     """The current stream's handle if the call can run as it is: `t` on the
     current device, no other stream asked for.  None otherwise."""
-    import torch
+    if torch is None:
+        _load()
     dev = t.get_device()
     if dev < 0:
         raise ValueError("tensors must be CUDA tensors")
@@ -111,7 +120,6 @@ class _There:
     what is allocated inside belongs to that stream."""
 
     def __init__(self, t, stream):
-        import torch
         if stream is not None and stream.device != t.device:
             raise ValueError("the stream belongs to %s, the tensors to %s" % (stream.device,
                                                                               t.device))
@@ -129,7 +137,6 @@ class _There:
 
 def _new(t):
     """An uninitialised contiguous tensor like `t`, and its strides."""
-    import torch
     out = torch.empty_like(t) if t.is_contiguous() else \
         torch.empty(t.shape, dtype=t.dtype, device=t.device)
     return out, _strides(out)
@@ -150,7 +157,6 @@ def _out_strides(t):
 
 
 def _int32(t, shape, what, dev):
-    import torch
     if t.dtype is not torch.int32 or t.get_device() != dev or t.shape != shape or \
             not t.is_contiguous():
         raise ValueError("%s must be a contiguous int32 tensor %s on cuda:%d" % (what, shape, dev))
@@ -200,7 +206,6 @@ def rope_freqs(dim, theta=10000.0, scaling=None, device="cuda"):
 
 
 def _positions(positions, N, B, dev):
-    import torch
     if positions.dtype not in (torch.int64, torch.int32) or positions.get_device() != dev or \
             not positions.is_contiguous():
         raise ValueError("positions must be a contiguous int32 or int64 tensor on cuda:%d" % dev)
@@ -211,7 +216,6 @@ def _positions(positions, N, B, dev):
 
 
 def _freqs(inv_freq, dev):
-    import torch
     if inv_freq.dtype is not torch.float64 or inv_freq.get_device() != dev or \
             inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous float64 vector on cuda:%d" % dev)
@@ -258,7 +262,6 @@ def rope(x, positions, inv_freq, layout="interleaved", amplitude=1.0, inverse=Fa
 def rope_tables(positions, inv_freq, amplitude=1.0, stream=None):
     """sage_rope_tables: (cos, sin), f32 [N, R / 2], the tables quant_qk and
     quant_qk_window take (R = D, interleaved pairs)."""
-    import torch
     st = _here(positions, stream)
     if st is None:
         with _There(positions, stream):
@@ -342,7 +345,6 @@ def cache_append(cache, k, v, pages, lengths, n_new=None, k_shift=None, stream=N
     stride) behind the `lengths` tokens that the sequences hold; the caller
     advances lengths.  n_new: int32 [B], tokens of each sequence (None: n).
     k_shift: f32 [heads, D] subtracted from the keys, or None."""
-    import torch
     st = _here(cache.k_i8, stream)
     if st is None:
         with _There(cache.k_i8, stream):
@@ -367,7 +369,6 @@ def cache_append(cache, k, v, pages, lengths, n_new=None, k_shift=None, stream=N
 
 
 def _shift_ok(cache, k_shift):
-    import torch
     if k_shift is not None and (tuple(k_shift.shape) != (cache.kv_heads, cache.head_dim) or
                                 k_shift.dtype != torch.float32 or not k_shift.is_contiguous() or
                                 k_shift.device != cache.device):
@@ -379,7 +380,6 @@ def cache_read(cache, pages, lengths, n, starts=None, k_shift=None, weights=Fals
     """sage_cache_read: (k, v), f32 [B, heads, n, D], of n tokens of each
     sequence from token starts[b] (int32 [B]; None: 0) on, zero where there is
     none; with `weights` also their summed weights, f32 [B, heads, n]."""
-    import torch
     st = _here(cache.k_i8, stream)
     if st is None:
         with _There(cache.k_i8, stream):
@@ -427,6 +427,12 @@ def _query(q, cache, sq, q_lens, max_len, scale):
                   D ** -0.5 if scale is None else scale)
 
 
+@functools.lru_cache(maxsize=256)
+def _attn_workspace(dev, *shape):
+    """sage_cache_attn_workspace_bytes of the current device, which is dev."""
+    return _L.sage_cache_attn_workspace_bytes(*shape)
+
+
 def cache_attn_workspace_bytes(cache, B, H, Nq, max_len, mask=None):
     """sage_cache_attn_workspace_bytes on the cache's device."""
     with _There(cache.k_i8, None):
@@ -447,7 +453,6 @@ def cache_attn(q, cache, pages, lengths, mask=None, q_lens=None, max_len=None, s
     sequence (None: Nq); other rows of out are left as they are.  max_len: a
     bound on the lengths known to the host (None: what the page table holds);
     it only chooses how the work is cut.  scale: None is 1 / sqrt(D)."""
-    import torch
     st = _here(cache.k_i8, stream)
     if st is None:
         with _There(cache.k_i8, stream):
@@ -472,8 +477,8 @@ def cache_attn(q, cache, pages, lengths, mask=None, q_lens=None, max_len=None, s
         return (out, lse) if return_lse else out
     L = _lib()
     if workspace is None:
-        n = L.sage_cache_attn_workspace_bytes(sq.B, cache.kv_heads, qs.H, qs.Nq, cache.head_dim,
-                                              qs.max_len, *m)
+        n = _attn_workspace(cache.index, sq.B, cache.kv_heads, qs.H, qs.Nq, cache.head_dim,
+                            qs.max_len, *m)
         if n > 16:  # else: one range a query tile, no partial results
             workspace = q.new_empty((n,), dtype=torch.uint8)
     elif workspace.device != q.device or not workspace.is_contiguous():
@@ -492,7 +497,6 @@ def cache_weights(q, cache, lse, pages, lengths, mask=None, q_lens=None, max_len
     the rows of q, from cache_attn's lse of the same arguments, added to (or,
     accumulate=False, written over) cache.weight -- or `weight`, a float32
     tensor [pages, heads, 64].  Returns that tensor."""
-    import torch
     st = _here(cache.k_i8, stream)
     if st is None:
         with _There(cache.k_i8, stream):
@@ -524,7 +528,6 @@ def cache_evict(cache, pages, lengths, keep, sink=0, recent=0, pages_out=None, w
     survivors' old places in order, then -1; int32 [B].  pages_out: int32 [B,
     >= ceil(keep / 64)], pages the survivors go to (none of them in `pages`);
     None: the sequences' own first pages."""
-    import torch
     st = _here(cache.k_i8, stream)
     if st is None:
         with _There(cache.k_i8, stream):
