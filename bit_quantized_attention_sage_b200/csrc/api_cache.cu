@@ -76,19 +76,30 @@ int visited_pages(const CacheMask& m, int max_len, int tile_tokens) {
   return static_cast<int>(std::min(pages, (m.sink + kPage - 1ll) / kPage + win / kPage + 3));
 }
 // Blocks that share `pages` pages of every head: two an SM, with eight pages
-// (four tiles a warp) each at least; a block a head where a head has no more.
-void plan_decode(long long units, int pages, int sms, int* chunks, int* whole) {
-  *whole = pages <= 8;
-  *chunks = static_cast<int>(*whole ? units : std::min(std::min<long long>(2ll * sms, kMaxShares), (units * pages + 7) / 8));
+// (four tiles a warp) each at least.  Or, `whole`, a block a head: no look-up
+// of its place and no join, but the heads of the last round walk their pages
+// alone, 0.32 us each.  Whole against shared, us, at 4 x 128 query heads:
+//   8 heads     1000 tokens 18 : 20   2000 23 : 20   4000  33 :  26
+//   128 heads   1000 tokens 21 : 28   4000 41 : 48
+//   512 heads   1000 tokens 46 : 50   4000 106 : 118 (of uneven lengths 83 : 89)
+// and past 64 pages one long sequence among short ones would cost more than
+// there is to gain.  (The weights have no join to save: 128 heads of 8000
+// tokens 39 us whole, 34 shared; equal at 1000.)
+void plan_decode(long long units, int pages, int sms, bool join, int* chunks, int* whole) {
+  const long long slots = std::min<long long>(2ll * sms, kMaxShares);
+  *whole = pages <= 8 || (join && (pages <= 24 || (pages <= 64 && units % slots >= slots / 3)));
+  *chunks = static_cast<int>(*whole ? units : std::min(slots, (units * pages + 7) / 8));
 }
 
 Plan plan_of(const CacheMask& m, int B, int Hkv, int G, int Nq, int D, int max_len, int sms) {
   Plan p{};
   const long long qrows = static_cast<long long>(Nq) * G;
+  // (16 rows of 16 x 8 heads of 8000 tokens: 122 us against 156 on tcgen05's
+  // 256-row tiles, 73 against 115 with 64 channels)
   p.prefill = qrows > kDecRows;
   if (!p.prefill) {
     const long long units = static_cast<long long>(B) * Hkv;
-    plan_decode(units, visited_pages(m, max_len, Nq), sms, &p.chunks, &p.whole);
+    plan_decode(units, visited_pages(m, max_len, Nq), sms, true, &p.chunks, &p.whole);
     p.blocks = p.chunks;
     p.rows = p.whole ? 0 : 2ull * p.chunks * decode_tile_rows(Nq, G);
   } else {
@@ -96,7 +107,9 @@ Plan plan_of(const CacheMask& m, int B, int Hkv, int G, int Nq, int D, int max_l
     const long long units = static_cast<long long>(B) * Hkv * row_tiles;
     const int pages = visited_pages(m, max_len, (kPreRows + G - 1) / G + 1);
     // one block an SM: the fewest ranges whose last round of blocks leaves at
-    // most a tenth of the SMs' time unused, of 16 pages at least
+    // most a tenth of the SMs' time unused, of 16 pages at least (24 heads, 2040
+    // rows on 26520 tokens: three ranges 798 us, one 1032; 8 heads, 256 rows: 67
+    // against 526)
     long long cp = std::max(4, pages);
     double best = 0.0;
     for (long long n = 1; n <= 64 && (n == 1 || pages / n >= 16); n++) {
@@ -335,13 +348,15 @@ SAGE_EXPORT sage_status sage_cache_weights(const sage_kv_cache* cache, const sag
   if (!sms) return SAGE_ERR_CUDA;
   const int pages = std::max(1, (query->max_len + kPage - 1) / kPage);
   const long long units = static_cast<long long>(seqs->B) * cache->heads;
-  if (static_cast<long long>(a.Nq) * a.G > kDecRows) {
+  // Up to eight query rows the keys stream past one mma.sync tile, up to 16
+  // with 64 channels (16 rows of 16 x 8 heads of 8000 tokens: 41 us against 47;
+  // with 128 channels 76 against 59).
+  if (static_cast<long long>(a.Nq) * a.G > (cache->D == 64 ? kDecRows : kDecRows / 2)) {
     // a block an SM, with eight pages each at least
     a.chunks = static_cast<int>(std::min<long long>(sms, (units * pages + 7) / 8));
     return status_of(launch_cache_weights(a, static_cast<cudaStream_t>(stream)));
   }
-  // up to 16 query rows the keys stream past one mma.sync tile
-  plan_decode(units, pages, sms, &a.chunks, &a.whole);
+  plan_decode(units, pages, sms, false, &a.chunks, &a.whole);
   CacheAttnMaps maps;
   if (!maps_of(cache, &maps)) return SAGE_ERR_CUDA;
   return status_of(launch_cache_weights_few(maps, a, static_cast<cudaStream_t>(stream)));

@@ -557,35 +557,54 @@ __global__ void __launch_bounds__(Shape<NT>::kWarps * 32, 2)
   }
   const int c = blockIdx.x, n = gridDim.x;
   const WaitCtx wc{a.budget, a.c.status, &s.abort};
-  int seen = 0;
+  // One loop for both ways of cutting, so that there is one copy of what it
+  // does: a call's first microseconds are instructions that come from L2.
+  int seen = 0, b, h = -1;  // h < 0: from the position x
+  long long x, end, before = 0;
   if (a.whole) {
     __syncthreads();
-    const int b = c / a.c.Hkv, len = seq_length(a.c, b), qn = query_len(a, b);
-    const PageRuns runs = seq_runs<WEIGHTS>(a, b, len, qn);
-    const int np = seq_work<WEIGHTS>(a, b);
-    if (np > 0) decode_head<D, NT, WEIGHTS>(s, maps, a, b, c % a.c.Hkv, len, qn, runs, 0, np, np, seen, wc);
-    return;
+    b = c / a.c.Hkv;
+    h = c - b * a.c.Hkv;
+    x = 0;
+    end = seq_work<WEIGHTS>(a, b);
+  } else {
+    // (locate's barriers also publish the ring's)
+    const Place pl = locate<kWarps, WEIGHTS>(s.place, a, [&](long long w) { return share_start(w, c, n); });
+    if (!WEIGHTS) cudaTriggerProgrammaticLaunchCompletion();
+    x = share_start(pl.work, c, n);
+    end = share_start(pl.work, c + 1, n);
+    before = pl.before;
+    b = pl.b;
   }
-  // (locate's barriers also publish the ring's)
-  const Place pl = locate<kWarps, WEIGHTS>(s.place, a, [&](long long w) { return share_start(w, c, n); });
-  if (!WEIGHTS) cudaTriggerProgrammaticLaunchCompletion();
-  long long x = share_start(pl.work, c, n);
-  const long long end = share_start(pl.work, c + 1, n);
-  long long before = pl.before;
-  for (int b = pl.b; x < end && b < a.c.B; b++) {
-    const int np = seq_work<WEIGHTS>(a, b);
-    if (np == 0) continue;
-    const int len = seq_length(a.c, b), qn = query_len(a, b);
-    const PageRuns runs = seq_runs<WEIGHTS>(a, b, len, qn);
-    for (long long rel = x - before * a.c.Hkv; x < end && rel < static_cast<long long>(np) * a.c.Hkv;) {
-      const int h = static_cast<int>(rel / np), p0 = static_cast<int>(rel - static_cast<long long>(h) * np);
-      const int p1 = static_cast<int>(min(static_cast<long long>(np), p0 + (end - x)));
-      decode_head<D, NT, WEIGHTS>(s, maps, a, b, h, len, qn, runs, p0, p1, np, seen, wc);
-      if (s.abort) return;
-      x += p1 - p0;
-      rel += p1 - p0;
+  int np = 0, len = 0, qn = 0, p0 = 0;
+  PageRuns runs{0, 0, 0};
+  bool fresh = true;
+  while (x < end && b < a.c.B) {
+    if (fresh) {  // the first head of this block in sequence b
+      fresh = false;
+      np = seq_work<WEIGHTS>(a, b);
+      len = seq_length(a.c, b);
+      qn = query_len(a, b);
+      runs = seq_runs<WEIGHTS>(a, b, len, qn);
+      if (h < 0 && np > 0) {
+        const long long rel = x - before * a.c.Hkv;
+        h = static_cast<int>(rel / np);
+        p0 = static_cast<int>(rel - static_cast<long long>(h) * np);
+      }
     }
-    before += np;
+    if (np == 0 || h == a.c.Hkv) {
+      before += np;
+      b++;
+      h = -1;
+      fresh = true;
+      continue;
+    }
+    const int p1 = static_cast<int>(min(static_cast<long long>(np), p0 + (end - x)));
+    decode_head<D, NT, WEIGHTS>(s, maps, a, b, h, len, qn, runs, p0, p1, np, seen, wc);
+    if (s.abort) return;
+    x += p1 - p0;
+    p0 = 0;
+    h++;
   }
 }
 

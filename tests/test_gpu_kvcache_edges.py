@@ -76,6 +76,32 @@ def test_many_sequences(n):
         check_weights(c, q, lse, tab, lengths, q_lens, "causal", kv.weight)
 
 
+@pytest.mark.parametrize("n", [1, 3])
+def test_many_sequences_in_shares(n):
+    # a page table wide enough that blocks share the pages of all heads
+    B, G, D = 700, 4, 64
+    rng = np.random.default_rng(n)
+    lengths = rng.integers(0, 150, B) * (rng.random(B) > 0.33)
+    lengths[0], lengths[1:200], lengths[-1] = 0, 0, 0
+    lengths[350] = 5000
+    lengths = lengths.tolist()
+    q_lens = rng.integers(0, n + 1, B)
+    q_lens[350] = n
+    q_lens = q_lens.tolist()
+    kv, tab, _ = filled(lengths, 1, D, n, weight=True)
+    tab = np.pad(tab, ((0, 0), (0, 20)), constant_values=-7)
+    c = ref.Cache(kv)
+    q = randn((B, G, n, D), n)
+    out = torch.full_like(q, 3.0)
+    lse = torch.full(q.shape[:3], 3.0, device="cuda")
+    sage.cache_attn(q, kv, dev(tab), dev(lengths), "causal", q_lens=dev(q_lens), out=out, lse=lse)
+    sage.cache_weights(q, kv, lse, dev(tab), dev(lengths), "causal", q_lens=dev(q_lens),
+                       accumulate=False)
+    ok()
+    check_attn(c, q, out, lse, tab, lengths, q_lens, "causal", D ** -0.5, untouched=3.0)
+    check_weights(c, q, lse, tab, lengths, q_lens, "causal", kv.weight)
+
+
 @pytest.mark.parametrize("G,n", [(1, 1), (8, 1), (16, 1), (5, 3), (8, 4)])
 @pytest.mark.parametrize("D", [64, 128])
 def test_one_head_in_many_shares(D, G, n):
