@@ -21,6 +21,15 @@
 // e4m3 product would need it (and P) in two limbs or more, the same tensor
 // time without the exactness.  256 rows a block halve the conversions per
 // row, which then fit the issue slots that the softmax leaves.
+//
+// Measured: 24 heads, 2040 rows on 26520 tokens, 128 channels, 830-857 us, 780
+// to 810 TFLOP/s.  A KV tile takes some 4200 clocks: of each row tile's chain,
+// softmax 2550 (the two tiles' overlap for a third of it), the slowest of its
+// four warps 390 more, O += P V and the next S 820, and 250 until the S is
+// seen; the products alone, issued back to back, take 2048.  Tried and slower
+// or no faster: two S buffers of 64 keys a row tile (905 us: another exchange
+// for every 64 keys), the two row tiles' softmax in turns (925), a share of
+// the exponentials on the fma pipes (equal), single-lane issue (851).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

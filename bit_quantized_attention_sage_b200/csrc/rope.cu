@@ -9,7 +9,11 @@
 // What bounds it: x read and y written once (HBM for a clip, the launch for a
 // token).  Angles need 64 bits (n * f in fp32 is off by whole radians at far
 // positions), so a block computes each cos/sin once, in shared memory, and
-// uses it for all its heads: the fp64 work is 1/heads of an element's.
+// uses it for all its heads: the fp64 work is 1/heads of an element's.  Four
+// heads' loads are on their way at once (one after another 55 us).
+// Measured: a clip of 12 heads x 32760 tokens x 128 channels, half of them
+// turned, 36 us, 5.6 TB/s (copy 6.5); a token of 16 x 32 heads 5.5 us, most of
+// it the launch and the angles' latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
