@@ -612,76 +612,88 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_prefill(const CacheAttnAr
   }
 }
 
-// Join of the KV ranges, a warp a row, the ranges in order.  A lane holds the
-// factor of one range; the partial rows come eight at a time.
+// Join of the KV ranges, the ranges in order; a block joins 16 rows of one
+// tile (what they share, the tile's pages and ranges, is worked out once), a
+// warp a row at a time.  A lane holds the factor of one range; the partial
+// rows come four at a time, on their way before the factors are known.
+// Measured: 24 heads x 2040 rows of three ranges 27 us, 76 MB, most of it under
+// the attention's tail (a warp a row that worked out everything for itself 45).
+constexpr int kMergeRows = 16;
 template <int D>
-__global__ void __launch_bounds__(128) k_cache_merge(const CacheAttnArgs a, int row_tiles, int tile_rows) {
-  cudaGridDependencySynchronize();  // launched under the attention kernel's tail
+__global__ void __launch_bounds__(128) k_cache_merge(const CacheAttnArgs a, int row_tiles) {
+  constexpr uint32_t kFull = 0xffffffffu;
+  constexpr int PER = D / 32;
+  static_assert(kPreRows % kMergeRows == 0, "rows of one tile");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long row = static_cast<long long>(blockIdx.x) * 4 + warp;
-  const long long per = static_cast<long long>(row_tiles) * tile_rows;
-  const long long bh = row / per;
-  if (bh >= static_cast<long long>(a.c.B) * a.c.Hkv) return;
-  const int r = static_cast<int>(row - bh * per), b = static_cast<int>(bh / a.c.Hkv),
-            h = static_cast<int>(bh % a.c.Hkv);
+  const int blocks = row_tiles * (kPreRows / kMergeRows);  // of a (sequence, key head)
+  const int bh = static_cast<int>(blockIdx.x) / blocks, first = (static_cast<int>(blockIdx.x) - bh * blocks) * kMergeRows;
+  const int b = bh / a.c.Hkv, h = bh - b * a.c.Hkv;
   const int len = seq_length(a.c, b), qn = query_len(a, b), rows = qn * a.G;
-  if (r >= rows) return;
-  const int r0 = r / tile_rows * tile_rows, r1 = min(rows, r0 + tile_rows);
+  if (first >= rows) return;
+  const int r0 = first / kPreRows * kPreRows, r1 = min(rows, r0 + kPreRows);
   const long long off = static_cast<long long>(len) - qn;
   const PageRuns runs = page_runs(a.mask, off + r0 / a.G, off + (r1 - 1) / a.G, len);
   const int nch = min(a.chunks, (runs.n + a.chunk_pages - 1) / a.chunk_pages);
   if (nch <= 1) return;  // the attention kernel wrote this tile itself
-  constexpr int PER = D / 32;
-  float o[PER], ls = 0.0f, mx = -INFINITY;
-#pragma unroll
-  for (int e = 0; e < PER; e++) o[e] = 0.0f;
-  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row * a.chunks;
-  for (int i = lane; i < nch; i += 32) mx = fmaxf(mx, ml[i].x);
-#pragma unroll
-  for (int x = 16; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-  const float* po = a.part_o + row * a.chunks * D + lane * PER;
-  for (int i0 = 0; i0 < nch; i0 += 32) {
-    float al = 0.0f;
-    const int mine = i0 + lane;
-    if (mine < nch) {
-      const float2 x = ml[mine];
-      al = x.x == -INFINITY ? 0.0f : ex2_approx(x.x - mx);
-      ls = fmaf(al, x.y, ls);
+  cudaGridDependencySynchronize();  // launched under the attention kernel's tail
+  auto load = [&](const float* p, float (&v)[PER]) {
+    if constexpr (PER == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(p);
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(p);
+      v[0] = x.x, v[1] = x.y;
     }
-    const int n = min(32, nch - i0);
+  };
+  for (int r = first + warp; r < min(r1, first + kMergeRows); r += 4) {
+    const size_t row = static_cast<size_t>(bh) * row_tiles * kPreRows + r;
+    const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row * a.chunks;
+    const float* po = a.part_o + row * a.chunks * D + lane * PER;
+    float v[4][PER];
+#pragma unroll
+    for (int k = 0; k < 4; k++) load(po + static_cast<size_t>(min(k, nch - 1)) * D, v[k]);
+    float o[PER], ls = 0.0f, mx = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < PER; e++) o[e] = 0.0f;
+    for (int i = lane; i < nch; i += 32) mx = fmaxf(mx, ml[i].x);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, x));
+    for (int i0 = 0; i0 < nch; i0 += 32) {
+      float al = 0.0f;
+      const int mine = i0 + lane;
+      if (mine < nch) {
+        const float2 x = ml[mine];
+        al = x.x == -INFINITY ? 0.0f : ex2_approx(x.x - mx);
+        ls = fmaf(al, x.y, ls);
+      }
+      const int n = min(32, nch - i0);
 #pragma unroll 1
-    for (int k0 = 0; k0 < n; k0 += 8) {
-      float v[8][PER];
+      for (int k0 = 0; k0 < n; k0 += 4) {
+        if (i0 + k0 > 0) {
 #pragma unroll
-      for (int k = 0; k < 8; k++) {
-        const int i = min(i0 + k0 + k, nch - 1);
+          for (int k = 0; k < 4; k++) load(po + static_cast<size_t>(min(i0 + k0 + k, nch - 1)) * D, v[k]);
+        }
 #pragma unroll
-        for (int e = 0; e < PER; e += 2) {
-          const float2 x = *reinterpret_cast<const float2*>(po + static_cast<size_t>(i) * D + e);
-          v[k][e] = x.x;
-          v[k][e + 1] = x.y;
+        for (int k = 0; k < 4; k++) {
+          const float x = __shfl_sync(kFull, al, (k0 + k) & 31);
+          // ranges past the end: their factor is 0, the row read in their
+          // place finite
+#pragma unroll
+          for (int e = 0; e < PER; e++) o[e] = fmaf(k0 + k < n ? x : 0.0f, v[k][e], o[e]);
         }
       }
-#pragma unroll
-      for (int k = 0; k < 8; k++) {
-        const float x = __shfl_sync(0xffffffffu, al, (k0 + k) & 31);
-        // ranges past the end: their factor is 0, the row read in their
-        // place finite
-#pragma unroll
-        for (int e = 0; e < PER; e++) o[e] = fmaf(k0 + k < n ? x : 0.0f, v[k][e], o[e]);
-      }
     }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) ls += __shfl_xor_sync(kFull, ls, x);
+    const float inv = ls > 0.0f ? 1.0f / ls : 0.0f;
+    const int tok = r / a.G, head = h * a.G + (r - tok * a.G);
+    const size_t ob = a.ob * b + a.oh * head + a.on * tok + lane * PER;
+#pragma unroll
+    for (int e = 0; e < PER; e += 2) store_o2(a, ob + e, o[e] * inv, o[e + 1] * inv);
+    if (lane == 0 && a.lse)
+      a.lse[(static_cast<size_t>(b) * a.H + head) * a.Nq + tok] =
+          ls > 0.0f ? (mx + log2f(ls)) * 0.69314718055994531f : -INFINITY;
   }
-#pragma unroll
-  for (int x = 16; x; x >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
-  const float inv = ls > 0.0f ? 1.0f / ls : 0.0f;
-  const int tok = r / a.G, head = h * a.G + r % a.G;
-  const size_t ob = a.ob * b + a.oh * head + a.on * tok + lane * PER;
-#pragma unroll
-  for (int e = 0; e < PER; e += 2) store_o2(a, ob + e, o[e] * inv, o[e + 1] * inv);
-  if (lane == 0 && a.lse)
-    a.lse[(static_cast<size_t>(b) * a.H + head) * a.Nq + tok] =
-        ls > 0.0f ? (mx + log2f(ls)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace
@@ -709,13 +721,13 @@ cudaError_t launch_cache_prefill(const CacheAttnArgs& a, cudaStream_t s) {
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(units * kPreRows / 4));
+  cfg.gridDim = dim3(static_cast<unsigned>(units * (kPreRows / kMergeRows)));
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return a.c.D == 128 ? cudaLaunchKernelEx(&cfg, k_cache_merge<128>, a, row_tiles, kPreRows)
-                      : cudaLaunchKernelEx(&cfg, k_cache_merge<64>, a, row_tiles, kPreRows);
+  return a.c.D == 128 ? cudaLaunchKernelEx(&cfg, k_cache_merge<128>, a, row_tiles)
+                      : cudaLaunchKernelEx(&cfg, k_cache_merge<64>, a, row_tiles);
 }
 
 }  // namespace sage
