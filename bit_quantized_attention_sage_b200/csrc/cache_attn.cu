@@ -630,8 +630,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_cache_join(const CacheAttnA
   __shared__ float4 sh_o[NT];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv;
+  // Launched under the attention kernel's tail.  Every block waits for that,
+  // also one with nothing to join: what comes next in the stream waits for
+  // this kernel only, so it must not end before the attention has.
   const int np = seq_work<false>(a, b);
-  if (np == 0) return;
+  if (np == 0) {
+    cudaGridDependencySynchronize();
+    return;
+  }
   long long sb = 0, sw = 0;  // pages of one head before b, and in all
   for (int i = tid; i < a.c.B; i += NT) {
     const int v = seq_work<false>(a, i);
@@ -657,9 +663,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_cache_join(const CacheAttnA
   work *= a.c.Hkv;
   const long long x0 = before * a.c.Hkv + static_cast<long long>(h) * np;
   const int c0 = share_of(work, x0, n), c1 = share_of(work, x0 + np - 1, n);
+  cudaGridDependencySynchronize();
   if (c0 == c1) return;  // one block had the whole head and wrote it
   const int qn = query_len(a, b), rows = qn * a.G, k = c1 - c0 + 1;
-  cudaGridDependencySynchronize();  // launched under the attention kernel's tail
   // the first partial of the head lies in slot 2 c + 1, the others in 2 c
   auto slot = [&](int i) { return (2 * static_cast<size_t>(c0 + i) + (i == 0)) * ROWS; };
   for (int i = tid; i < k * ROWS; i += NT) {

@@ -629,13 +629,18 @@ __global__ void __launch_bounds__(128) k_cache_merge(const CacheAttnArgs a, int 
   const int bh = static_cast<int>(blockIdx.x) / blocks, first = (static_cast<int>(blockIdx.x) - bh * blocks) * kMergeRows;
   const int b = bh / a.c.Hkv, h = bh - b * a.c.Hkv;
   const int len = seq_length(a.c, b), qn = query_len(a, b), rows = qn * a.G;
-  if (first >= rows) return;
   const int r0 = first / kPreRows * kPreRows, r1 = min(rows, r0 + kPreRows);
-  const long long off = static_cast<long long>(len) - qn;
-  const PageRuns runs = page_runs(a.mask, off + r0 / a.G, off + (r1 - 1) / a.G, len);
-  const int nch = min(a.chunks, (runs.n + a.chunk_pages - 1) / a.chunk_pages);
+  int nch = 0;
+  if (first < rows) {
+    const long long off = static_cast<long long>(len) - qn;
+    const PageRuns runs = page_runs(a.mask, off + r0 / a.G, off + (r1 - 1) / a.G, len);
+    nch = min(a.chunks, (runs.n + a.chunk_pages - 1) / a.chunk_pages);
+  }
+  // Launched under the attention kernel's tail.  Every block waits, also one
+  // with nothing to join: what comes next in the stream waits for this kernel
+  // only, so it must not end before the attention has.
+  cudaGridDependencySynchronize();
   if (nch <= 1) return;  // the attention kernel wrote this tile itself
-  cudaGridDependencySynchronize();  // launched under the attention kernel's tail
   auto load = [&](const float* p, float (&v)[PER]) {
     if constexpr (PER == 4) {
       const float4 x = *reinterpret_cast<const float4*>(p);

@@ -305,3 +305,20 @@ def test_refusals_of_the_wrappers():
         sage.cache_attn(q, big, dev([list(range(64))]), dev([4000]),
                         workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))
     ok()
+
+
+@pytest.mark.parametrize("n,B,length", [(1, 37, 4700), (1, 1, 9000), (40, 3, 2000)])
+def test_what_follows_sees_the_whole_result(n, B, length):
+    # heads that no block cuts leave the join nothing to do; the copy behind
+    # the call still waits for the attention
+    kv, tab, _ = filled([length] * B, 8, 128, 3)
+    t, ln, q = dev(tab), dev([length] * B), randn((B, 8, n, 128), 5)
+    want = sage.cache_attn(q, kv, t, ln, "causal")
+    torch.cuda.synchronize()
+    out = torch.empty_like(q)
+    for _ in range(50):
+        out.zero_()
+        sage.cache_attn(q, kv, t, ln, "causal", out=out)
+        got = out.clone()
+        assert torch.equal(got, want)
+    ok()
