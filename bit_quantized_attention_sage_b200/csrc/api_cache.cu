@@ -87,7 +87,7 @@ int visited_pages(const CacheMask& m, int max_len, int tile_tokens) {
 // tokens 39 us whole, 34 shared; equal at 1000.)
 void plan_decode(long long units, int pages, int sms, bool join, int* chunks, int* whole) {
   const long long slots = std::min<long long>(2ll * sms, kMaxShares);
-  *whole = pages <= 8 || (join && (pages <= 24 || (pages <= 64 && units % slots >= slots / 3)));
+  *whole = pages <= 8 || (join && (pages <= 24 || (pages <= 64 && (units - 1) % slots + 1 >= slots / 3)));
   *chunks = static_cast<int>(*whole ? units : std::min(slots, (units * pages + 7) / 8));
 }
 

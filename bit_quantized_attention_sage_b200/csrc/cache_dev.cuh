@@ -250,6 +250,26 @@ template <int W, bool WEIGHTS, typename X>
 __device__ __forceinline__ Place locate(PlaceSmem<W>& s, const CacheAttnArgs& a, X x) {
   constexpr int NT = W * 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // Every warp by itself, one barrier instead of five (weights of 2 x 32 tokens
+  // 41.0 -> 40.0 us, of 16 tokens 27.5 -> 26.8, attention of 32 113.4 -> 112.9).
+  if (a.c.B <= 32) {
+    const int n = lane < a.c.B ? seq_work<WEIGHTS>(a, lane) : 0;
+    int run = n;  // (at most 2^24 pages a sequence)
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += v;
+    }
+    Place p;
+    p.work = static_cast<long long>(__shfl_sync(0xffffffffu, run, 31)) * a.c.Hkv;
+    const long long at = x(p.work);
+    const uint32_t here = __ballot_sync(0xffffffffu, static_cast<long long>(run - n) * a.c.Hkv <= at &&
+                                                         at < static_cast<long long>(run) * a.c.Hkv);
+    p.b = here ? __ffs(here) - 1 : a.c.B;
+    p.before = __shfl_sync(0xffffffffu, run - n, p.b & 31);
+    __syncthreads();
+    return p;
+  }
   const int first = tid < a.c.B ? seq_work<WEIGHTS>(a, tid) : 0;
   long long mine = first;
   for (int b = tid + NT; b < a.c.B; b += NT) mine += seq_work<WEIGHTS>(a, b);

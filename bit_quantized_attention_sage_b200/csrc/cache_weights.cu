@@ -19,8 +19,8 @@
 //   21      copies pages, whole, into a ring of raw tiles
 // so copies, conversions and products run under the sums.
 //
-// 41 us for two sequences of 32000 and 20988 keys, 8 heads, 32 tokens of 4
-// query heads each: 342 TFLOP/s, 1.4 TB/s.  A tile takes some 1650 clocks; exp2
+// 40 us for two sequences of 32000 and 20988 keys, 8 heads, 32 tokens of 4
+// query heads each: 350 TFLOP/s, 1.4 TB/s.  A tile takes some 1650 clocks; exp2
 // (16 a clock and SM) is 1024 of them, and the sums' broadcasts, the codes'
 // conversion and the products' operands share the rest of the shared memory's
 // time.  A block's start and the first rows take 9 us.  Every warp doing copies,
