@@ -352,23 +352,24 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // index among equal ones.  The smallest weight that stays is found by radix
 // selection: three passes over 11, 11 and 10 bits (the first digit then splits
 // an octave in four, so a heavy tail spreads over many bins).  Each of the four
-// blocks takes a quarter of the sequence; then a quarter of the bins, summed
-// over the blocks' shared memories; a lone block took 45 us for 26520 tokens
-// and left most SMs idle.  One sweep in index order then writes the survivors, every warp
+// blocks takes a quarter of the sequence, then all of the bins, summed over the
+// blocks' shared memories; a lone block took 45 us for 26520 tokens and left
+// most SMs idle.  One sweep in index order then writes the survivors, every warp
 // its own run of tokens.  The weights are read from memory once and kept in
 // shared memory where they fit (65536 tokens); longer sequences read them
 // again (L2) in every pass.  Measured: 8 x 8 heads of 16000 tokens 20 us, 24
-// heads of 26520 22 us: the latency of the three passes' exchanges and of the
-// two sweeps, not the 4 MB of weights.
+// heads of 26520 21 us: the latency of the three passes and of the two sweeps,
+// not the 4 MB of weights.  (With each block taking a quarter of the bins, three
+// exchanges a pass instead of one, 21 and 22.)
 __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThreads) k_select(const EvictArgs a) {
   namespace cg = cooperative_groups;
   extern __shared__ uint32_t sel[];
   constexpr int W = kSelThreads / 32;
-  static_assert(kSelThreads * kSelCluster == kSelBins, "a bin of the cluster's histogram for every thread");
-  uint32_t* hist = sel;             // [kSelBins]
-  uint32_t* keys = sel + kSelBins;  // [a.sel_keys], of this block's tokens
+  static_assert(kSelThreads * 4 == kSelBins, "four bins of the histogram for every thread");
+  uint32_t* hist = sel;                 // [3][kSelBins], one for each pass
+  uint32_t* keys = sel + 3 * kSelBins;  // [a.sel_keys], of this block's tokens
   int* unit = reinterpret_cast<int*>(keys + a.sel_keys);  // [a.sel_keys / 64]: (page, head) of its pages, or -1
-  __shared__ uint32_t sh_prefix, sh_need, sh_sum[W], quarter;
+  __shared__ uint32_t sh_prefix, sh_need, sh_sum[W];
   __shared__ int n_above[W], n_tie[W], total[2];
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank());
@@ -422,22 +423,29 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
   uint32_t prefix = 0, left = static_cast<uint32_t>(need);
   if (need > 0) {
     const int c0 = max(t0, lo), c1 = min(t1, hi);
+    for (int i = tid; i < 3 * kSelBins; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
 #pragma unroll 1
     for (int pass = 0; pass < 3; pass++) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
       const uint32_t mask = (1u << bits) - 1u;
-      for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
+      uint32_t* bins = hist + pass * kSelBins;
       for (int i = c0 + tid; i < c1; i += kSelThreads) {
         const uint32_t k = key(i);
-        if (pass == 0 || (k >> (shift + bits)) == prefix) atomicAdd(&hist[(k >> shift) & mask], 1u);
+        if (pass == 0 || (k >> (shift + bits)) == prefix) atomicAdd(&bins[(k >> shift) & mask], 1u);
       }
       cluster.sync();
-      // this thread's bin, from the top, of the whole cluster
-      const int bin = kSelBins - 1 - all_tid;
-      uint32_t cnt = 0;
+      // this thread's four bins, from the top, of the whole cluster: every
+      // block finds the threshold by itself, so this is the pass's only
+      // exchange
+      const int quad = kSelBins / 4 - 1 - tid;
+      uint4 c4 = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-      for (int r = 0; r < kSelCluster; r++) cnt += cluster.map_shared_rank(hist, r)[bin];
+      for (int r = 0; r < kSelCluster; r++) {
+        const uint4 o = reinterpret_cast<const uint4*>(cluster.map_shared_rank(bins, r))[quad];
+        c4 = make_uint4(c4.x + o.x, c4.y + o.y, c4.z + o.z, c4.w + o.w);
+      }
+      const uint32_t cnt = c4.x + c4.y + c4.z + c4.w;
       uint32_t run = cnt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -446,27 +454,19 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
       }
       if (lane == 31) sh_sum[warp] = run;
       __syncthreads();
-      uint32_t below = lane < W ? sh_sum[lane] : 0u, mine = lane < warp ? below : 0u;
+      uint32_t mine = lane < warp ? sh_sum[lane & (W - 1)] : 0u;
 #pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        below += __shfl_xor_sync(kFull, below, o);
-        mine += __shfl_xor_sync(kFull, mine, o);
-      }
-      if (tid == 0) quarter = below;
-      cluster.sync();
+      for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(kFull, mine, o);
       uint32_t before = run - cnt + mine;
-#pragma unroll
-      for (int r = 0; r < kSelCluster; r++)
-        if (r < rank) before += *cluster.map_shared_rank(&quarter, r);
-      // the bin in which the count from the top reaches `left`, to all blocks
+      // the bin in which the count from the top reaches `left`
       if (before < left && before + cnt >= left) {
-#pragma unroll
-        for (int r = 0; r < kSelCluster; r++) {
-          *cluster.map_shared_rank(&sh_prefix, r) = (prefix << bits) | static_cast<uint32_t>(bin);
-          *cluster.map_shared_rank(&sh_need, r) = left - before;
-        }
+        const uint32_t down[4] = {c4.w, c4.z, c4.y, c4.x};
+        int e = 0;
+        while (before + down[e] < left) before += down[e++];
+        sh_prefix = (prefix << bits) | static_cast<uint32_t>(4 * quad + 3 - e);
+        sh_need = left - before;
       }
-      cluster.sync();
+      __syncthreads();
       prefix = sh_prefix;
       left = sh_need;
     }
@@ -801,7 +801,7 @@ size_t cache_evict_ws_bytes(int B, int Hkv, int D, int keep, bool in_place) {
 
 cudaError_t cache_evict_prepare() {
   return cudaFuncSetAttribute(k_select, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (kSelBins + kSelKeys + kSelKeys / kPage) * 4);
+                              (3 * kSelBins + kSelKeys + kSelKeys / kPage) * 4);
 }
 
 cudaError_t launch_cache_evict(const EvictArgs& args, cudaStream_t s) {
@@ -811,7 +811,7 @@ cudaError_t launch_cache_evict(const EvictArgs& args, cudaStream_t s) {
   a.sel_keys = static_cast<int>(share < kSelKeys ? share : kSelKeys);
   a.from = static_cast<int*>(args.ws);
   a.ws = static_cast<char*>(args.ws) + cache_evict_list_bytes(a.c.B, a.c.Hkv, a.keep);
-  k_select<<<a.c.B * a.c.Hkv * kSelCluster, kSelThreads, (kSelBins + a.sel_keys + a.sel_keys / kPage) * 4, s>>>(a);
+  k_select<<<a.c.B * a.c.Hkv * kSelCluster, kSelThreads, (3 * kSelBins + a.sel_keys + a.sel_keys / kPage) * 4, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const dim3 grid((a.keep + kPage - 1) / kPage, a.c.Hkv, a.c.B);
