@@ -1,6 +1,7 @@
 // cache_attn.cu -- attention over the paged 8-bit cache for few query rows
-// (single tokens, grouped heads), the merge of KV ranges, and, in the same
-// stream of keys, the attention weight that each cached key received.
+// (single tokens, grouped heads), the join of heads that several blocks shared,
+// and, in the same stream of keys, the attention weight that each cached key
+// received.
 //
 // The query heads that share a key head are rows of one tile: row r of
 // (sequence b, key head h) is token r / G, head h G + r % G.
@@ -747,14 +748,20 @@ cudaError_t prepare_d() {
   cudaError_t e = prepare_one<D, 1, false>();
   if (e == cudaSuccess) e = prepare_one<D, 2, false>();
   if (e == cudaSuccess) e = prepare_one<D, 1, true>();
-  if (e == cudaSuccess) e = prepare_one<D, 2, true>();
+  if constexpr (D == 64) {  // (weights of more than 8 rows at D = 128: cache_weights.cu)
+    if (e == cudaSuccess) e = prepare_one<D, 2, true>();
+  }
   return e;
 }
 template <int D, bool WEIGHTS>
 cudaError_t launch_d(const CacheAttnMaps& m, const CacheAttnArgs& a, cudaStream_t s) {
   const bool one = decode_tile_rows(a.Nq, a.G) == 8;
-  if (one) k_cache_decode<D, 1, WEIGHTS><<<a.chunks, Shape<1>::kWarps * 32, sizeof(DecSmem<D, 1>), s>>>(m, a);
-  else k_cache_decode<D, 2, WEIGHTS><<<a.chunks, Shape<2>::kWarps * 32, sizeof(DecSmem<D, 2>), s>>>(m, a);
+  if constexpr (WEIGHTS && D == 128) {
+    k_cache_decode<D, 1, true><<<a.chunks, Shape<1>::kWarps * 32, sizeof(DecSmem<D, 1>), s>>>(m, a);
+  } else {
+    if (one) k_cache_decode<D, 1, WEIGHTS><<<a.chunks, Shape<1>::kWarps * 32, sizeof(DecSmem<D, 1>), s>>>(m, a);
+    else k_cache_decode<D, 2, WEIGHTS><<<a.chunks, Shape<2>::kWarps * 32, sizeof(DecSmem<D, 2>), s>>>(m, a);
+  }
   cudaError_t e = cudaGetLastError();
   if (WEIGHTS || e != cudaSuccess || a.whole) return e;
   // the join starts while the last attention blocks still run and waits for
