@@ -158,11 +158,11 @@ __device__ __forceinline__ void stage_limbs(DecSmem<D, NT>& s, const CacheAttnAr
     load_q8(a, at, raw);
     float f[8];
     q8_floats(a, raw[0], f);
-    float m = 0.0f;
+    const float m = row_max<CH>(f);
+    bool finite = true;
 #pragma unroll
-    for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(f[e]));
-#pragma unroll
-    for (int o = CH / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    for (int e = 0; e < 8; e++) finite = finite && fabsf(f[e]) <= FLT_MAX;
+    const uint32_t bad = __ballot_sync(kFull, !finite) >> (threadIdx.x & 31 & ~(CH - 1)) & ((1u << CH) - 1u);
     const int p = max(row_power(m) - 7, -126);  // m 2^-p in [2^21, 2^22)
     const float inv = pow2i(-p);
     uint32_t w[3][2] = {{0u, 0u}, {0u, 0u}, {0u, 0u}};
@@ -179,7 +179,8 @@ __device__ __forceinline__ void stage_limbs(DecSmem<D, NT>& s, const CacheAttnAr
 #pragma unroll
     for (int x = 0; x < 3; x++)
       *reinterpret_cast<uint2*>(&s.q[x][r][c * 8]) = make_uint2(w[x][0], w[x][1]);
-    if (c == 0) s.rowf[r] = pow2i(p) * (a.scale * kLog2e);
+    // (a row with a NaN or an infinity: its scores become NaN)
+    if (c == 0) s.rowf[r] = bad ? __int_as_float(0x7FFFFFFF) : pow2i(p) * (a.scale * kLog2e);
   }
 }
 
@@ -250,23 +251,29 @@ __device__ __forceinline__ void decode_head(DecSmem<D, NT>& s, const CacheAttnMa
   float f[NT][2];
   KeyRange kr[NT][2];
   float nl[NT][2];  // WEIGHTS: -lse log2(e); -inf: weight 0
+  bool bad[NT][2], any_bad = false;  // what the row sees is NaN
 #pragma unroll
   for (int n = 0; n < NT; n++) {
 #pragma unroll
     for (int e = 0; e < 2; e++) {  // rows that this lane's columns are
       const int r = n * 8 + t * 2 + e;
       f[n][e] = s.rowf[n * 8 + t * 2 + e];
+      bad[n][e] = f[n][e] != f[n][e];
       kr[n][e] = KeyRange{0, 0, 0};
       nl[n][e] = -INFINITY;
       if (r < rows) {
         kr[n][e] = key_range(a.mask, off + r / a.G, len);
         if (WEIGHTS) {
           const float v = __ldg(a.lse_in + (static_cast<size_t>(b) * a.H + h * a.G + r % a.G) * a.Nq + r / a.G);
-          if (v != -INFINITY) nl[n][e] = -v * kLog2e;
+          if (v != v) bad[n][e] = true;
+          else if (v != -INFINITY) nl[n][e] = -v * kLog2e;
         }
       }
+      if (bad[n][e]) f[n][e] = 0.0f;
+      any_bad = any_bad || bad[n][e];
     }
   }
+  any_bad = __any_sync(kFull, any_bad);
   // keys [full_lo, full_hi) and those below full_sink are seen by every row
   // that is there: tiles inside need no mask.  Rows that are not there see
   // whatever those do and are never stored.
@@ -352,6 +359,15 @@ __device__ __forceinline__ void decode_head(DecSmem<D, NT>& s, const CacheAttnMa
                                       static_cast<float>(low[mt][n][e]));
               }
         }
+      }
+      if (any_bad) {
+#pragma unroll
+        for (int mt = 0; mt < 2; mt++)
+#pragma unroll
+          for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+              if (bad[n][e & 1]) sc[mt][n][e] = __int_as_float(0x7FFFFFFF);
       }
       if (!(j0 + kHalf <= full_sink || (j0 >= full_lo && j0 + kHalf <= full_hi))) {
 #pragma unroll
@@ -522,7 +538,8 @@ __device__ __forceinline__ void decode_head(DecSmem<D, NT>& s, const CacheAttnMa
 #pragma unroll
     for (int w = 0; w < kWarps; w++) {
       const float mw = s.ml[w][r][0];
-      const float al = mw == -INFINITY ? 0.0f : ex2_approx(mw - mx);
+      // (no maximum: nothing seen, sum 0, or NaN alone, sum NaN)
+      const float al = mw == -INFINITY ? 0.0f * s.ml[w][r][1] : ex2_approx(mw - mx);
       const float2 v = *reinterpret_cast<const float2*>(
           reinterpret_cast<const float*>(s.kv[0][0][0]) + w * kWarpFloats + r * D + d);
       ox = fmaf(al, v.x, ox);
@@ -533,12 +550,12 @@ __device__ __forceinline__ void decode_head(DecSmem<D, NT>& s, const CacheAttnMa
       *reinterpret_cast<float2*>(a.part_o + (slot + r) * D + d) = make_float2(ox, oy);
       if (d == 0) *reinterpret_cast<float2*>(a.part_ml + (slot + r) * 2) = make_float2(mx - kBoost, ls);
     } else {
-      const float inv = ls > 0.0f ? 1.0f / ls : 0.0f;
+      const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
       const int tok = r / a.G, head = h * a.G + r % a.G;
       store_o2(a, a.ob * b + a.oh * head + a.on * tok + d, ox * inv, oy * inv);
       if (d == 0 && a.lse)
         a.lse[(static_cast<size_t>(b) * a.H + head) * a.Nq + tok] =
-            ls > 0.0f ? (mx - kBoost + log2f(ls)) * kLn2 : -INFINITY;
+            ls == 0.0f ? -INFINITY : ls > 0.0f ? (mx - kBoost + log2f(ls)) * kLn2 : ls;
     }
   }
   // the ring held the partial rows: order them before the next head's loads
@@ -685,7 +702,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_cache_join(const CacheAttnA
 #pragma unroll
     for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
     for (int p = lane; p < k; p += 32) {
-      const float al = fac[p][r] == -INFINITY ? 0.0f : ex2_approx(fac[p][r] - mx);
+      const float al = fac[p][r] == -INFINITY ? 0.0f * lsum[p][r] : ex2_approx(fac[p][r] - mx);
       fac[p][r] = al;
       ls = fmaf(al, lsum[p][r], ls);
     }
@@ -724,14 +741,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_cache_join(const CacheAttnA
       }
     }
     if (!live || grp != 0) continue;
-    const float ls = tot[1][r], inv = ls > 0.0f ? 1.0f / ls : 0.0f;
+    const float ls = tot[1][r], inv = ls == 0.0f ? 0.0f : 1.0f / ls;
     const int tok = r / a.G, head = h * a.G + r % a.G;
     const size_t ob = a.ob * b + a.oh * head + a.on * tok + d;
     store_o2(a, ob, o.x * inv, o.y * inv);
     store_o2(a, ob + 2, o.z * inv, o.w * inv);
     if (d == 0 && a.lse)
       a.lse[(static_cast<size_t>(b) * a.H + head) * a.Nq + tok] =
-          ls > 0.0f ? (tot[0][r] + log2f(ls)) * kLn2 : -INFINITY;
+          ls == 0.0f ? -INFINITY : ls > 0.0f ? (tot[0][r] + log2f(ls)) * kLn2 : ls;
   }
 }
 

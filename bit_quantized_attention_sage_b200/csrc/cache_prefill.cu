@@ -476,7 +476,7 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
   const bool part = nch > 1;
   const size_t urow = (static_cast<size_t>(b) * a.c.Hkv + h) * (static_cast<size_t>(row_tiles) * (2 * BM)) + row;
   const size_t pr = urow * a.chunks + chunk;
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const int tok = row / a.G, head = h * a.G + row % a.G;
   const size_t ob = a.ob * b + a.oh * static_cast<size_t>(head) + a.on * static_cast<size_t>(tok);
   const bool vec = ((reinterpret_cast<uintptr_t>(a.o) | (a.ob * 2) | (a.oh * 2) | (a.on * 2)) & 15) == 0;
@@ -528,7 +528,7 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
     *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m - kBoost, l);
   } else if (a.lse) {
     a.lse[(static_cast<size_t>(b) * a.H + head) * a.Nq + tok] =
-        l > 0.0f ? (m - kBoost + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        l == 0.0f ? -INFINITY : l > 0.0f ? (m - kBoost + log2f(l)) * 0.69314718055994531f : l;
   }
 }
 
@@ -668,7 +668,8 @@ __global__ void __launch_bounds__(128) k_cache_merge(const CacheAttnArgs a, int 
       const int mine = i0 + lane;
       if (mine < nch) {
         const float2 x = ml[mine];
-        al = x.x == -INFINITY ? 0.0f : ex2_approx(x.x - mx);
+        // (no maximum: nothing seen, sum 0, or NaN alone, sum NaN)
+        al = x.x == -INFINITY ? 0.0f * x.y : ex2_approx(x.x - mx);
         ls = fmaf(al, x.y, ls);
       }
       const int n = min(32, nch - i0);
@@ -690,14 +691,14 @@ __global__ void __launch_bounds__(128) k_cache_merge(const CacheAttnArgs a, int 
     }
 #pragma unroll
     for (int x = 16; x; x >>= 1) ls += __shfl_xor_sync(kFull, ls, x);
-    const float inv = ls > 0.0f ? 1.0f / ls : 0.0f;
+    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
     const int tok = r / a.G, head = h * a.G + (r - tok * a.G);
     const size_t ob = a.ob * b + a.oh * head + a.on * tok + lane * PER;
 #pragma unroll
     for (int e = 0; e < PER; e += 2) store_o2(a, ob + e, o[e] * inv, o[e + 1] * inv);
     if (lane == 0 && a.lse)
       a.lse[(static_cast<size_t>(b) * a.H + head) * a.Nq + tok] =
-          ls > 0.0f ? (mx + log2f(ls)) * 0.69314718055994531f : -INFINITY;
+          ls == 0.0f ? -INFINITY : ls > 0.0f ? (mx + log2f(ls)) * 0.69314718055994531f : ls;
   }
 }
 

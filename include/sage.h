@@ -679,7 +679,8 @@ size_t sage_cache_attn_workspace_bytes(int B, int heads, int H, int Nq, int D, i
  *   lse       f32 [B, H, Nq] contiguous, natural log, or NULL.  With a
  *             shifted cache it is that of the shifted scores.
  * A row that sees no key (an empty sequence; more query rows than tokens)
- * gets 0 and lse = -inf.  Q is not quantized; probabilities enter the second
+ * gets 0 and lse = -inf.  A NaN in a row makes that row NaN and no other.  Q is
+ * not quantized; probabilities enter the second
  * product as fp16 relative to the row's largest term, sums are fp32.
  * Errors: SAGE_ERR_INVALID_ARG / SAGE_ERR_UNSUPPORTED (more than 2^31 - 1
  * blocks or B * heads) before anything is enqueued; SAGE_ERR_CUDA if a launch fails. */

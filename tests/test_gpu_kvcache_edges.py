@@ -322,3 +322,35 @@ def test_what_follows_sees_the_whole_result(n, B, length):
         got = out.clone()
         assert torch.equal(got, want)
     ok()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [3, 7, 20])  # 6 and 14 rows, 40
+@pytest.mark.parametrize("length", [100, 9000])
+def test_a_row_that_is_not_finite_stays_alone(D, n, length):
+    G, bad = 2, 1
+    kv, tab, _ = filled([length], 2, D, n, weight=True)
+    t, ln = dev(tab), dev([length])
+    q = randn((1, 2 * G, n, D), n)
+    want, wl = sage.cache_attn(q, kv, t, ln, "causal", return_lse=True)
+    ww = sage.cache_weights(q, kv, wl, t, ln, "causal", accumulate=False).clone()
+    for value in (float("nan"), float("inf")):
+        p = q.clone()
+        p[0, 1, bad, 5] = value
+        o, lse = sage.cache_attn(p, kv, t, ln, "causal", return_lse=True)
+        w = sage.cache_weights(p, kv, lse, t, ln, "causal", accumulate=False)
+        ok()
+        rest = torch.ones(o.shape[:3], dtype=torch.bool, device="cuda")
+        rest[0, 1, bad] = False
+        assert torch.equal(o[rest], want[rest]) and torch.equal(lse[rest], wl[rest])
+        if value != value:
+            assert torch.isnan(o[0, 1, bad]).all() and torch.isnan(lse[0, 1, bad])
+        # the other key head, and the keys behind the row
+        at = np.arange(length - n + bad + 1, length)
+        pg, slot = torch.from_numpy(tab[0][at // 64]).long(), torch.from_numpy(at % 64)
+        assert torch.equal(w[pg, 0, slot], ww[pg, 0, slot])
+        every = torch.from_numpy(tab[0]).long()
+        full = every[:length // 64]
+        assert torch.equal(w[full, 1], ww[full, 1])
+        if value != value:
+            assert torch.isnan(w[full, 0]).all()
