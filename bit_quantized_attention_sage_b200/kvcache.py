@@ -120,6 +120,8 @@ class _There:
     what is allocated inside belongs to that stream."""
 
     def __init__(self, t, stream):
+        if torch is None:
+            _load()
         if stream is not None and stream.device != t.device:
             raise ValueError("the stream belongs to %s, the tensors to %s" % (stream.device,
                                                                               t.device))

@@ -354,3 +354,20 @@ def test_a_row_that_is_not_finite_stays_alone(D, n, length):
         assert torch.equal(w[full, 1], ww[full, 1])
         if value != value:
             assert torch.isnan(w[full, 0]).all()
+
+
+def test_any_call_may_be_the_first(monkeypatch):
+    from bit_quantized_attention_sage_b200 import kvcache
+    kv = sage.KVCache8(64, 2, 64)
+    q = randn((1, 4, 1, 64), 1)
+    t, ln, f = dev([list(range(64))]), dev([0]), torch.ones(32, dtype=torch.float64, device="cuda")
+    for call in (lambda: sage.cache_attn_workspace_bytes(kv, 1, 4, 1, 4096, "causal"),
+                 lambda: sage.cache_attn(q, kv, t, ln),
+                 lambda: sage.cache_append(kv, q[:, :2], q[:, :2], t, ln),
+                 lambda: sage.cache_read(kv, t, ln, 1),
+                 lambda: sage.rope(q, dev([3]), f),
+                 lambda: sage.rope_tables(dev([3]), f)):
+        monkeypatch.setattr(kvcache, "torch", None)
+        kvcache._TYPES.clear()
+        call()
+    ok()
