@@ -475,7 +475,7 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
   const int seg = ((t1 - t0 + W - 1) / W + 31) / 32 * 32;
   const int s0 = min(t1, t0 + warp * seg), s1 = min(t1, s0 + seg);
   // 2: stays, 1: equal to the threshold, 0: goes
-  auto judge = [&](int i) -> int {
+  auto fate = [&](int i) -> int {
     if (i < lo || i >= hi) return 2;
     if (need <= 0) return 0;
     const uint32_t k = key(i);
@@ -484,7 +484,7 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
   int above = 0, tie = 0;
 #pragma unroll 4
   for (int i = s0 + lane; i < s1; i += 32) {
-    const int j = judge(i);
+    const int j = fate(i);
     above += j == 2;
     tie += j == 1;
   }
@@ -523,7 +523,7 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
   cluster.sync();  // no block leaves while another reads its totals
   at += min(ties, static_cast<int>(left));  // of the ties before, the first `left` stay
   for (int i = s0 + lane; i - lane < s1; i += 32) {
-    const int j = i < s1 ? judge(i) : 0;
+    const int j = i < s1 ? fate(i) : 0;
     const uint32_t lower = (1u << lane) - 1u;
     const uint32_t mt = __ballot_sync(kFull, j == 1);
     const bool stay = j == 2 || (j == 1 && ties + __popc(mt & lower) < static_cast<int>(left));
