@@ -369,8 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_weights(const CacheAttnAr
             s.meta[t % kMeta].ks[lane - at] = ks;
           }
           const uint32_t has = __ballot_sync(kFull, mine && unit >= 0);
+          __syncwarp();  // both pages' data before the arrival that publishes it
           if (lane == at) mbar_arrive_expect_tx(&s.r_full[st], __popc(has) * (kPage * D));
-          __syncwarp();
+          __syncwarp();  // the copies' bytes are expected before the copies
           if (mine && unit >= 0)
             copy_page(s.raw[st] + (lane - at) * (kPage * D), a.c.k_i8 + static_cast<size_t>(unit) * (kPage * D),
                       kPage * D, &s.r_full[st]);
