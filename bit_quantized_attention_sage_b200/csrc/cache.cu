@@ -363,9 +363,10 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // exchanges a pass instead of one, 21 and 22.)
 __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThreads) k_select(const EvictArgs a) {
   namespace cg = cooperative_groups;
-  extern __shared__ uint32_t sel[];
+  extern __shared__ __align__(16) uint32_t sel[];  // read as uint4: bins, keys
   constexpr int W = kSelThreads / 32;
   static_assert(kSelThreads * 4 == kSelBins, "four bins of the histogram for every thread");
+  static_assert(kSelBins % 4 == 0 && kPage % 4 == 0, "bins and keys start on 16 bytes");
   uint32_t* hist = sel;                 // [3][kSelBins], one for each pass
   uint32_t* keys = sel + 3 * kSelBins;  // [a.sel_keys], of this block's tokens
   int* unit = reinterpret_cast<int*>(keys + a.sel_keys);  // [a.sel_keys / 64]: (page, head) of its pages, or -1
