@@ -19,8 +19,9 @@
 // running one in steps of at least 2^8: y <= 2^15, and fp16(y) is off by at
 // most 2^-11 of each weight down to 2^-21 of the largest term, where fp16's
 // subnormal range begins.  The sum L takes y 2^-e in fp32 before that
-// rounding.  e4m3 value codes are exact in fp16.  O = (sum y code) / L; the
-// value scales need no multiplication.
+// rounding, or, on pages far below the largest e, a power that is still a
+// number (cache_dev.cuh).  e4m3 value codes are exact in fp16.
+// O = (sum y code) / L; the value scales need no multiplication.
 //
 // What bounds it: the codes, read once (2 D bytes a key and head).  Every
 // warp walks half pages of its own (32 keys) through a private ring of two
@@ -298,6 +299,7 @@ __device__ __forceinline__ void decode_head(DecSmem<D, NT>& s, const CacheAttnMa
     }
 
   bool ok = true;
+  int top_exp = kMinVExp;  // the largest value exponent so far
   for (int i = 0; i < mine; i++) {
     const int st = (seen + i) % kStages;
     ok = __all_sync(kFull, mbar_wait(&s.full[warp][st], ((seen + i) / kStages) & 1, wc, kSiteDecPage));
@@ -429,9 +431,9 @@ __device__ __forceinline__ void decode_head(DecSmem<D, NT>& s, const CacheAttnMa
 #pragma unroll
             for (int e = 0; e < 2; e++) {
               const float mn = fmaxf(m[n][e], pm[n][e]);
-              const float al = m[n][e] == mn ? 1.0f : ex2_approx(m[n][e] - mn);  // 0 from -inf
+              const float down = m[n][e] == mn ? 0.0f : m[n][e] - mn, al = ex2_approx(down);  // 0 from -inf
               m[n][e] = mn;
-              l[n][e] *= al;
+              l[n][e] = add_scaled(0.0f, l[n][e], down, al);
 #pragma unroll
               for (int d = 0; d < D / 16; d++) {
                 o[d][n][e] *= al;
@@ -439,7 +441,9 @@ __device__ __forceinline__ void decode_head(DecSmem<D, NT>& s, const CacheAttnMa
               }
             }
         }
-        const float un = pow2i(min(-md.ve, 127));
+        top_exp = max(top_exp, md.ve);
+        const int fe = sum_exp(md.ve, top_exp);
+        const float un = sum_unit(fe);
         uint32_t pb[2][NT][2];  // B fragments of P^T, 16 keys each
 #pragma unroll
         for (int n = 0; n < NT; n++) {
@@ -457,6 +461,16 @@ __device__ __forceinline__ void decode_head(DecSmem<D, NT>& s, const CacheAttnMa
               const __half2 y = __floats2half2_rn(y0, y1);
               pb[mt][n][k] = transpose8(*reinterpret_cast<const uint32_t*>(&y));
             }
+          if (fe != md.ve) {
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+              const float nf = m[n][e] == -INFINITY ? 0.0f : kBoost + static_cast<float>(fe) - m[n][e];
+              rs[e] = 0.0f;
+#pragma unroll
+              for (int k = 0; k < 4; k++)
+                rs[e] += ex2_approx(fmaf(sc[k >> 1][n][(k & 1) * 2 + e], c[n][e], nf));
+            }
+          }
           l[n][0] = fmaf(rs[0], un, l[n][0]);
           l[n][1] = fmaf(rs[1], un, l[n][1]);
         }
@@ -539,12 +553,13 @@ __device__ __forceinline__ void decode_head(DecSmem<D, NT>& s, const CacheAttnMa
     for (int w = 0; w < kWarps; w++) {
       const float mw = s.ml[w][r][0];
       // (no maximum: nothing seen, sum 0, or NaN alone, sum NaN)
-      const float al = mw == -INFINITY ? 0.0f * s.ml[w][r][1] : ex2_approx(mw - mx);
+      const bool none = mw == -INFINITY;
+      const float al = none ? 0.0f * s.ml[w][r][1] : ex2_approx(mw - mx);
       const float2 v = *reinterpret_cast<const float2*>(
           reinterpret_cast<const float*>(s.kv[0][0][0]) + w * kWarpFloats + r * D + d);
       ox = fmaf(al, v.x, ox);
       oy = fmaf(al, v.y, oy);
-      ls = fmaf(al, s.ml[w][r][1], ls);
+      ls = add_scaled(ls, s.ml[w][r][1], none ? 0.0f : mw - mx, al);
     }
     if (p1 - p0 < np) {
       *reinterpret_cast<float2*>(a.part_o + (slot + r) * D + d) = make_float2(ox, oy);
@@ -702,9 +717,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_cache_join(const CacheAttnA
 #pragma unroll
     for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
     for (int p = lane; p < k; p += 32) {
-      const float al = fac[p][r] == -INFINITY ? 0.0f * lsum[p][r] : ex2_approx(fac[p][r] - mx);
+      const float down = fac[p][r] == -INFINITY ? 0.0f : fac[p][r] - mx;
+      const float al = fac[p][r] == -INFINITY ? 0.0f * lsum[p][r] : ex2_approx(down);
       fac[p][r] = al;
-      ls = fmaf(al, lsum[p][r], ls);
+      ls = add_scaled(ls, lsum[p][r], down, al);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) ls += __shfl_xor_sync(kFull, ls, o);

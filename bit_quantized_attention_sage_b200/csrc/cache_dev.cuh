@@ -186,6 +186,28 @@ __device__ __forceinline__ void stage_rows(const CacheAttnArgs& a, int b, int h,
   }
 }
 
+// ---------------------------------------------------------------- sums of weights
+//
+// y = 2^(t + e - M + 7) of a key with score t on a page of value exponent e; a
+// row's sum adds y 2^-e.  Exponents lie up to 160 apart, so y may be below every
+// fp32 number (2^-126) where y 2^-e is what the sum consists of.  Pages kFar
+// or more below E, the largest exponent so far, therefore take
+// 2^(t + f - M + 7) 2^-f for the sum, f = E - kFar.  Nothing is lost then: with
+// M = t' + e' of a key that was seen, e' <= E, that power is 2^(t - t' - 53) at
+// least, and as t + e <= M + 8 it is 2^(15 + 160 - kFar) at most.  (The product
+// with the values keeps y: against 2^(t' + e') it is nothing.)
+constexpr int kFar = 60;
+__device__ __forceinline__ int sum_exp(int e, int top) { return max(e, top - kFar); }
+__device__ __forceinline__ float sum_unit(int f) { return pow2i(min(-f, 127)); }
+
+// s + x 2^d, d <= 0, al = 2^d (0 below 2^-126): a sum x of pages far below the
+// new reference is scaled in two steps.
+__device__ __forceinline__ float add_scaled(float s, float x, float d, float al) {
+  if (d >= -100.0f) return fmaf(al, x, s);
+  const float h = ex2_approx(0.5f * d);
+  return s + x * h * h;
+}
+
 __device__ __forceinline__ int query_len(const CacheAttnArgs& a, int b) {
   if (!a.q_lens) return a.Nq;
   const int n = __ldg(a.q_lens + b);

@@ -344,6 +344,7 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
   KeyRange kr{0, 0, 0x7FFFFFFF};
   if (valid) kr = key_range(a.mask, off + row / a.G, len);
   float m = -INFINITY, l = 0.0f;
+  int top_exp = kMinVExp;  // the largest value exponent so far
   bool ok = true;
   for (int it = 0; it < nk; it++) {
     ok = __all_sync(kFull, mbar_wait(&s.s_full[t], it & 1, w, kSitePreS));
@@ -353,6 +354,8 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
     // a zero scale must not meet -inf as 0 * inf
     const float c[2] = {fmaxf(f * md.ks[0], FLT_MIN), fmaxf(f * md.ks[1], FLT_MIN)};
     const float ve[2] = {static_cast<float>(md.ve[0]), static_cast<float>(md.ve[1])};
+    top_exp = max(top_exp, max(md.ve[0], md.ve[1]));
+    const int fe[2] = {sum_exp(md.ve[0], top_exp), sum_exp(md.ve[1], top_exp)};
     uint32_t sv[128];
     tmem_ld128(tS, sv);
 #pragma unroll
@@ -396,9 +399,10 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
     }
     const float top = fmaxf(fmaf(fmaxf(mx[0][0], mx[0][1]), c[0], ve[0]),
                             fmaf(fmaxf(mx[1][0], mx[1][1]), c[1], ve[1]));
-    if (__any_sync(kFull, top > m + kLazy)) {
+    // (a page far below the largest exponent takes its sum there, too)
+    if (__any_sync(kFull, top > m + kLazy) || fe[0] != md.ve[0]) {
       const float mn = fmaxf(m, top);
-      const float al = mn == m ? 1.0f : ex2_approx(m - mn);  // 0 from -inf
+      const float down = mn == m ? 0.0f : m - mn, al = ex2_approx(down);  // 0 from -inf
       // O holds the sum of the tiles before: its last product completed
       // before s_full did
       if (it > 0) {
@@ -411,9 +415,10 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
           tmem_st32(tO + d, o);
         }
       }
-      l *= al;
+      l = add_scaled(0.0f, l, down, al);
       m = mn;
       const float nm = (m == -INFINITY ? 0.0f : kBoost - m) + ve[0];
+      const float nf = (m == -INFINITY ? 0.0f : kBoost - m) + static_cast<float>(fe[0]);
       sum = 0.0f;
       // S is still in TMEM; P of 32 keys takes the columns of the 16 before
 #pragma unroll 1
@@ -425,7 +430,8 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
           const int j = md.j0[0] + k + e;
           const bool see = md.j0[0] >= 0 && (j < kr.sink || (j >= kr.lo && j < kr.hi));
           const float v = see ? ex2_approx(fmaf(__uint_as_float(x[e]), c[0], nm)) : 0.0f;
-          sum += v;
+          if (fe[0] == md.ve[0]) sum += v;
+          else sum += see ? ex2_approx(fmaf(__uint_as_float(x[e]), c[0], nf)) : 0.0f;
           x[e] = __float_as_uint(v);
         }
 #pragma unroll
@@ -441,12 +447,18 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
       for (int j = 0; j < 32; j++) pk[j] = sv[j];
       tmem_st32(tS, pk);
     }
-    l = fmaf(sum, pow2i(min(-md.ve[0], 127)), l);
+    l = fmaf(sum, sum_unit(fe[0]), l);
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.p_full[t][0]);
     {
       const float base = m == -INFINITY ? 0.0f : kBoost - m;
+      float far_sum = 0.0f;
+      if (fe[1] != md.ve[1]) {
+        const float nf = base + static_cast<float>(fe[1]);
+#pragma unroll
+        for (int j = 0; j < kPage; j++) far_sum += ex2_approx(fmaf(__uint_as_float(sv[64 + j]), c[1], nf));
+      }
       float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
       const float2 cc = make_float2(c[1], c[1]), nn = make_float2(base + ve[1], base + ve[1]);
       uint32_t pk[32];
@@ -464,7 +476,7 @@ __device__ __forceinline__ void softmax(PreSmem<D>& s, const CacheAttnArgs& a, u
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.p_full[t][1]);
       const float2 a2 = __fadd2_rn(acc[0], acc[1]);
-      l = fmaf(a2.x + a2.y, pow2i(min(-md.ve[1], 127)), l);
+      l = fmaf(fe[1] == md.ve[1] ? a2.x + a2.y : far_sum, sum_unit(fe[1]), l);
     }
   }
   if (!ok) return;
@@ -669,8 +681,9 @@ __global__ void __launch_bounds__(128) k_cache_merge(const CacheAttnArgs a, int 
       if (mine < nch) {
         const float2 x = ml[mine];
         // (no maximum: nothing seen, sum 0, or NaN alone, sum NaN)
-        al = x.x == -INFINITY ? 0.0f * x.y : ex2_approx(x.x - mx);
-        ls = fmaf(al, x.y, ls);
+        const float down = x.x == -INFINITY ? 0.0f : x.x - mx;
+        al = x.x == -INFINITY ? 0.0f * x.y : ex2_approx(down);
+        ls = add_scaled(ls, x.y, down, al);
       }
       const int n = min(32, nch - i0);
 #pragma unroll 1

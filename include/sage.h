@@ -680,8 +680,10 @@ size_t sage_cache_attn_workspace_bytes(int B, int heads, int H, int Nq, int D, i
  *             shifted cache it is that of the shifted scores.
  * A row that sees no key (an empty sequence; more query rows than tokens)
  * gets 0 and lse = -inf.  A NaN in a row makes that row NaN and no other.  Q is
- * not quantized; probabilities enter the second
- * product as fp16 relative to the row's largest term, sums are fp32.
+ * not quantized; probabilities p enter the second product as fp16 relative to
+ * the row's largest p * 2^v_exp: within 2^-11 each down to 2^-21 of that, less
+ * exact below, and nothing under 2^-31.  Sums are fp32, and the sum of the
+ * probabilities (lse) is within fp32's rounding whatever the pages' v_exp are.
  * Errors: SAGE_ERR_INVALID_ARG / SAGE_ERR_UNSUPPORTED (more than 2^31 - 1
  * blocks or B * heads) before anything is enqueued; SAGE_ERR_CUDA if a launch fails. */
 sage_status sage_cache_attn(const sage_kv_cache *cache, const sage_kv_seqs *seqs,
