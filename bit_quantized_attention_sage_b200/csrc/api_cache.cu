@@ -138,7 +138,7 @@ int sm_count() {
 }
 
 bool attn_shape_ok(const sage_kv_cache* c, const sage_kv_seqs* s, int H, int Nq, int max_len) {
-  if (H < 1 || H % c->heads || Nq < 1 || Nq > (1 << 24)) return false;
+  if (H < 0 || H % c->heads || Nq < 0 || Nq > (1 << 24)) return false;
   if (max_len < 0 || max_len > static_cast<long long>(s->max_pages) * kPage) return false;
   return static_cast<long long>(H / c->heads) * Nq <= (1 << 28);
 }
@@ -149,12 +149,15 @@ bool maps_of(const sage_kv_cache* c, CacheAttnMaps* m) {
          api_tile_map(&m->v, c->v_f8, kPage, tiles, c->D, kPage / 2);
 }
 
+// A query without rows: the weights' sum over none of them is zero.
+bool no_rows(const sage_kv_query* q) { return q->H == 0 || q->Nq == 0; }
+
 sage_status attn_common(const sage_kv_cache* c, const sage_kv_seqs* s, const sage_kv_query* q, int mask,
                         int mask_block, int win, int sink, CacheAttnArgs* a) {
   if (!cache_ok(c) || !seqs_ok(s) || !q) return SAGE_ERR_INVALID_ARG;
   if (!attn_shape_ok(c, s, q->H, q->Nq, q->max_len)) return SAGE_ERR_INVALID_ARG;
   if (q->type != kTypeBf16 && q->type != kTypeF16) return SAGE_ERR_INVALID_ARG;
-  if (!al(q->q, 2) || !strides_ok(q->q_strides) || (q->q_lens && !al(q->q_lens, 4)))
+  if ((!no_rows(q) && !al(q->q, 2)) || !strides_ok(q->q_strides) || (q->q_lens && !al(q->q_lens, 4)))
     return SAGE_ERR_INVALID_ARG;
   if (!std::isfinite(q->scale) || q->scale < 0.0f) return SAGE_ERR_INVALID_ARG;
   const sage_status st = mask_of(mask, mask_block, win, sink, &a->mask);
@@ -311,6 +314,7 @@ SAGE_EXPORT sage_status sage_cache_attn(const sage_kv_cache* cache, const sage_k
                                         int sink, void* out, const long long o_strides[3], float* lse,
                                         void* workspace, size_t workspace_bytes, void* stream) {
   if (!al(out, 2) || !strides_ok(o_strides) || (lse && !al(lse, 4))) return SAGE_ERR_INVALID_ARG;
+  if (!query || no_rows(query)) return SAGE_ERR_INVALID_ARG;
   CacheAttnArgs a{};
   const sage_status st = attn_common(cache, seqs, query, mask, mask_block, win, sink, &a);
   if (st != SAGE_OK) return st;
@@ -338,10 +342,19 @@ SAGE_EXPORT sage_status sage_cache_attn(const sage_kv_cache* cache, const sage_k
 SAGE_EXPORT sage_status sage_cache_weights(const sage_kv_cache* cache, const sage_kv_seqs* seqs,
                                            const sage_kv_query* query, int mask, int mask_block, int win,
                                            int sink, const float* lse, int accumulate, void* stream) {
-  if (!al(lse, 4) || !cache_ok(cache) || !cache->weight) return SAGE_ERR_INVALID_ARG;
+  if (!query || (!no_rows(query) && !al(lse, 4)) || !cache_ok(cache) || !cache->weight)
+    return SAGE_ERR_INVALID_ARG;
   CacheAttnArgs a{};
   const sage_status st = attn_common(cache, seqs, query, mask, mask_block, win, sink, &a);
   if (st != SAGE_OK) return st;
+  if (no_rows(query)) {
+    if (accumulate) return SAGE_OK;
+    // one group of no tokens: the few-row kernel then reads no query row
+    a.G = 1;
+    a.H = cache->heads;
+    a.Nq = 0;
+    a.q_lens = nullptr;
+  }
   a.lse_in = lse;
   a.accumulate = accumulate != 0;
   const int sms = sm_count();

@@ -515,7 +515,7 @@ def cache_weights(q, cache, lse, pages, lengths, mask=None, q_lens=None, max_len
     if tuple(w.shape) != tuple(cache.k_i8.shape[:3]) or w.dtype != torch.float32 or \
             w.device != cache.device or not w.is_contiguous():
         raise ValueError("weight must be a contiguous float32 tensor [pages, heads, %d]" % PAGE)
-    if sq.B == 0 or q.shape[1] == 0 or q.shape[2] == 0:
+    if sq.B == 0:
         return w
     _check(_lib().sage_cache_weights(
         ctypes.byref(cache.struct(w)), ctypes.byref(sq), ctypes.byref(qs), *_mask(mask),

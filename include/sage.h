@@ -695,7 +695,8 @@ sage_status sage_cache_attn(const sage_kv_cache *cache, const sage_kv_seqs *seqs
  *   weight[token] (+)= sum over the query rows of the key head's group of
  *                      exp(scale q.k - lse[row])   (visible pairs only)
  * with sage_cache_attn's lse of the same call.  accumulate = 1 adds to
- * cache->weight, 0 overwrites the weights of all tokens of the sequences.  A
+ * cache->weight, 0 overwrites the weights of all tokens of the sequences.
+ * H or Nq may be 0 here (q and lse are then not read): the sum is 0.  A
  * token's sum does not depend on the order of threads; where sequences share
  * a page their sums are added in no fixed order (accumulate = 1). */
 sage_status sage_cache_weights(const sage_kv_cache *cache, const sage_kv_seqs *seqs,

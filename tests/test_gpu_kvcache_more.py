@@ -1,4 +1,5 @@
-"""More of the paged 8-bit cache: odd page counts in the summed weights."""
+"""More of the paged 8-bit cache: odd page counts and empty queries in the
+summed weights."""
 import numpy as np
 import pytest
 import torch
@@ -31,3 +32,30 @@ def test_weights_of_odd_page_counts(D):
         t = np.arange(x)
         used[torch.from_numpy(tab[b][t // 64]).long(), :, torch.from_numpy(t % 64)] = True
     assert (kv.weight[~used.cuda()] == 7.0).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H,n", [(4, 0), (0, 3), (0, 0)])
+def test_empty_queries_overwrite_the_weights(D, H, n):
+    # the sum over no rows is zero; other slots and an accumulating call stay
+    lengths = [0, 1, 64, 200, 5000]
+    kv, tab, _ = filled(lengths, 2, D, 4, weight=True)
+    kv.weight.copy_(torch.rand(kv.weight.shape) + 1)
+    before = kv.weight.clone()
+    q = torch.zeros((5, H, n, D), dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(q.shape[:3], device="cuda")
+    q_lens = dev([n, 0, n, n, 0])
+    for kw in ({}, {"q_lens": q_lens}):
+        assert sage.cache_weights(q, kv, lse, dev(tab), dev(lengths), "causal", **kw) is kv.weight
+        ok()
+        assert torch.equal(kv.weight, before)
+    for max_len in (None, 1):
+        kv.weight.copy_(before)
+        sage.cache_weights(q, kv, lse, dev(tab), dev(lengths), "causal", q_lens=q_lens,
+                           accumulate=False, max_len=max_len)
+        ok()
+        want = before.clone()
+        for b, x in enumerate(lengths):
+            t = np.arange(x)
+            want[torch.from_numpy(tab[b][t // 64]).long(), :, torch.from_numpy(t % 64)] = 0
+        assert torch.equal(kv.weight, want)

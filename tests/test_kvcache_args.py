@@ -191,3 +191,16 @@ def test_more_heads_than_blocks(L):
     c = cache(n_pages=1, heads=65535)
     assert L.sage_cache_attn(c, seqs(B=65535, max_pages=100), query(H=65535, max_len=6400), 0, 0, 0, 0,
                              P, S3, None, P, 1 << 60, None) == 2
+
+
+def test_rows_are_needed_where_they_are_read(L):
+    # a query without rows is refused by the attention; the weights take it,
+    # without q and lse, and refuse what is wrong with the rest
+    for kw in (dict(H=0), dict(Nq=0), dict(H=0, Nq=0)):
+        assert L.sage_cache_attn(cache(), seqs(), query(**kw), 0, 0, 0, 0, P, S3, None, P, 1 << 40, None) == 1
+    for kw in (dict(H=-2), dict(Nq=-1), dict(Nq=0, type=2), dict(H=0, q_lens=65538), dict(Nq=0, max_len=257),
+               dict(Nq=0, scale=float("nan"))):
+        assert L.sage_cache_weights(cache(), seqs(), query(**kw), 0, 0, 0, 0, P, 0, None) == 1, kw
+    assert L.sage_cache_weights(cache(weight=None), seqs(), query(Nq=0), 0, 0, 0, 0, None, 0, None) == 1
+    assert L.sage_cache_weights(cache(), seqs(), None, 0, 0, 0, 0, P, 0, None) == 1
+    assert L.sage_cache_attn(cache(), seqs(), None, 0, 0, 0, 0, P, S3, None, P, 1 << 40, None) == 1
