@@ -23,6 +23,7 @@ constexpr int kThreads = 256;
 
 constexpr float kRound = 12582912.0f;       // 1.5 * 2^23
 constexpr float kNearTie = 3.0517578e-5f;   // 2^-15: twice the error of x * fp32(1 / s) at 127
+constexpr float kTinyScale = 1e-36f;        // below, neither s nor 1 / s need be a normal number
 constexpr float kNearTieScaled = 1.5258789e-5f;  // 2^-16: twice that of code * fp32(s / s')
 
 // The low bytes of four words as one.
@@ -229,7 +230,7 @@ __device__ __forceinline__ void append_page(const AppendArgs& a, int b, int h, i
     if (KEYS) c.k_scale[unit] = s;
     else c.v_exp[unit] = static_cast<int8_t>(ve);
   }
-  const bool tiny = !(s >= 1e-36f);
+  const bool tiny = !(s >= kTinyScale);
   const float inv = tiny ? 0.0f : __frcp_rn(s), pv = pow2i(-ve);
 #pragma unroll
   for (int i = 0; i < PER; i++) {
@@ -633,7 +634,9 @@ __device__ __forceinline__ void requantize(const EvictArgs& a, int h, int po, si
       if (s_src[i] != top) {
         // round-half-even(code * ratio) in the low byte of the sum with 1.5 *
         // 2^23 (one rounding); next to a tie of any of the 16 fp64 decides.
-        // |code| * s_src <= 127 top for every survivor, so nothing clamps.
+        // |code| * s_src <= 127 top for every survivor, so nothing clamps;
+        // a scale near the subnormal numbers is rounded by more than that
+        // allows for, and the slow way does clamp.
         const float s = s_src[i], ratio = top > 0.0f ? s / top : 0.0f;
         float worst = 0.0f;
 #pragma unroll
@@ -652,7 +655,7 @@ __device__ __forceinline__ void requantize(const EvictArgs& a, int h, int po, si
           worst = fmax3(worst, fmax3(rem[0], rem[1], rem[2]), rem[3]);
           q[j] = low_bytes(y[0], y[1], y[2], y[3]);
         }
-        if (worst > 0.5f - kNearTieScaled) {
+        if (worst > 0.5f - kNearTieScaled || !(top >= kTinyScale)) {
           q[0] = rescale_keys(x[i].x, s, top);
           q[1] = rescale_keys(x[i].y, s, top);
           q[2] = rescale_keys(x[i].z, s, top);

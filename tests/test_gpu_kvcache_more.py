@@ -1,5 +1,5 @@
 """More of the paged 8-bit cache: odd page counts and empty queries in the
-summed weights."""
+summed weights, prunes of subnormal keys."""
 import numpy as np
 import pytest
 import torch
@@ -59,3 +59,30 @@ def test_empty_queries_overwrite_the_weights(D, H, n):
             t = np.arange(x)
             want[torch.from_numpy(tab[b][t // 64]).long(), :, torch.from_numpy(t % 64)] = 0
         assert torch.equal(kv.weight, want)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prune_of_subnormal_keys(D):
+    # scales of a few last places: the new scale is rounded by more than the
+    # codes' range allows for, and codes past it are held at +-127
+    n, keep = 512, 128
+    kv, tab, _ = filled([n], 2, D, 5, weight=True)
+    pg = torch.from_numpy(tab[0]).long()
+    g = torch.Generator().manual_seed(1)
+    top = torch.randint(1, 8, kv.weight.shape, generator=g)
+    code = torch.randint(-127, 128, kv.k_i8.shape, generator=g)
+    kv.k_i8.copy_((code.sign() * (code.abs() % (top[..., None] + 1))).to(torch.int8))
+    # multiples of the least fp32 number, 2^-149: 7 of 55 .. 61 of them / 127
+    # round to 3, and 7 * 55 / 3 is past 127
+    steps = torch.randint(55, 62, kv.k_scale.shape, generator=g).to(torch.int32)
+    kv.k_scale.copy_(steps.view(torch.float32))
+    kv.weight[pg] = torch.rand((len(pg), 2, 64), generator=g).cuda()
+    c = ref.Cache(kv)
+    sage.cache_evict(kv, dev(tab), dev([n]), keep)
+    ok()
+    got, p = ref.Cache(kv), tab[0][:2].astype(np.int64)
+    for h in range(2):
+        _, K, S, _, _, _ = c.evict(tab[0], n, keep, 0, 0, h)
+        assert np.array_equal(got.s[p, h], S)
+        assert (np.abs(K) == 127).any()
+        assert np.array_equal(got.k[p, h], K)
