@@ -26,13 +26,30 @@ _MASKS = "mask must be None, 'causal', ('block_causal', n) or " \
 
 torch = None  # the module, once a call has brought a tensor (the package imports without it)
 _TYPES = {}   # torch dtype -> type code
+_Turn = None  # rope as an autograd function
 
 
 def _load():
-    global torch
+    global torch, _Turn
     import torch as t
     torch = t
     _TYPES.update({t.bfloat16: 0, t.float16: 1, t.float32: 2})
+
+    class Turn(t.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, positions, inv_freq, layout, amplitude, inverse):
+            ctx.save_for_backward(positions, inv_freq)
+            ctx.how = layout, amplitude, inverse
+            return rope(x, positions, inv_freq, layout, amplitude, inverse)
+
+        @staticmethod
+        def backward(ctx, dy):
+            layout, amplitude, inverse = ctx.how
+            if dy.stride(-1) != 1:
+                dy = dy.contiguous()
+            return (rope(dy, *ctx.saved_tensors, layout, amplitude, not inverse),) + (None,) * 5
+
+    _Turn = Turn
 
 
 def _type(t):
@@ -230,8 +247,10 @@ def rope(x, positions, inv_freq, layout="interleaved", amplitude=1.0, inverse=Fa
     stride, any others).  positions: int32/int64 [N] or [B, N]; inv_freq: fp64
     [R / 2] (rope_freqs), R <= D channels are turned.  layout: "interleaved"
     pairs (2p, 2p + 1), "half" pairs (p, p + R/2).  inverse: turn back -- the
-    gradient of the forward call with respect to x, from that of its result.
-    out: None, a tensor like x, or x itself."""
+    gradient of the forward call with respect to x, from that of its result;
+    autograd takes it so where x requires a gradient (positions and inv_freq
+    have none, and out cannot be given).  out: None, a tensor like x, or x
+    itself."""
     kind = _type(x)
     if x.dim() != 4 or kind < 0:
         raise ValueError("x must be a bf16, fp16 or fp32 tensor [B, H, N, D]")
@@ -241,6 +260,12 @@ def rope(x, positions, inv_freq, layout="interleaved", amplitude=1.0, inverse=Fa
     if st is None:
         with _There(x, stream):
             return rope(x, positions, inv_freq, layout, amplitude, inverse, out)
+    if (x.requires_grad or inv_freq.requires_grad) and torch.is_grad_enabled():
+        if inv_freq.requires_grad:
+            raise ValueError("inv_freq has no gradient: detach it")
+        if out is not None:
+            raise ValueError("out cannot be given where x requires a gradient")
+        return _Turn.apply(x, positions, inv_freq, layout, amplitude, inverse)
     B, H, N, D = x.shape
     dev = x.get_device()
     pos, p64, pstride = _positions(positions, N, B, dev)
