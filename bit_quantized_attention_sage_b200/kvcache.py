@@ -175,6 +175,49 @@ def _out_strides(t):
     return _strides(t)
 
 
+def _meets(x, xs, y, ys, budget=2000):
+    """Whether the output y, of x's shape, has memory in common with x in another
+    way than being x: elements at the same places with the same strides (xs and
+    ys, of _strides).  Such an output would overwrite inputs that other blocks
+    have yet to read.  (True also where a search of `budget` steps does not
+    tell.)"""
+    es = x.element_size()
+    B, H, N, D = x.shape
+    away = y.data_ptr() - x.data_ptr()
+    first = xs if away >= 0 else ys
+    if abs(away) >= ((B - 1) * first[0] + (H - 1) * first[1] + (N - 1) * first[2] + D) * es or \
+            away == 0 and xs[:] == ys[:]:
+        return False
+    # bytes from a run of D channels of x to one of y: away + the sum of
+    # step * [lo .. hi] over the strides; the runs meet where that is within
+    # D * es.  The largest stride first leaves a choice or two of each.
+    reach = {}
+    for strides, of_x in ((xs, True), (ys, False)):
+        for s, n in zip(strides, x.shape):
+            lo, hi = reach.get(s * es, (0, 0))
+            reach[s * es] = (lo - n + 1, hi) if of_x else (lo, hi + n - 1)
+    steps = sorted(((s, lo, hi) for s, (lo, hi) in reach.items() if s), reverse=True)
+    rest = [(0, 0)]
+    for s, lo, hi in reversed(steps):
+        rest.insert(0, (rest[0][0] + s * lo, rest[0][1] + s * hi))
+
+    def search(i, at):  # some sum of the steps from i on brings `at` within the run
+        nonlocal budget
+        budget -= 1
+        low, high = at + rest[i][0], at + rest[i][1]
+        if budget < 0 or low >= D * es or high <= -D * es:
+            return budget < 0
+        if i == len(steps):
+            return True
+        s, lo, hi = steps[i]
+        a, b = rest[i + 1]
+        k0 = max(lo, -((at + b + D * es - 1) // s))
+        k1 = min(hi, (D * es - 1 - at - a) // s)
+        return any(search(i + 1, at + s * k) for k in range(k0, k1 + 1))
+
+    return search(0, away)
+
+
 def _int32(t, shape, what, dev):
     if t.dtype is not torch.int32 or t.get_device() != dev or t.shape != shape or \
             not t.is_contiguous():
@@ -250,7 +293,8 @@ def rope(x, positions, inv_freq, layout="interleaved", amplitude=1.0, inverse=Fa
     gradient of the forward call with respect to x, from that of its result;
     autograd takes it so where x requires a gradient (positions and inv_freq
     have none, and out cannot be given).  out: None, a tensor like x, or x
-    itself."""
+    itself; one that shares memory with x in another way is written by a copy
+    of the result."""
     kind = _type(x)
     if x.dim() != 4 or kind < 0:
         raise ValueError("x must be a bf16, fp16 or fp32 tensor [B, H, N, D]")
@@ -279,6 +323,8 @@ def rope(x, positions, inv_freq, layout="interleaved", amplitude=1.0, inverse=Fa
         raise ValueError("out must have x's shape, type and device")
     else:
         ys = _out_strides(out)
+        if _meets(x, xs, out, ys):
+            return out.copy_(rope(x, positions, inv_freq, layout, amplitude, inverse))
     if B and H and N and D:
         _check(_lib().sage_rope(x.data_ptr(), out.data_ptr(), kind, B, H, N, D, R, xs, ys, pos, p64,
                                 pstride, freq, amplitude, layout == "half", bool(inverse), st),
@@ -479,7 +525,9 @@ def cache_attn(q, cache, pages, lengths, mask=None, q_lens=None, max_len=None, s
     window_frames, sink_tokens).  q_lens: int32 [B], query rows of each
     sequence (None: Nq); other rows of out are left as they are.  max_len: a
     bound on the lengths known to the host (None: what the page table holds);
-    it only chooses how the work is cut.  scale: None is 1 / sqrt(D)."""
+    it only chooses how the work is cut.  scale: None is 1 / sqrt(D).  out:
+    None, a tensor like q, or q itself; one that shares memory with q in
+    another way is written by a copy of the result."""
     st = _here(cache.k_i8, stream)
     if st is None:
         with _There(cache.k_i8, stream):
@@ -494,6 +542,11 @@ def cache_attn(q, cache, pages, lengths, mask=None, q_lens=None, max_len=None, s
         raise ValueError("out must have q's shape, type and device")
     else:
         os = _out_strides(out)
+        if _meets(q, qs.q_strides, out, os):
+            r = cache_attn(q, cache, pages, lengths, mask, q_lens, max_len, scale, torch.clone(out),
+                           lse, return_lse, workspace)
+            out.copy_(r[0] if return_lse else r)
+            return (out, r[1]) if return_lse else out
     if lse is None:
         if return_lse:
             lse = cache.k_scale.new_empty(q.shape[:3])

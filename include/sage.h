@@ -554,7 +554,8 @@ int sage_abi_version(void);
  * result rounded once.
  *   x, y             device, type 0 bf16, 1 fp16, 2 fp32: [B, H, N, D] with
  *                    unit channel stride and the given strides (elements) of
- *                    B, H and N; y may be x itself (same strides)
+ *                    B, H and N; y may be x itself (same strides) and must
+ *                    not share memory with it in another way
  *   positions        device int64 (positions_64 = 1) or int32: N of them,
  *                    batch entry b's at b * positions_stride (0: shared)
  *   inv_freq         device f64 [R / 2], 8-byte aligned
@@ -675,7 +676,9 @@ size_t sage_cache_attn_workspace_bytes(int B, int heads, int H, int Nq, int D, i
  *             reference context of `sink` tokens -- the masks of
  *             sage_attn_fwd and sage_attn_fwd_window.  mask_block = 1 makes 3
  *             a window of `win` tokens with `sink` leading ones.
- *   out       device, the query's type, [B, H, Nq, D] with its own strides
+ *   out       device, the query's type, [B, H, Nq, D] with its own strides;
+ *             it may be the query itself (same strides), and must not share
+ *             memory with it in another way
  *   lse       f32 [B, H, Nq] contiguous, natural log, or NULL.  With a
  *             shifted cache it is that of the shifted scores.
  * A row that sees no key (an empty sequence; more query rows than tokens)

@@ -1,5 +1,5 @@
 """More of the paged 8-bit cache: odd page counts and empty queries in the
-summed weights, prunes of subnormal keys."""
+summed weights, prunes of subnormal keys, outputs over their inputs."""
 import numpy as np
 import pytest
 import torch
@@ -86,3 +86,35 @@ def test_prune_of_subnormal_keys(D):
         assert np.array_equal(got.s[p, h], S)
         assert (np.abs(K) == 127).any()
         assert np.array_equal(got.k[p, h], K)
+
+
+@pytest.mark.parametrize("case", ["itself", "token_on", "token_back", "other_head_order", "fused"])
+@pytest.mark.parametrize("n", [1, 2, 300])
+def test_outputs_over_their_inputs(case, n):
+    # every form gives what an output of its own does, and leaves the rest of
+    # the buffer alone
+    B, H, D, lengths = 2, 4, 64, [3000, 70]
+    kv, tab, _ = filled(lengths, 2, D, n)
+    f, _ = sage.rope_freqs(D)
+    pos = torch.arange(n, device="cuda") * 100
+    t, ln = dev(tab), dev(lengths)
+    for call in (lambda x, out=None: sage.rope(x, pos, f, layout="half", out=out),
+                 lambda x, out=None: sage.cache_attn(x, kv, t, ln, "causal", out=out),
+                 lambda x, out=None: sage.cache_attn(x, kv, t, ln, "causal", out=out, return_lse=True)[0]):
+        base = randn((B, n + 1, 3, H, D), n)
+        q = base[:, :n, 0].transpose(1, 2)
+        out = {"itself": q, "token_on": base[:, 1:, 0].transpose(1, 2),
+               "token_back": q, "other_head_order": base[:, :n, :2].reshape(B, n, 2 * H, D),
+               "fused": base[:, :n, 1].transpose(1, 2)}[case]
+        if case == "token_back":
+            q = base[:, 1:, 0].transpose(1, 2)
+        if case == "other_head_order":  # rows of q as heads of the result
+            flat = base.view(-1)
+            q = torch.as_strided(flat, (B, H, n, D), (3 * H * D * (n + 1), D, 3 * H * D, 1))
+            out = torch.as_strided(flat, (B, H, n, D), (3 * H * D * (n + 1), D * n, D, 1))
+        want, rest = call(q), base.clone()
+        rest_out = torch.as_strided(rest, out.shape, out.stride(), out.storage_offset())
+        rest_out.copy_(want)
+        assert call(q, out) is out
+        ok()
+        assert torch.equal(out, want) and torch.equal(base, rest)

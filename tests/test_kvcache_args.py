@@ -204,3 +204,42 @@ def test_rows_are_needed_where_they_are_read(L):
     assert L.sage_cache_weights(cache(weight=None), seqs(), query(Nq=0), 0, 0, 0, 0, None, 0, None) == 1
     assert L.sage_cache_weights(cache(), seqs(), None, 0, 0, 0, 0, P, 0, None) == 1
     assert L.sage_cache_attn(cache(), seqs(), None, 0, 0, 0, 0, P, S3, None, P, 1 << 40, None) == 1
+
+
+def test_outputs_over_their_inputs():
+    # against the elements themselves, of strided views of one buffer
+    import random
+    rng = random.Random(1)
+    for dt in (torch.float32, torch.bfloat16):
+        base = torch.zeros(2000, dtype=dt)
+        index = torch.arange(2000)
+        seen = [0, 0]
+        for _ in range(3000):
+            shape = [rng.randint(1, 3) for _ in range(4)]
+
+            def view():
+                step, at = [0, 0, 0], shape[3] + rng.randint(0, 2)
+                for i in rng.sample(range(3), 3):
+                    step[i], at = at, at * shape[i] + rng.randint(0, 1)
+                if rng.random() < 0.5:
+                    step = [rng.randint(0, 40) for _ in range(3)]
+                return (*step, 1), rng.randint(0, 60)
+
+            sx, ox = view()
+            sy, oy = view()
+            if rng.random() < 0.5:
+                sy = sx
+            x, y = (torch.as_strided(base, shape, s, o) for s, o in ((sx, ox), (sy, oy)))
+            ix, iy = (torch.as_strided(index, shape, s, o) for s, o in ((sx, ox), (sy, oy)))
+            want = not torch.equal(ix, iy) and bool(set(ix.flatten().tolist()) & set(iy.flatten().tolist()))
+            assert kvcache._meets(x, kvcache._strides(x), y, kvcache._strides(y)) == want
+            seen[want] += 1
+        assert min(seen) > 500
+    # heads of one fused projection are apart, far buffers too
+    qkv = torch.zeros((2, 2040, 3, 24, 128), dtype=torch.bfloat16)
+    q, k, v = (qkv[:, :, i].transpose(1, 2) for i in range(3))
+    far = torch.zeros((2, 24, 2040, 128), dtype=torch.bfloat16)
+    for y, want in ((k, False), (v, False), (far, False), (q, False), (q[:, :, 1:], True)):
+        x = q[:, :, :y.shape[2]]
+        assert kvcache._meets(x, kvcache._strides(x), y, kvcache._strides(y)) == want
+        assert kvcache._meets(y, kvcache._strides(y), x, kvcache._strides(x)) == want
