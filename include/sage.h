@@ -633,7 +633,7 @@ typedef struct {
  * rescaled and rounded to nearest even.  Every rounding is exact (one
  * round-half-even of the real quotient).  Slots behind the new tokens of a
  * fresh page become zero, and the new tokens' weights too.  Appending the same
- * tokens at the same lengths again changes nothing.  Tokens past the page
+ * tokens at the same lengths again changes nothing else.  Tokens past the page
  * table are recorded as above and dropped.  Inputs must be finite. */
 sage_status sage_cache_append(const sage_kv_cache *cache, const sage_kv_seqs *seqs,
                               const void *k, const void *v, int type, int n,
@@ -642,7 +642,8 @@ sage_status sage_cache_append(const sage_kv_cache *cache, const sage_kv_seqs *se
 
 /* Values of n tokens of each sequence from token starts[b] on (NULL: 0), as
  * the codes stand for them: k (+ k_shift, if given) and v f32 [B, heads, n, D],
- * weight f32 [B, heads, n] or NULL.  Zero where there is no token. */
+ * weight f32 [B, heads, n] or NULL.  Zero where there is no token.  k, v and
+ * k_shift are 16-byte aligned. */
 sage_status sage_cache_read(const sage_kv_cache *cache, const sage_kv_seqs *seqs, int n,
                             const int32_t *starts, const float *k_shift, float *k, float *v,
                             float *weight, void *stream);
@@ -663,8 +664,9 @@ typedef struct {
     float scale;
 } sage_kv_query;
 
-/* Workspace of sage_cache_attn on the current device, bytes (0: invalid),
- * 16-byte aligned.  It holds partial results: calls that may run at the same
+/* Workspace of sage_cache_attn with these arguments on the current device,
+ * bytes (0: invalid), 16-byte aligned.  (Not monotonic: a shorter max_len can
+ * take more.)  It holds partial results: calls that may run at the same
  * time, captured ones among them, need one each. */
 size_t sage_cache_attn_workspace_bytes(int B, int heads, int H, int Nq, int D, int max_len,
                                        int mask, int mask_block, int win, int sink);
@@ -718,8 +720,11 @@ size_t sage_cache_evict_workspace_bytes(int B, int heads, int D, int keep, int i
  * head its own; their codes are requantized to the new page's scales:
  *   k_scale = max over its tokens of fp32(scale * fp32(max |code| / 127)),
  *   v_exp   = the smallest e >= -40 that covers its values,
- * each code rounded to nearest even once (a page whose tokens all stay keeps
- * its codes and scales).  Their weights move along.
+ * each code rounded to nearest even once.  Their weights move along.  (Tokens
+ * that an append put on a fresh page and that stay a page keep their values
+ * exactly: the keys' codes and scale are the same, the values' codes the same or
+ * doubled.  Where a page's key scale is larger than its tokens need, larger ones
+ * having been taken back by shorter lengths, its keys are rounded anew.)
  *   pages_out   device int32 [B, out_pages], out_pages >= ceil(keep / 64):
  *               where they go; these pages must not be among the pages read
  *               or appear twice.  NULL: the sequence's own first pages;

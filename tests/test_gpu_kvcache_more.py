@@ -1,5 +1,6 @@
 """More of the paged 8-bit cache: odd page counts and empty queries in the
-summed weights, prunes of subnormal keys, outputs over their inputs."""
+summed weights, prunes of subnormal keys and of shortened sequences, outputs
+over their inputs."""
 import numpy as np
 import pytest
 import torch
@@ -118,3 +119,40 @@ def test_outputs_over_their_inputs(case, n):
         assert call(q, out) is out
         ok()
         assert torch.equal(out, want) and torch.equal(base, rest)
+
+
+@pytest.mark.parametrize("place", ["in", "out"])
+def test_prune_of_a_shortened_sequence(place):
+    # a page whose scales are larger than its tokens need (larger ones were
+    # taken back) gets those its tokens need; a page with scales of its own
+    # tokens keeps its values
+    D, B = 64, 1
+    kv = sage.KVCache8(10, 2, D, track_weight=True)
+    tab = np.array([[4, 1, 7, 2]], np.int32)
+    large, small = randn((B, 2, 70, D), 1) * 100, randn((B, 2, 246, D), 2)
+    sage.cache_append(kv, large, large, dev(tab), dev([0]))
+    sage.cache_append(kv, small, small, dev(tab), dev([10]))  # shortened to 10 tokens
+    sage.cache_append(kv, small, small, dev(tab), dev([3]))   # to 3
+    lengths, keep = [249], 192
+    kv.weight.zero_()
+    for i in range(3):
+        kv.weight[int(tab[0, i])] = 1.0
+    c = ref.Cache(kv)
+    assert c.k[4, 0, 3:].max() < 127  # the large tokens' scale
+    po = None if place == "in" else np.array([[9, 8, 6]], np.int32)
+    kept, _ = sage.cache_evict(kv, dev(tab), dev(lengths), keep, pages_out=None if po is None else dev(po))
+    ok()
+    got = ref.Cache(kv)
+    pg = (tab if po is None else po)[0][:3].astype(np.int64)
+    for h in range(2):
+        assert kept[0, h].tolist() == list(range(192))
+        _, K, S, V, E, _ = c.evict(tab[0], lengths[0], keep, 0, 0, h)
+        assert np.array_equal(got.k[pg, h], K) and np.array_equal(got.s[pg, h], S)
+        assert np.array_equal(got.v[pg, h], V) and np.array_equal(got.e[pg, h], E)
+    # whole pages of their own scales: the key of absmax has code 127, so the new
+    # scale is s fp32(127 / 127); a largest value just above 448 2^e was rounded
+    # down to 448 2^e, whose least exponent is e, so value codes may double
+    own = tab[0][1:3].astype(np.int64)
+    assert np.array_equal(got.k[pg[1:]], c.k[own]) and np.array_equal(got.s[pg[1:]], c.s[own])
+    val = [x.v * np.exp2(x.e.astype(np.float64))[..., None, None] for x in (got, c)]
+    assert np.array_equal(val[0][pg[1:]], val[1][own])
