@@ -224,6 +224,8 @@ SAGE_EXPORT sage_status sage_rope(const void* x, void* y, int type, int B, int H
   a.amplitude = amplitude;
   a.half = half != 0;
   a.inverse = inverse != 0;
+  a.sms = sm_count();
+  if (!a.sms) return SAGE_ERR_CUDA;
   return status_of(launch_rope(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -157,6 +157,7 @@ struct RopeArgs {
   const double* inv_freq;            // [R / 2]
   float amplitude;
   int half, inverse;
+  int sms;                           // of the device
 };
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
 cudaError_t launch_rope_tables(const RopeArgs& a, float* cosv, float* sinv, cudaStream_t s);

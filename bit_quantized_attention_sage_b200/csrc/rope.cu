@@ -211,12 +211,16 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_tables(const RopeArgs a, 
 template <typename T>
 cudaError_t launch_type(const RopeArgs& a, bool vec, cudaStream_t s) {
   // tokens per block: as many as the cos/sin buffer holds, 16 at most; the
-  // heads are cut into groups only while the blocks would not fill the GPU
-  // twice over (every group computes its angles again)
+  // heads are cut into groups only until there is a block for every SM (every
+  // group computes its angles again).  Cut until there are one, two, four
+  // blocks an SM, us, R = D = 128: one token of 64 x 32 heads 8.2 : 8.2 : 10.2,
+  // 4 x 100 tokens of 24 heads 8.2 : 10.2 : 12.3, 2040 tokens of 24 heads 12.3 :
+  // 14.3 : 18.4, 9000 of 12 heads 20.5 : 20.5 : 24.6; fewer blocks were slower on
+  // none of 13 shapes.
   const int tile = min(max(1, kRopePairs / max(1, a.R / 2)), min(a.N, 16));
   const int nb = (a.N + tile - 1) / tile;
   int groups = 1;
-  while (groups < a.H && static_cast<long long>(nb) * a.B * groups < 592) groups *= 2;
+  while (groups < a.H && static_cast<long long>(nb) * a.B * groups < a.sms) groups *= 2;
   const int heads = (a.H + groups - 1) / groups;
   const dim3 grid(nb, (a.H + heads - 1) / heads, a.B);
   if (a.half) {
