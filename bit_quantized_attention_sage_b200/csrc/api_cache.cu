@@ -82,6 +82,13 @@ int visited_pages(const CacheMask& m, int max_len, int tile_tokens) {
 //   8 heads     1000 tokens 18 : 20   2000 23 : 20   4000  33 :  26
 //   128 heads   1000 tokens 21 : 28   4000 41 : 48
 //   512 heads   1000 tokens 46 : 50   4000 106 : 118 (of uneven lengths 83 : 89)
+// The bounds, whole against shared from a cold L2 (in brackets a warm one):
+//   24 pages, 8 heads      18 : 18 (18 : 17), 28 pages 21 : 23 (21 : 22), 32
+//                          pages 23 : 18 (23 : 17)
+//   64 pages, heads of the last round (of 296), one round:
+//     72   37 : 39 (35 : 31)    96   39 : 43 (37 : 34)   104   39 : 45 (36 : 36)
+//   two rounds:
+//     72  100 : 96 (90 : 82)    96  102 : 102 (90 : 85)  104  102 : 104 (90 : 87)
 // and past 64 pages one long sequence among short ones would cost more than
 // there is to gain.  (The weights have no join to save: 128 heads of 8000
 // tokens 39 us whole, 34 shared; equal at 1000.)

@@ -12,8 +12,9 @@
 // those three int8 limbs, so Q K^T is three int8 products on the key codes as
 // they lie in the cache: exact int32, no conversion of the codes (five
 // instructions per four of them to fp16, half of the loop's issue slots).
-// The limbs join in fp32, rounded once; the page's key scale, the row's power
-// and log2(e) * softmax scale multiply the sum.
+// The limbs join in fp32, rounded twice (the lower two's sum, then the whole; by
+// 2^-24 of sum |q k| each at most); the page's key scale, the row's power and
+// log2(e) * softmax scale multiply the sum.
 // Probabilities.  y = 2^(t + e - M + 7), t the score in log2 units, e the
 // page's value exponent, M a reference maximum of t + e that follows the
 // running one in steps of at least 2^8: y <= 2^15, and fp16(y) is off by at

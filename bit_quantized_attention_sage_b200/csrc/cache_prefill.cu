@@ -628,8 +628,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_prefill(const CacheAttnAr
 // tile (what they share, the tile's pages and ranges, is worked out once), a
 // warp a row at a time.  A lane holds the factor of one range; the partial
 // rows come four at a time, on their way before the factors are known.
-// Measured: 24 heads x 2040 rows of three ranges 27 us, 76 MB, most of it under
-// the attention's tail (a warp a row that worked out everything for itself 45).
+// Measured: 24 heads x 2040 rows of three ranges 27 us, 76 MB, behind the
+// attention and not under it (a warp a row that worked out everything for
+// itself 45).
 constexpr int kMergeRows = 16;
 template <int D>
 __global__ void __launch_bounds__(128) k_cache_merge(const CacheAttnArgs a, int row_tiles) {
@@ -648,9 +649,10 @@ __global__ void __launch_bounds__(128) k_cache_merge(const CacheAttnArgs a, int 
     const PageRuns runs = page_runs(a.mask, off + r0 / a.G, off + (r1 - 1) / a.G, len);
     nch = min(a.chunks, (runs.n + a.chunk_pages - 1) / a.chunk_pages);
   }
-  // Launched under the attention kernel's tail.  Every block waits, also one
-  // with nothing to join: what comes next in the stream waits for this kernel
-  // only, so it must not end before the attention has.
+  // The attention kernel gives no signal of its own, so this kernel's blocks
+  // come as its last blocks leave.  Every block waits, also one with nothing to
+  // join: what comes next in the stream waits for this kernel only, so it must
+  // not end before the attention has.
   cudaGridDependencySynchronize();
   if (nch <= 1) return;  // the attention kernel wrote this tile itself
   auto load = [&](const float* p, float (&v)[PER]) {
@@ -734,8 +736,8 @@ cudaError_t launch_cache_prefill(const CacheAttnArgs& a, cudaStream_t s) {
   else k_cache_prefill<64><<<grid, kThreads, sizeof(PreSmem<64>), s>>>(a, row_tiles);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.chunks == 1) return e;
-  // the merge starts while the last attention blocks still run and waits for
-  // them on the device (programmatic dependent launch)
+  // programmatic dependent launch: the merge's launch is under the attention,
+  // its blocks come when every attention block has ended
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;

@@ -23,7 +23,8 @@
 // query heads each: 350 TFLOP/s, 1.4 TB/s.  A tile takes some 1650 clocks; exp2
 // (16 a clock and SM) is 1024 of them, and the sums' broadcasts, the codes'
 // conversion and the products' operands share the rest of the shared memory's
-// time.  A block's start and the first rows take 9 us.  Every warp doing copies,
+// time.  A block's start and the first rows take 9 us.  704 threads leave 80
+// registers each, of which the roles spill 114 bytes (96 at D = 64).  Every warp doing copies,
 // products and sums in turn (two blocks an SM): 58 us, the blocks fell into
 // phase and exp2 idled half the time.  Groups of summing warps: two 47 us,
 // three 41, four 41; one group that converts: 47; products of 64 rows into
