@@ -7,7 +7,7 @@ import torch
 
 import bit_quantized_attention_sage_b200 as sage
 import cache_ref as ref
-from test_gpu_kvcache import dev, filled, ok
+from test_gpu_kvcache import check_attn, dev, filled, ok
 from test_gpu_kvcache_edges import check_weights, randn
 
 pytestmark = pytest.mark.gpu
@@ -156,3 +156,18 @@ def test_prune_of_a_shortened_sequence(place):
     assert np.array_equal(got.k[pg[1:]], c.k[own]) and np.array_equal(got.s[pg[1:]], c.s[own])
     val = [x.v * np.exp2(x.e.astype(np.float64))[..., None, None] for x in (got, c)]
     assert np.array_equal(val[0][pg[1:]], val[1][own])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,n", [(1, 1), (8, 1), (8, 2), (5, 4), (9, 2)])
+def test_one_long_head(D, G, n):
+    # a hundred shares and more of one head, more than 32 ranges of keys
+    lengths = [70001]
+    kv, tab, _ = filled(lengths, 1, D, G, weight=True)
+    c = ref.Cache(kv)
+    q = randn((1, G, n, D), n)
+    o, lse = sage.cache_attn(q, kv, dev(tab), dev(lengths), "causal", return_lse=True)
+    sage.cache_weights(q, kv, lse, dev(tab), dev(lengths), "causal", accumulate=False)
+    ok()
+    check_attn(c, q, o, lse, tab, lengths, [n], "causal", D ** -0.5)
+    check_weights(c, q, lse, tab, lengths, [n], "causal", kv.weight)

@@ -98,3 +98,24 @@ def test_refusals_where_a_gradient_is_recorded():
     p.add_(1)  # the backward pass would turn by other angles
     with pytest.raises(RuntimeError):
         y.sum().backward()
+
+
+def test_captured_forward_and_backward():
+    # (no eager graph of x may live meanwhile: torch keeps the leaf's node on
+    # that graph's stream, for every operator)
+    f, _ = sage.rope_freqs(64)
+    pos = torch.arange(70, device="cuda")
+    x, dy = rand((2, 4, 70, 64), 12, "bf16").requires_grad_(), rand((2, 4, 70, 64), 13, "bf16")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = sage.rope(x, pos, f, layout="half")
+        (dx,) = torch.autograd.grad(y, x, dy)
+    for seed in (14, 15):
+        with torch.no_grad():
+            x.copy_(rand(x.shape, seed, "bf16"))
+            dy.copy_(rand(x.shape, seed + 9, "bf16"))
+        pos.add_(1000)
+        g.replay()
+        with torch.no_grad():
+            assert torch.equal(y, sage.rope(x, pos, f, layout="half"))
+            assert torch.equal(dx, sage.rope(dy, pos, f, layout="half", inverse=True))
