@@ -12,7 +12,7 @@ A streaming or serving loop keeps one ``KVCache8`` and, per step:
 
 Every call takes the tensors' device (not the current one) and, without
 ``stream``, that device's current stream; what it allocates belongs to that
-stream.
+stream.  Autograd sees rope alone: the cache's calls record no gradient.
 """
 import ctypes
 import functools
